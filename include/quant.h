@@ -15,9 +15,9 @@
  *
  * Memory, streams and errors are gemm.h's: all pointers are device pointers
  * owned by the caller, no pointer is kept after a call, nothing is allocated,
- * `stream` is a cudaStream_t (NULL = the legacy default stream), and every
- * entry point enqueues its work, returns without synchronising and gives a
- * gemm_status_t.  Argument checks are made on the host before
+ * `stream` is a cudaStream_t (NULL = the legacy default stream), every entry
+ * point but gemm_fp8_checked enqueues its work and returns without
+ * synchronising, and every entry point gives a gemm_status_t.  Argument checks are made on the host before
  * anything is enqueued.  Leading dimensions are in elements (bytes for the
  * packed 4-bit weights) and may exceed the row length; a single row's leading
  * dimension is not looked at.  Outputs must not overlap inputs or each other
@@ -95,6 +95,16 @@ int quantize_fp8(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dty
 int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
              int64_t ldb, void* C, int64_t ldc, const float* a_scale, const float* b_scale,
              int dtype, void* stream);
+
+/*
+ * gemm_fp8_checked -- gemm_fp8, then synchronise `stream` and read (and clear)
+ * the kernels' device status word: GEMM_ERR_TIMEOUT if a pipeline wait ran out
+ * (C is then undefined; gemm_debug_set's hooks apply), GEMM_ERR_CUDA if the
+ * stream reported an error.  Meant for tests and debugging.
+ */
+int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                     int64_t ldb, void* C, int64_t ldc, const float* a_scale, const float* b_scale,
+                     int dtype, void* stream);
 
 /*
  * gemv_w4 -- C[i,j] = sum_k x[i,k] * scales[j,k/group] * (w[j,k] - zeros[j,k/group])

@@ -244,6 +244,10 @@ int staging_get(int dev, int which, size_t bytes, void** out) {
 
 }  // namespace
 
+namespace ssp {
+DebugHooks debug_hooks() { return {g_wait_limit_ns, g_withhold_arrive}; }
+}  // namespace ssp
+
 extern "C" {
 
 int gemm(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,

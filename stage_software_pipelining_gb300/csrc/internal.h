@@ -55,6 +55,13 @@ struct SimtLaunch {
     int split_parts;
 };
 
+// gemm_debug_set's values, for the tensor-core kernels of other files.
+struct DebugHooks {
+    int64_t wait_limit_ns;
+    int withhold_arrive;
+};
+DebugHooks debug_hooks();
+
 // Enqueue the tensor-core GEMM (K > 0, M > 0, N > 0, alpha != 0).  Returns a
 // gemm_status_t.
 int tc_launch(const TcLaunch& L, cudaStream_t stream);

@@ -43,6 +43,9 @@ struct Fp8Launch {
     int out_bf16;  // 0 fp16, 1 bf16
 };
 int fp8_launch(const Fp8Launch& L, cudaStream_t stream);
+struct GemmDeviceStatus;
+// The fp8 kernels' device status word, read and reset (synchronous).
+int fp8_read_and_clear_status(GemmDeviceStatus* out);
 
 // 4-bit weights (gemv_w4.cu); M, N, K > 0.
 struct W4Launch {

@@ -92,6 +92,18 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
     return ssp::fp8_launch({M, N, K, A, lda, B, ldb, C, ldc, a_scale, b_scale, dtype == QUANT_BF16}, s);
 }
 
+int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                     int64_t ldb, void* C, int64_t ldc, const float* a_scale, const float* b_scale,
+                     int dtype, void* stream) {
+    int st = gemm_fp8(M, N, K, A, lda, B, ldb, C, ldc, a_scale, b_scale, dtype, stream);
+    if (st != GEMM_OK) return st;
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
+    ssp::GemmDeviceStatus ds;
+    st = ssp::fp8_read_and_clear_status(&ds);
+    if (st != GEMM_OK) return st;
+    return ds.code != 0 ? GEMM_ERR_TIMEOUT : GEMM_OK;
+}
+
 int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
             int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
             int group, void* C, int64_t ldc, int dtype, void* stream) {

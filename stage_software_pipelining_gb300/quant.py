@@ -23,7 +23,7 @@ GROUPS = (32, 64, 128)          # K per scale of the 4-bit weights
 E4M3_MAX = 448.0                # largest e4m3 value
 
 # Every extern "C" symbol include/quant.h declares.
-EXPORTS = ("add_rmsnorm", "quantize_fp8", "gemm_fp8", "gemv_w4", "quantize_w4")
+EXPORTS = ("add_rmsnorm", "quantize_fp8", "gemm_fp8", "gemm_fp8_checked", "gemv_w4", "quantize_w4")
 
 _TYPES = {torch.float32: QUANT_F32, torch.float16: QUANT_F16, torch.bfloat16: QUANT_BF16}
 _E4M3 = torch.float8_e4m3fn
@@ -42,6 +42,7 @@ def load_library():
                                         i64, p, p]
             lib.quantize_fp8.argtypes = [i64, i64, p, i64, i32, p, i64, p, p]
             lib.gemm_fp8.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, p, i32, p]
+            lib.gemm_fp8_checked.argtypes = lib.gemm_fp8.argtypes
             lib.gemv_w4.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, i32, p, i64,
                                     i32, p]
             lib.quantize_w4.argtypes = [i64, i64, p, i64, i32, i32, p, i64, p, i64, i32, p, i64, p]
@@ -174,8 +175,10 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *,
 
 
 def gemm_fp8(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, a_scale: torch.Tensor,
-             b_scale: torch.Tensor, *, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
-    """C = diag(a_scale) A B diag(b_scale) in place (libgemm.so gemm_fp8).
+             b_scale: torch.Tensor, *, stream: torch.cuda.Stream | None = None,
+             checked: bool = False) -> torch.Tensor:
+    """C = diag(a_scale) A B diag(b_scale) in place (libgemm.so gemm_fp8, or
+    gemm_fp8_checked, which synchronises and reports a wait that ran out).
 
     A: M x K float8_e4m3fn, row-major; B: K x N float8_e4m3fn, column-major (a
     transposed view of the N x K weights); C: M x N fp16 or bf16, row-major;
@@ -194,7 +197,7 @@ def gemm_fp8(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, a_scale: torch.T
     ldc = _rows(C, "C", C.dtype, (M, N), device)
     _vector(a_scale, "a_scale", torch.float32, M, device)
     _vector(b_scale, "b_scale", torch.float32, N, device)
-    _call("gemm_fp8", device, stream, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(),
+    _call("gemm_fp8_checked" if checked else "gemm_fp8", device, stream, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(),
           ldc, a_scale.data_ptr(), b_scale.data_ptr(), _TYPES[C.dtype])
     return C
 

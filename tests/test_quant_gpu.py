@@ -210,7 +210,7 @@ def fp8_case(M, N, K, dtype, seed=20):
     return C.view
 
 
-FP8_SHAPES = [(1, 1, 1), (1, 64, 128), (1, 4096, 512), (2, 130, 33), (8, 256, 1000), (15, 17, 129), (16, 384, 2048),
+FP8_SHAPES = [(300, 700, 8), (2000, 900, 512), (1300, 2600, 300), (1, 1, 1), (1, 64, 128), (1, 4096, 512), (2, 130, 33), (8, 256, 1000), (15, 17, 129), (16, 384, 2048),
               (17, 100, 256), (33, 1000, 640), (48, 2048, 512), (64, 129, 127), (65, 512, 384), (100, 260, 512),
               (128, 128, 128), (129, 129, 129), (200, 520, 192), (255, 777, 1040), (256, 256, 2048),
               (300, 4096, 256), (513, 1025, 257), (1000, 1504, 1000), (2048, 512, 64), (1, 3, 2000)]
@@ -255,6 +255,23 @@ def test_gemm_fp8_overflow_and_scales(M):
     Q.gemm_fp8(A, W.t(), C, sa, sb)
     expect = (K * sa[:, None] * sb[None, :]).to(F16)
     assert torch.equal(C, expect) and torch.isinf(C).any() and not C[0].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 600, 2048), (600, 600, 2048), (200, 300, 1500)])
+def test_gemm_fp8_stuck_pipeline_is_reported(M, N, K):
+    """A stage whose copy never comes ends in GEMM_ERR_TIMEOUT, and the next call is right."""
+    A, sa = fp8_rows(rand(42, M, K))
+    W, sb = fp8_rows(rand(43, N, K))
+    C = torch.empty(M, (N + 7) // 8 * 8, dtype=BF16, device="cuda")[:, :N]
+    try:
+        G.debug_set(wait_limit_ns=50_000_000, withhold_arrive=1)
+        with pytest.raises(G.GemmError, match="TIMEOUT"):
+            Q.gemm_fp8(A, W.t(), C, sa, sb, checked=True)
+    finally:
+        G.debug_set()
+    Q.gemm_fp8(A, W.t(), C, sa, sb, checked=True)
+    ref, absb = R.gemm_fp8(A, W.t(), sa, sb)
+    R.check_rounded(C, ref, 2.0 ** -22, R.SUM_REL * absb, "after a timeout")
 
 
 def test_gemm_fp8_empty():
