@@ -119,7 +119,8 @@ int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  * are fp32.  K = 0 gives C = 0.
  * Alignment (GEMM_ERR_ALIGN otherwise): x and W start on 16-byte boundaries,
  * ldx*2 and ldw are multiples of 16; the others are aligned to their element.
- * M and N above 2^31 - 1 and K above 2^30 are GEMM_ERR_UNSUPPORTED.
+ * M and N above 2^31 - 1, K above 2^26 and lds or ldz above 2^22 are
+ * GEMM_ERR_UNSUPPORTED.
  */
 int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
             int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,

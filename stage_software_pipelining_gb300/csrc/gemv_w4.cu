@@ -1,87 +1,23 @@
 // gemv_w4.cu -- C[i,j] = sum_groups scales[j,g] * sum_{k in g} x[i,k] * (w[j,k] - zeros[j,g])
-// with 4-bit weights w, and the kernel that makes them.
+// with 4-bit weights w, for up to 16 rows of x, and the kernel that makes such
+// weights.  (More rows: gemv_w4_tc.cu.)
 //
 // w4_kernel is bound by reading the weights.  A warp of the CTA copies blocks
-// of them (128 or 256 rows by 256 or 128 of K) and of x through a ring of
-// shared-memory stages with tensor copies; eight warps turn the nibbles into
-// 16-bit values in registers and multiply them with mma.sync, weights as the
-// 16-row operand and up to 8 NT rows of x as the columns.  (tcgen05 takes its
-// operands from shared memory or TMEM: values that were just unpacked in
-// registers would have to be written out again, and the products are far
-// from a limit here.)  The sums of a group are scaled in fp32 once they are
-// complete, so that no weight is rounded.  K is also cut over the CTAs of a
-// cluster, whose partials are added in order through distributed shared memory.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
+// of them (64 rows by 256 of K) and of x through a ring of shared-memory stages
+// with tensor copies; eight warps turn the nibbles into 16-bit values in
+// registers and multiply them with mma.sync, weights as the 16-row operand and
+// up to 8 NT rows of x as the columns.  The sums of a group are scaled in fp32
+// once they are complete, so that no weight is rounded.  K is also cut over the
+// CTAs of a cluster, whose partials are added in order through distributed
+// shared memory.
 #include <type_traits>
 
-#include "../../include/quant.h"
-#include "internal.h"
-#include "ptx.cuh"
-#include "quant.h"
+#include "gemv_w4.cuh"
 
 namespace ssp {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float f32_of(T v);
-template <>
-__device__ __forceinline__ float f32_of(float v) { return v; }
-template <>
-__device__ __forceinline__ float f32_of(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float f32_of(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T of_f32(float v);
-template <>
-__device__ __forceinline__ __half of_f32(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 of_f32(float v) { return __float2bfloat16_rn(v); }
-
-constexpr int kWarps = 8;                       // consumer warps; one more issues the copies
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kMaxStages = 8;
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;
-
-struct W4Params {
-    int M, N, K;
-    int tiles_m, groups;  // groups of a row
-    int blocks;           // K blocks of KS
-    int split;            // CTAs of a cluster, each with a part of the K blocks
-    int stages, x_rows;   // ring depth; rows of x in a stage
-    const void* scales;
-    long long lds;
-    const uint8_t* zeros;
-    long long ldz;
-    void* C;
-    long long ldc;
-};
-
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((n & 15u) == 0) {
-            if (*abort) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
+using namespace w4;
 
 // D = A B + C of 16 x 8 x 16 on one warp, fp32 accumulation.
 template <bool BF16>
@@ -98,90 +34,81 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// (a & mask) | magic in one instruction.
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
-    return r;
-}
-
-__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
-__device__ __forceinline__ __nv_bfloat162 b2(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
-template <typename V>
-__device__ __forceinline__ uint32_t u32(V v) { return *reinterpret_cast<uint32_t*>(&v); }
-
-// Eight 4-bit weights less their zero point, as four pairs (k, k + 4), exact in
-// 16 bits.  A nibble under the exponent of 2^7 (bf16: 7 mantissa bits) or 2^10
-// (fp16) reads as 128 + w or 1024 + w, from which 128 + z or 1024 + z is
-// subtracted; an fp16 nibble four places higher reads as 1024 + 16 w, of which
-// a sixteenth less 64 + z is one multiply-add and saves the shift.
+// The same eight weights without their zero point: bf16 128 + w; fp16 the
+// bare bits, w 2^-24 in pairs 0 and 2 and w 2^-20 in pairs 1 and 3.
 template <bool BF16>
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t zero, uint32_t zero16, uint32_t (&p)[4]) {
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
     if constexpr (BF16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            p[i] = u32(__hsub2(b2(and_or(w >> (4 * i), 0x000f000fu, 0x43004300u)), b2(zero)));
+        for (int i = 0; i < 4; ++i) p[i] = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
     } else {
-        const __half2 sixteenth = h2(0x2c002c00u);  // 1/16
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t v = w >> (8 * i);
-            p[2 * i] = u32(__hsub2(h2(and_or(v, 0x000f000fu, 0x64006400u)), h2(zero)));
-            p[2 * i + 1] = u32(__hfma2(h2(and_or(v, 0x00f000f0u, 0x64006400u)), sixteenth, h2(zero16)));
-        }
+        p[0] = w & 0x000f000fu;
+        p[1] = w & 0x00f000f0u;
+        p[2] = (w >> 8) & 0x000f000fu;
+        p[3] = (w >> 8) & 0x00f000f0u;
     }
 }
 
-// The zero point as unpack wants it: (128 + z) or (1024 + z) twice, and for
-// fp16 -(64 + z) twice.
-template <bool BF16>
-__device__ __forceinline__ void zero_of(uint32_t z, uint32_t& zero, uint32_t& zero16) {
-    if constexpr (BF16) {
-        zero = (0x4300u | z) * 0x00010001u;
-        zero16 = 0;
-    } else {
-        zero = (0x6400u | z) * 0x00010001u;
-        zero16 = (0xd400u | (z << 4)) * 0x00010001u;  // -(64 + z): 2^6 has 16 steps a unit
-    }
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-// Geometry of a CTA for up to 8 NT rows of x: R weight rows (32 a warp) by
-// blocks of KS of K (128 a warp).
-template <int NT>
-struct Geo {
-    static constexpr int WK = NT == 4 ? 1 : 2;   // warps along K
-    static constexpr int WR = kWarps / WK;       // warps along the weight rows
-    static constexpr int R = 32 * WR;
-    static constexpr int KS = 128 * WK;
-    static constexpr int W_BYTES = R * KS / 2;
-    static constexpr int MT = 8 * NT;
-    static constexpr int PITCH = R + 4;          // of a partial's rows: no bank conflicts when written
-    static constexpr int PART_FLOATS = WK * MT * PITCH;
-};
+// Geometry of a CTA: CW consuming warps and one that issues copies.  A
+// consuming warp takes 32 weight rows of a stage; stages go to the WK groups
+// of warps in turn.  Two CTAs an SM.
+constexpr int WK = 4;
+constexpr int WR = 2;
+constexpr int CW = WK * WR;
+constexpr int R = 32 * WR;          // weight rows of a tile
+constexpr int kThreads = 32 * (CW + 1);
+constexpr int kBudget = 100 * 1024; // dynamic shared memory
+constexpr int W_BYTES = R * KS / 2;
+constexpr int PITCH = R + 4;        // of a partial's rows: no bank conflicts when written
 
-template <bool BF16, int NT, int GROUP>
+// SLOTS: one row of x (SLOTS = 8) or up to four (2) leave columns of the
+// 16 x 8 x 16 product empty.  They hold other groups: column `slot * 8/SLOTS +
+// row` sees x only in the K of group `slot` and zeros elsewhere, so SLOTS
+// groups accumulate side by side and are scaled together, each by the lane
+// that holds its column, where one slot would have all four lanes of a row
+// scale the same group.
+//
+// With SLOTS = 8 that makes a group's end cheap enough to move the zero point
+// there as well: sum x (w - z) = sum x w' - z' sum x with w' a nibble as it
+// lies under its mask, and sum x from one more product whose weights are all
+// alike, summed in the same order.  fp16 takes the bare nibble, a subnormal
+// w 2^-24 (or w 2^-20, four bits up: sums of their own), bf16 128 + w under an
+// exponent.  That is 5 (fp16) or 7 (bf16) instructions for 8 weights in place
+// of 9 or 11.  All of it is fp32; the difference of the two sums has about 2
+// (fp16) or 30 (bf16) times the rounding of sum x (w - z), far below a 16-bit
+// result's own.  Weights that all equal the zero point 8 give exactly 0.
+template <bool BF16, int NT, int SLOTS, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 2)
-    w4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const W4Params p) {
+    w4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-    using Gm = Geo<NT>;
-    constexpr int KS = Gm::KS, R = Gm::R;
-    constexpr int SUB = 128 / GROUP;        // groups in a warp's 128 of K
+    static_assert(SLOTS == 1 || NT == 1, "slots fill the columns of a single tile");
+    constexpr int MT = 8 * NT;
+    constexpr int GPS = KS / GROUP;      // groups of a stage
+    constexpr int LG = (GPS + 3) / 4;    // values a lane loads where four lanes share a row's groups
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ unsigned long long bars[2 * kMaxStages];
+    __shared__ uint4 no_x[SLOTS > 1 ? 32 : 1];  // zeros, as long as one row of x in a stage
     __shared__ int abort_word;
     const int S = p.stages;
-    const int x_bytes = p.x_rows * KS * 2;
+    const int x_rows = SLOTS == 8 ? 1 : p.x_rows;
+    const int x_bytes = x_rows * KS * 2;
     const int x_slot = (x_bytes + 127) & ~127;
-    uint8_t* x_ring = smem + S * Gm::W_BYTES;
+    uint8_t* x_ring = smem + S * W_BYTES;
     float* part = reinterpret_cast<float*>(smem);  // over the ring once it is read
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = p.split;
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int cl = static_cast<int>(blockIdx.x) / split;
-    const int m0 = (cl % p.tiles_m) * Gm::MT, n0 = (cl / p.tiles_m) * R;
+    const int m0 = (cl % p.tiles_m) * MT, n0 = (cl / p.tiles_m) * R;
     const int k0 = static_cast<int>(static_cast<long long>(p.blocks) * rank / split);
     const int k1 = static_cast<int>(static_cast<long long>(p.blocks) * (rank + 1) / split);
     const uint32_t bar0 = smem_addr(bars);
@@ -194,24 +121,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_prefetch_desc(&tmX);
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), kWarps);
+            mbar_init(empty_bar(s), WR);
         }
         abort_word = 0;
         fence_barrier_init();
     }
+    if (SLOTS > 1 && threadIdx.x < 32) no_x[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     griddep_launch_dependents();
     griddep_wait();
 
     int issued = 0;  // the producing thread's stages
-    if (warp == kWarps) {
+    if (warp == CW) {
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
             for (int kb = k0; kb < k1; ++kb, ++issued) {
                 if (!wait_for(empty_bar(s), ph ^ 1u, abort_flag)) break;
-                mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(Gm::W_BYTES + x_bytes));
-                tma_load_2d(smem_addr(smem + s * Gm::W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
+                mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(W_BYTES + x_bytes));
+                tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
                 tma_load_3d(smem_addr(x_ring + s * x_slot), &tmX, full_bar(s), 0, m0, kb * (KS / 32));
                 if (++s == S) {
                     s = 0;
@@ -220,169 +148,261 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         __syncwarp();
+        __syncthreads();
+        if (*abort_flag) {
+            // Copies that nobody waited for land before the ring is reused.
+            if (lane == 0)
+                for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j)
+                    drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1));
+            __syncthreads();
+        }
     } else {
-        const int wr = warp % Gm::WR, wk = warp / Gm::WR;
+        const int wr = warp % WR, wk = warp / WR;
         const int g = lane >> 2, c = lane & 3;
-        // The scales (and zero points) of this lane's four rows g, g + 8, g + 16,
-        // g + 24 of the warp: lane c of a row's four loads group min(c, SUB - 1)
-        // of the warp's 128 of K, one block ahead.  Rows past N read the last
-        // row's; their results are not stored.
-        const T* sp[4];
-        const uint8_t* zp[4];
+        // This lane's four weight rows are 8 i + g of the warp's 32.  Rows past N
+        // read the last row's scales; their results are not stored.
+        const T* s_tile = static_cast<const T*>(p.scales) + n0 * p.lds;
+        const uint8_t* z_tile = ZEROS ? p.zeros + n0 * p.ldz : nullptr;
+        uint32_t s_off[4], z_off[4];  // within the tile's rows
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const long long n = min(n0 + 32 * wr + 8 * i + g, p.N - 1);
-            sp[i] = static_cast<const T*>(p.scales) + n * p.lds;
-            zp[i] = p.zeros ? p.zeros + n * p.ldz : nullptr;
+            const int n = min(32 * wr + 8 * i + g, p.N - 1 - n0);
+            s_off[i] = static_cast<uint32_t>(n * static_cast<int>(p.lds));
+            z_off[i] = ZEROS ? static_cast<uint32_t>(n * static_cast<int>(p.ldz)) : 0u;
         }
-        T sv[4];
-        uint32_t zv[4];
-        auto fetch = [&](int kb) {
-            const int gi = kb * (KS / GROUP) + wk * SUB + (c < SUB ? c : SUB - 1);
-            const bool in = kb < k1 && gi < p.groups;
+        auto scale_at = [&](int i, int kb, int group) -> T {
+            const int gi = kb * GPS + group;
+            return kb < k1 && gi < p.groups ? s_tile[s_off[i] + static_cast<uint32_t>(gi)] : of_f32<T>(0.0f);
+        };
+        auto zero_at = [&](int i, int kb, int group) -> uint32_t {
+            const int gi = kb * GPS + group;
+            return kb < k1 && gi < p.groups ? z_tile[z_off[i] + static_cast<uint32_t>(gi)] : 0u;
+        };
+        // Scales, a stage ahead (SLOTS = 8: those of the running SLOTS groups).
+        //   SLOTS = 8: [0], [1] the two columns of this lane, groups 2c and 2c + 1
+        //   SLOTS = 2: [u] group 2u + c/2 of the stage
+        //   SLOTS = 1: [u] group 4u + c (a lane a group; the others ask for it)
+        constexpr int SV = SLOTS == 8 ? 2 : SLOTS == 2 ? GPS / 2 : LG;
+        T sv[SV][4];
+        // Zero points: SLOTS = 8 as the scales, else [u] group 4u + c.
+        constexpr int ZV = SLOTS == 8 ? 2 : LG;
+        uint32_t zv[ZV][4];
+        auto fetch_scales = [&](int kb) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sv[i] = in ? sp[i][gi] : of_f32<T>(0.0f);
-                zv[i] = !p.zeros ? 8u : in ? zp[i][gi] : 0u;
+            for (int u = 0; u < SV; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (SLOTS == 8) {
+                        const int slot = 2 * c + u, stage = kb + WK * (slot / GPS);
+                        sv[u][i] = scale_at(i, stage, slot % GPS);
+                        if constexpr (ZEROS) zv[u][i] = zero_at(i, stage, slot % GPS);
+                    } else if constexpr (SLOTS == 2) {
+                        sv[u][i] = scale_at(i, kb, 2 * u + (c >> 1));
+                    } else {
+                        sv[u][i] = scale_at(i, kb, min(4 * u + c, GPS - 1));
+                    }
+                }
+        };
+        auto fetch_zeros = [&](int kb) {
+            if constexpr (ZEROS && SLOTS != 8) {
+#pragma unroll
+                for (int u = 0; u < LG; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) zv[u][i] = zero_at(i, kb, min(4 * u + c, GPS - 1));
             }
         };
-        fetch(k0);
-        float acc[2][NT][4] = {};
-        int s = 0;
+        if constexpr (SLOTS != 8) fetch_scales(k0 + wk);
+        fetch_zeros(k0 + wk);
+
+        float acc[2][NT][4] = {};  // scaled sums (SLOTS = 8: [.][.][0], [2] of rows g, g + 8)
+        float sub[2][NT][4] = {};  // sums of the running groups
+        // SLOTS = 8: groups so far; fp16's sums of w 2^-20; sum x (fp16: of k in
+        // sub, of k in sub16) times the weight that stands for it
+        int pos = 0;
+        float sub16[2][4] = {}, xsum[4] = {}, xsum16[4] = {};
+        constexpr uint32_t kAlike = !BF16 ? 0x3c003c00u : ZEROS ? 0x43004300u : 0x43084308u;  // 1; 128; 136
+        // This lane's word of 16-byte chunk 0 in a 128-byte swizzled row: chunk j
+        // of row r lies at chunk j ^ (r & 7).
+        const uint32_t w_row = smem_addr(smem) + static_cast<uint32_t>((32 * wr + g) * 128 + 16 * g + 4 * c);
+        constexpr int XM = 8 / SLOTS;  // rows of x side by side in the columns
+        uint32_t x_off[NT];
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+            x_off[b] = smem_addr(x_ring) + static_cast<uint32_t>(min(8 * b + g % XM, x_rows - 1) * 64 + 16 * c);
+        const uint32_t no_x_at = smem_addr(no_x) + 16u * c;
+        int s = wk;
         uint32_t ph = 0;
-        // This lane's byte in a 128-byte (64-byte) swizzled row: 16-byte chunk
-        // j of row r is at j ^ (r & 7) (j ^ ((r >> 1) & 3)).
-        const uint32_t w_row = static_cast<uint32_t>((32 * wr + g) * (KS / 2) + 4 * c);
-        for (int kb = k0; kb < k1; ++kb) {
-            float scale[4];
-            uint32_t zero[4];
+        for (int kb = k0 + wk; kb < k1; kb += WK) {
+            float scale[SV][4];
+            uint32_t zero[LG][4];
+            if constexpr (SLOTS == 8) {
+                if (pos == 0) fetch_scales(kb);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                scale[i] = f32_of(sv[i]);
-                zero[i] = zv[i];
+                for (int u = 0; u < SV; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) scale[u][i] = f32_of(sv[u][i]);
             }
+#pragma unroll
+            for (int u = 0; u < LG; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if constexpr (ZEROS && SLOTS != 8) zero[u][i] = zero_of<BF16>(zv[u][i]);
             if (!wait_for(full_bar(s), ph, abort_flag)) break;
-            fetch(kb + 1);
-            const uint32_t w_at = smem_addr(smem + s * Gm::W_BYTES) + w_row;
-            const uint32_t x_at = smem_addr(x_ring + s * x_slot);
-            float sub[2][NT][4];
+            if constexpr (SLOTS != 8) fetch_scales(kb + WK);
+            fetch_zeros(kb + WK);
+            const uint32_t w_at = w_row + static_cast<uint32_t>(s * W_BYTES);
+            const uint32_t x_at = static_cast<uint32_t>(s * x_slot);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // 32 of K
-                if (j % (GROUP / 32) == 0)
+            for (int u = 0; u < GPS; ++u) {  // a group of K
+                uint32_t z0[4], z16[4];
 #pragma unroll
-                    for (int a = 0; a < 2; ++a)
-#pragma unroll
-                        for (int b = 0; b < NT; ++b)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) sub[a][b][e] = 0.0f;
-                // x of this lane's column (row of x) and eight k, re-paired (k, k + 4).
-                uint32_t xb[NT][4];
-#pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    const int m = min(8 * b + g, p.x_rows - 1);
-                    const uint4 v = ld_shared_v4(x_at + static_cast<uint32_t>(((wk * 4 + j) * p.x_rows + m) * 64 + 16 * c));
-                    xb[b][0] = __byte_perm(v.x, v.z, 0x5410);
-                    xb[b][1] = __byte_perm(v.x, v.z, 0x7632);
-                    xb[b][2] = __byte_perm(v.y, v.w, 0x5410);
-                    xb[b][3] = __byte_perm(v.y, v.w, 0x7632);
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (!ZEROS || SLOTS == 8) z0[i] = zero_of<BF16>(8u);
+                    else z0[i] = GPS == 1 ? zero[0][i] : __shfl_sync(0xffffffffu, zero[u / 4][i], u % 4, 4);
+                    z16[i] = zero16_of<BF16>(z0[i]);
                 }
+                const bool mine = SLOTS == 1 || g / XM == (SLOTS == 8 ? pos + u : u % SLOTS);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {  // 16 weight rows
-                    uint32_t q[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int i = 2 * a + h;  // rows 8 i + g of the warp
-                        const int chunk = Gm::WK == 2 ? (wk * 4 + j) ^ g : j ^ ((g >> 1) & 3);
-                        const uint32_t w = ld_shared_u32(w_at + static_cast<uint32_t>(8 * i * (KS / 2) + 16 * chunk));
-                        const uint32_t z = SUB == 1 ? zero[i] : __shfl_sync(0xffffffffu, zero[i], (lane & 28) + j / (GROUP / 32));
-                        uint32_t z0, z16;
-                        zero_of<BF16>(z, z0, z16);
-                        unpack<BF16>(w, z0, z16, q[h]);
-                    }
-                    const uint32_t lo[4] = {q[0][0], q[1][0], q[0][1], q[1][1]};
-                    const uint32_t hi[4] = {q[0][2], q[1][2], q[0][3], q[1][3]};
+                for (int jj = 0; jj < GROUP / 32; ++jj) {  // 32 of K
+                    const int j = u * (GROUP / 32) + jj;
+                    // x of this lane's column and eight k, re-paired (k, k + 4).
+                    uint32_t xb[NT][4];
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        mma16816<BF16>(sub[a][b], lo, xb[b][0], xb[b][1]);
-                        mma16816<BF16>(sub[a][b], hi, xb[b][2], xb[b][3]);
+                        uint32_t at;
+                        if constexpr (SLOTS == 8) at = (mine ? x_at + x_off[b] : no_x_at) + 64u * j;
+                        else at = x_at + x_off[b] + static_cast<uint32_t>(j * x_rows * 64);
+                        if (SLOTS == 2 && !mine) at = no_x_at;
+                        const uint4 v = ld_shared_v4(at);
+                        xb[b][0] = __byte_perm(v.x, v.z, 0x5410);
+                        xb[b][1] = __byte_perm(v.x, v.z, 0x7632);
+                        xb[b][2] = __byte_perm(v.y, v.w, 0x5410);
+                        xb[b][3] = __byte_perm(v.y, v.w, 0x7632);
                     }
-                }
-                if (j % (GROUP / 32) == GROUP / 32 - 1) {  // a group is complete: scale its sums
+                    if constexpr (SLOTS == 8) {
+                        const uint32_t alike[4] = {kAlike, kAlike, kAlike, kAlike};
+                        if constexpr (BF16) {
+                            mma16816<BF16>(xsum, alike, xb[0][0], xb[0][1]);
+                            mma16816<BF16>(xsum, alike, xb[0][2], xb[0][3]);
+                        } else {
+                            mma16816<BF16>(xsum, alike, xb[0][0], xb[0][2]);
+                            mma16816<BF16>(xsum16, alike, xb[0][1], xb[0][3]);
+                        }
+                    }
 #pragma unroll
-                    for (int a = 0; a < 2; ++a)
+                    for (int a = 0; a < 2; ++a) {  // 16 weight rows
+                        uint32_t q[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int i = 2 * a + h;
-                            const float f = SUB == 1 ? scale[i] : __shfl_sync(0xffffffffu, scale[i], (lane & 28) + j / (GROUP / 32));
-#pragma unroll
-                            for (int b = 0; b < NT; ++b) {
-                                acc[a][b][2 * h] = fmaf(f, sub[a][b][2 * h], acc[a][b][2 * h]);
-                                acc[a][b][2 * h + 1] = fmaf(f, sub[a][b][2 * h + 1], acc[a][b][2 * h + 1]);
-                            }
+                            const uint32_t w = ld_shared_u32((w_at ^ static_cast<uint32_t>(16 * j)) +
+                                                             static_cast<uint32_t>(8 * i * (KS / 2)));
+                            if constexpr (SLOTS == 8) nibbles<BF16>(w, q[h]);
+                            else unpack<BF16>(w, z0[i], z16[i], q[h]);
                         }
+                        if constexpr (SLOTS == 8 && !BF16) {
+                            const uint32_t even[4] = {q[0][0], q[1][0], q[0][2], q[1][2]};
+                            const uint32_t odd[4] = {q[0][1], q[1][1], q[0][3], q[1][3]};
+                            mma16816<BF16>(sub[a][0], even, xb[0][0], xb[0][2]);
+                            mma16816<BF16>(sub16[a], odd, xb[0][1], xb[0][3]);
+                            continue;
+                        }
+                        const uint32_t lo[4] = {q[0][0], q[1][0], q[0][1], q[1][1]};
+                        const uint32_t hi[4] = {q[0][2], q[1][2], q[0][3], q[1][3]};
+#pragma unroll
+                        for (int b = 0; b < NT; ++b) {
+                            mma16816<BF16>(sub[a][b], lo, xb[b][0], xb[b][1]);
+                            mma16816<BF16>(sub[a][b], hi, xb[b][2], xb[b][3]);
+                        }
+                    }
+                }
+                if constexpr (SLOTS != 8) {
+                    if (u % SLOTS == SLOTS - 1) {  // the groups are complete: scale their sums
+#pragma unroll
+                        for (int a = 0; a < 2; ++a)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int i = 2 * a + h;
+                                const float f = SLOTS == 2 ? scale[u / 2 % SV][i]
+                                                : GPS == 1 ? scale[0][i]
+                                                           : __shfl_sync(0xffffffffu, scale[u / 4 % SV][i], u % 4, 4);
+#pragma unroll
+                                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                    for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                                        acc[a][b][e] = fmaf(f, sub[a][b][e], acc[a][b][e]);
+                                        sub[a][b][e] = 0.0f;
+                                    }
+                            }
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty_bar(s));
-            if (++s == S) {
-                s = 0;
+            s += WK;
+            if (s >= S) {
+                s -= S;
                 ph ^= 1u;
+            }
+            if constexpr (SLOTS == 8) {
+                pos += GPS;
+                if (pos == 8 || kb + WK >= k1) {
+                    pos = 0;
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = 2 * a + (e >> 1), u = e & 1;
+                            const float z = ZEROS ? static_cast<float>(zv[u][i]) : 8.0f;
+                            float t;
+                            if constexpr (BF16) {
+                                t = ZEROS ? fmaf(-fmaf(z, 0x1p-7f, 1.0f), xsum[u], sub[a][0][e]) : sub[a][0][e] - xsum[u];
+                            } else {
+                                t = fmaf(-z, xsum[u], sub[a][0][e] * 0x1p24f) +
+                                    fmaf(-z, xsum16[u], sub16[a][e] * 0x1p20f);
+                            }
+                            acc[a][0][e & 2] = fmaf(f32_of(sv[u][i]), t, acc[a][0][e & 2]);
+                            sub[a][0][e] = sub16[a][e] = 0.0f;
+                        }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) xsum[e] = xsum16[e] = 0.0f;
+                }
             }
         }
         // The ring is read by every warp before partials lie over it.
         __syncthreads();
         if (*abort_flag) __syncthreads();
-        float* mine = part + wk * Gm::MT * Gm::PITCH;
+        float* mine = part + wk * MT * PITCH;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int n = 32 * wr + 16 * a + 8 * (e >> 1) + g, m = 8 * b + 2 * c + (e & 1);
-                    mine[m * Gm::PITCH + n] = acc[a][b][e];
+                    const int n = 32 * wr + 16 * a + 8 * (e >> 1) + g;
+                    float v = acc[a][b][e];
+                    if constexpr (SLOTS == 8) {  // the eight slots are in four lanes
+                        if (e & 1) continue;
+                        v += __shfl_xor_sync(0xffffffffu, v, 1);
+                        v += __shfl_xor_sync(0xffffffffu, v, 2);
+                        if (c == 0) mine[n] = v;
+                    } else if constexpr (SLOTS == 2) {  // column 4 slot + row
+                        v += __shfl_xor_sync(0xffffffffu, v, 2);
+                        if (c < 2) mine[(2 * c + (e & 1)) * PITCH + n] = v;
+                    } else {
+                        mine[(8 * b + 2 * c + (e & 1)) * PITCH + n] = v;
+                    }
                 }
-    }
-    if (warp == kWarps) {
-        __syncthreads();
-        if (*abort_flag) {
-            // Copies that nobody waited for land before the ring is reused.
-            if (lane == 0)
-                for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j) {
-                    const unsigned long long t0 = globaltimer_ns();
-                    while (!mbar_try_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1)))
-                        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-                }
-            __syncthreads();
-        }
     }
     if (split > 1) cluster_sync_all();
     else __syncthreads();
     // CTA `rank` adds the cluster's partials of its share of the outputs, in
     // order, four adjacent ones a thread.
-    const int rows = min(Gm::MT, p.M - m0);
-    const int total = rows * (R / 4);
-    const uint32_t part_addr = smem_addr(part);
+    const int total = min(MT, p.M - m0) * (R / 4);
     for (int i = total * rank / split + static_cast<int>(threadIdx.x); i < total * (rank + 1) / split; i += kThreads) {
         const int m = i / (R / 4), col = i % (R / 4) * 4;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int r = 0; r < split; ++r)
-#pragma unroll
-            for (int k = 0; k < Gm::WK; ++k) {
-                const int at = (k * Gm::MT + m) * Gm::PITCH + col;
-                const float4 u = split == 1 ? *reinterpret_cast<const float4*>(part + at)
-                                            : ld_cluster_f4(mapa_shared(part_addr + 4u * at, static_cast<uint32_t>(r)));
-                v.x += u.x;
-                v.y += u.y;
-                v.z += u.z;
-                v.w += u.w;
-            }
-        const int n = n0 + col;
-        T* out = static_cast<T*>(p.C) + static_cast<long long>(m0 + m) * p.ldc + n;
-        const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) out[e] = of_f32<T>(f[e]);
+        store4<T>(p, m0 + m, n0 + col, add_partials(smem_addr(part), m * PITCH + col, WK, MT * PITCH, split));
     }
     if (split > 1) cluster_sync_all();  // the peers have read this CTA's partials
 }
@@ -428,45 +448,14 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4QuantLaunch p)
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
-// The packed weights as N rows of K/2 bytes, boxes of R rows by one K block,
-// swizzled over the block's bytes.
-template <int NT>
-bool encode_w(CUtensorMap* map, const W4Launch& L) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(L.K / 2), static_cast<cuuint64_t>(L.N)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(L.ldw)};
-    cuuint32_t box[2] = {Geo<NT>::KS / 2, Geo<NT>::R};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(L.W), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              Geo<NT>::KS == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // x as K/32 slices of M rows by 32 elements (64 bytes): a box lands slice by
 // slice, so that a warp's 16-byte reads of eight rows touch every bank once.
-template <int NT>
 bool encode_x(CUtensorMap* map, const W4Launch& L, int x_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {32, static_cast<cuuint64_t>(L.M), static_cast<cuuint64_t>(L.K / 32)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(L.ldx * 2), 64};
-    cuuint32_t box[3] = {32, static_cast<cuuint32_t>(x_rows), Geo<NT>::KS / 32};
+    cuuint32_t box[3] = {32, static_cast<cuuint32_t>(x_rows), KS / 32};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, L.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
               const_cast<void*>(L.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -474,78 +463,45 @@ bool encode_x(CUtensorMap* map, const W4Launch& L, int x_rows) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16, int NT, int GROUP>
+template <bool BF16, int NT, int SLOTS, int GROUP, bool ZEROS>
 int launch_one(const W4Launch& L, cudaStream_t stream) {
-    using Gm = Geo<NT>;
-    W4Params p = {};
-    p.M = static_cast<int>(L.M);
-    p.N = static_cast<int>(L.N);
-    p.K = static_cast<int>(L.K);
-    p.groups = static_cast<int>(L.K / GROUP);
-    p.blocks = static_cast<int>((L.K + Gm::KS - 1) / Gm::KS);
-    p.tiles_m = static_cast<int>((L.M + Gm::MT - 1) / Gm::MT);
-    p.x_rows = static_cast<int>(L.M < Gm::MT ? L.M : Gm::MT);
-    p.scales = L.scales;
-    p.lds = L.lds;
-    p.zeros = L.zeros;
-    p.ldz = L.ldz;
-    p.C = L.C;
-    p.ldc = L.ldc;
-    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * ((L.N + Gm::R - 1) / Gm::R);
-    const int sms = tc_current_device_sms();
-    if (sms <= 0) return GEMM_ERR_CUDA;
-    // Two CTAs an SM.  Cut K over up to 8 CTAs while they are all resident and
-    // each keeps two blocks.
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * sms && p.blocks / (2 * split) >= 2) split *= 2;
-    p.split = split;
-    if (tiles * split > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
-    const int slot = Gm::W_BYTES + ((p.x_rows * Gm::KS * 2 + 127) & ~127);
-    constexpr int kBudget = 110 * 1024;
-    int stages = (kBudget - 1024) / slot;
-    if (stages > kMaxStages) stages = kMaxStages;
-    p.stages = stages;
-    static_assert(Gm::PART_FLOATS * 4 <= 3 * Gm::W_BYTES && 3 * (Gm::W_BYTES + Gm::MT * Gm::KS * 2) <= kBudget - 1024,
-                  "the partials lie over the ring, which has three stages at least");
+    Params p = params_of(L);
+    p.tiles_m = 1;
+    p.x_rows = static_cast<int>(L.M);
+    const int slot = W_BYTES + ((p.x_rows * KS * 2 + 127) & ~127);
+    const int stages = (kBudget - 1024) / slot;
+    p.stages = stages < kMaxStages ? stages : kMaxStages;
+    static_assert(WK * 8 * NT * PITCH * 4 <= 5 * W_BYTES && 5 * (W_BYTES + 8 * NT * KS * 2) <= kBudget - 1024,
+                  "the partials lie over the ring, which has five stages at least");
+    auto kernel = w4_kernel<BF16, NT, SLOTS, GROUP, ZEROS>;
+    static Residency res;
+    int resident[9];
+    if (!res.get(reinterpret_cast<const void*>(kernel), kThreads, kBudget, resident)) return GEMM_ERR_LAUNCH;
+    const int64_t tiles = (L.N + R - 1) / R;
+    p.split = choose_split(tiles, p.blocks, 2, resident);
     CUtensorMap tmW, tmX;
-    if (!encode_w<NT>(&tmW, L) || !encode_x<NT>(&tmX, L, p.x_rows)) return GEMM_ERR_LAUNCH;
-    auto kernel = w4_kernel<BF16, NT, GROUP>;
-    {
-        static std::mutex mu;
-        static bool done[64] = {};
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GEMM_ERR_CUDA;
-        std::lock_guard<std::mutex> g(mu);
-        if (!done[dev]) {
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget) != cudaSuccess)
-                return GEMM_ERR_LAUNCH;
-            done[dev] = true;
-        }
-    }
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(1024 + stages * slot);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, p) == cudaSuccess && cudaGetLastError() == cudaSuccess
-               ? GEMM_OK
-               : GEMM_ERR_LAUNCH;
+    if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
+        !encode_x(&tmX, L, p.x_rows))
+        return GEMM_ERR_LAUNCH;
+    return launch(kernel, tmW, tmX, p, tiles, kThreads, 1024 + p.stages * slot, stream);
 }
 
-template <int NT>
+template <bool BF16, int NT, int SLOTS, int GROUP>
+int launch_zeros(const W4Launch& L, cudaStream_t stream) {
+    return L.zeros ? launch_one<BF16, NT, SLOTS, GROUP, true>(L, stream)
+                   : launch_one<BF16, NT, SLOTS, GROUP, false>(L, stream);
+}
+
+template <int NT, int SLOTS, int GROUP>
+int launch_type(const W4Launch& L, cudaStream_t stream) {
+    return L.bf16 ? launch_zeros<true, NT, SLOTS, GROUP>(L, stream) : launch_zeros<false, NT, SLOTS, GROUP>(L, stream);
+}
+
+template <int NT, int SLOTS>
 int launch_group(const W4Launch& L, cudaStream_t stream) {
-    if (L.group == 32) return L.bf16 ? launch_one<true, NT, 32>(L, stream) : launch_one<false, NT, 32>(L, stream);
-    if (L.group == 64) return L.bf16 ? launch_one<true, NT, 64>(L, stream) : launch_one<false, NT, 64>(L, stream);
-    return L.bf16 ? launch_one<true, NT, 128>(L, stream) : launch_one<false, NT, 128>(L, stream);
+    if (L.group == 32) return launch_type<NT, SLOTS, 32>(L, stream);
+    if (L.group == 64) return launch_type<NT, SLOTS, 64>(L, stream);
+    return launch_type<NT, SLOTS, 128>(L, stream);
 }
 
 template <typename T>
@@ -557,11 +513,11 @@ void quantize_of(const W4QuantLaunch& L, unsigned grid, cudaStream_t stream) {
 }  // namespace
 
 int w4_launch(const W4Launch& L, cudaStream_t stream) {
-    // One tile of up to 8, 16 or 32 rows of x; more rows are tiles of 32, each
-    // of which reads the weights once more.
-    if (L.M <= 8) return launch_group<1>(L, stream);
-    if (L.M <= 16) return launch_group<2>(L, stream);
-    return launch_group<4>(L, stream);
+    if (L.M == 1) return launch_group<1, 8>(L, stream);
+    if (L.M <= 4) return launch_group<1, 2>(L, stream);
+    if (L.M <= 8) return launch_group<1, 1>(L, stream);
+    if (L.M <= 16) return launch_group<2, 1>(L, stream);
+    return w4_launch_tc(L, stream);
 }
 
 int w4_quantize_launch(const W4QuantLaunch& L, cudaStream_t stream) {

@@ -1,0 +1,294 @@
+// gemv_w4.cuh -- what the two kernels of the 4-bit product share: the unpacking
+// of nibbles, bounded waits, tensor maps and the choice of the K split.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "../../include/quant.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "quant.h"
+
+namespace ssp {
+namespace w4 {
+
+template <typename T>
+__device__ __forceinline__ float f32_of(T v);
+template <>
+__device__ __forceinline__ float f32_of(float v) { return v; }
+template <>
+__device__ __forceinline__ float f32_of(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float f32_of(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T of_f32(float v);
+template <>
+__device__ __forceinline__ __half of_f32(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 of_f32(float v) { return __float2bfloat16_rn(v); }
+
+constexpr int KS = 256;        // K of a stage: one 128-byte swizzle row of nibbles
+constexpr int kMaxStages = 8;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+
+struct Params {
+    int M, N, K;
+    int tiles_m, groups;  // groups of a row
+    int blocks;           // stages of K
+    int split;            // CTAs of a cluster, each with a part of the stages
+    int stages, x_rows;   // ring depth; rows of x in a stage
+    uint32_t idesc;
+    int s_vec, z_vec;     // rows of scales on 16-byte, of zeros on 8-byte boundaries
+    const void* scales;
+    long long lds;
+    const uint8_t* zeros;
+    long long ldz;
+    void* C;
+    long long ldc;
+};
+
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 15u) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// The same for a whole warp: true if the phase completed for every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, wait_for(bar, parity, abort)) != 0;
+}
+
+// Bounded wait without a look at the abort flag.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+}
+
+// (a & mask) | magic in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
+    return r;
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ __nv_bfloat162 b2(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
+template <typename V>
+__device__ __forceinline__ uint32_t u32(V v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+// Eight 4-bit weights less their zero point, as four pairs (k, k + 4), exact in
+// 16 bits.  A nibble under the exponent of 2^7 (bf16: 7 mantissa bits) or 2^10
+// (fp16) reads as 128 + w or 1024 + w, from which 128 + z or 1024 + z is
+// subtracted; an fp16 nibble four places higher reads as 1024 + 16 w, of which
+// a sixteenth less 64 + z is one multiply-add and saves the shift.
+template <bool BF16>
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t zero, uint32_t zero16, uint32_t (&p)[4]) {
+    if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = u32(__hsub2(b2(and_or(w >> (4 * i), 0x000f000fu, 0x43004300u)), b2(zero)));
+    } else {
+        const __half2 sixteenth = h2(0x2c002c00u);  // 1/16
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t v = w >> (8 * i);
+            p[2 * i] = u32(__hsub2(h2(and_or(v, 0x000f000fu, 0x64006400u)), h2(zero)));
+            p[2 * i + 1] = u32(__hfma2(h2(and_or(v, 0x00f000f0u, 0x64006400u)), sixteenth, h2(zero16)));
+        }
+    }
+}
+
+// The zero point as unpack wants it: (128 + z) or (1024 + z) twice, and from
+// that, for fp16, -(64 + z) twice (at 2^6 fp16 has 16 steps a unit).
+template <bool BF16>
+__device__ __forceinline__ uint32_t zero_of(uint32_t z) {
+    return z * 0x00010001u + (BF16 ? 0x43004300u : 0x64006400u);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t zero16_of(uint32_t zero) {
+    return BF16 ? 0u : (zero - 0x64006400u) * 16u + 0xd400d400u;
+}
+
+// The cluster's partial sums of outputs [4 i, 4 i + 4) of a tile, added in
+// rank order, `parts` of them a CTA, `stride` floats apart.
+__device__ __forceinline__ float4 add_partials(uint32_t part_addr, int at, int parts, int stride, int split) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = 0; c < split; ++c) {
+        const uint32_t base = split == 1 ? part_addr : mapa_shared(part_addr, static_cast<uint32_t>(c));
+        for (int k = 0; k < parts; ++k) {
+            const float4 u = ld_cluster_f4(base + 4u * static_cast<uint32_t>(k * stride + at));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+    }
+    return v;
+}
+
+// Four adjacent outputs of a row, those below N.
+template <typename T>
+__device__ __forceinline__ void store4(const Params& p, int m, int n, float4 v) {
+    T* out = static_cast<T*>(p.C) + static_cast<long long>(m) * p.ldc + n;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) out[e] = of_f32<T>(f[e]);
+}
+
+// ---------------------------------------------------------------- host side
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// A row-major matrix in boxes of 128 bytes of a row by box_rows rows, 128-byte
+// swizzled; zeros outside it.
+inline bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
+                 int64_t ld_bytes, int box_cols, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld_bytes)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of a kernel that the current device holds at once, by cluster size
+// 1..8; asked for once a device, with the kernel's shared-memory limit.
+struct Residency {
+    std::mutex mu;
+    bool known[64] = {};
+    int ctas[64][9] = {};
+
+    bool get(const void* kernel, int threads, int smem, int (&out)[9]) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+        std::lock_guard<std::mutex> g(mu);
+        if (!known[dev]) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return false;
+            for (int c = 1; c <= 8; ++c) {
+                cudaLaunchAttribute attr;
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = static_cast<unsigned>(c);
+                attr.val.clusterDim.y = 1;
+                attr.val.clusterDim.z = 1;
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(static_cast<unsigned>(c));
+                cfg.blockDim = dim3(static_cast<unsigned>(threads));
+                cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                int n = 0;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                    cudaGetLastError();
+                    n = 0;
+                }
+                ctas[dev][c] = n * c;
+            }
+            if (ctas[dev][1] <= 0) return false;
+            known[dev] = true;
+        }
+        for (int c = 0; c <= 8; ++c) out[c] = ctas[dev][c];
+        return true;
+    }
+};
+
+// Cut K over 1 to 8 CTAs, a cluster, `least_blocks` stages each at least: the
+// cut with the least time, counted in stages.  CTAs share the SMs evenly, so
+// rounds of resident CTAs count in fractions, but a CTA's start and end (the
+// cluster's barriers among them) cost about as much as eight stages each round
+// (measured with every cut on 4096^2 to 28672 x 8192).
+inline int choose_split(int64_t tiles, int blocks, int least_blocks, const int (&resident)[9]) {
+    int split = 1;
+    double least = 0.0;
+    for (int c = 1; c <= 8 && (c == 1 || blocks / c >= least_blocks); ++c) {
+        if (resident[c] <= 0) continue;
+        const double rounds = static_cast<double>(tiles) * c / resident[c];
+        const double whole = static_cast<double>((tiles * c + resident[c] - 1) / resident[c]);
+        const double work = (rounds < 1.0 ? 1.0 : rounds) * ((blocks + c - 1) / c) + 8.0 * whole;
+        if (c == 1 || work < 0.95 * least) {
+            split = c;
+            least = work;
+        }
+    }
+    return split;
+}
+
+// Parameters that do not depend on the kernel's geometry.
+inline Params params_of(const W4Launch& L) {
+    Params p = {};
+    p.M = static_cast<int>(L.M);
+    p.N = static_cast<int>(L.N);
+    p.K = static_cast<int>(L.K);
+    p.groups = static_cast<int>(L.K / L.group);
+    p.blocks = static_cast<int>((L.K + KS - 1) / KS);
+    p.scales = L.scales;
+    p.lds = L.lds;
+    p.zeros = L.zeros;
+    p.ldz = L.ldz;
+    p.s_vec = reinterpret_cast<uintptr_t>(L.scales) % 16 == 0 && (L.N == 1 || L.lds % 8 == 0);
+    p.z_vec = reinterpret_cast<uintptr_t>(L.zeros) % 8 == 0 && (L.N == 1 || L.ldz % 8 == 0);
+    p.C = L.C;
+    p.ldc = L.ldc;
+    return p;
+}
+
+// Launch with clusters of p.split CTAs, overlapping the previous kernel's end.
+template <typename Kernel>
+int launch(Kernel kernel, const CUtensorMap& tmW, const CUtensorMap& tmX, const Params& p, int64_t tiles, int threads,
+           int smem, cudaStream_t stream) {
+    if (tiles * p.split > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, p) == cudaSuccess && cudaGetLastError() == cudaSuccess
+               ? GEMM_OK
+               : GEMM_ERR_LAUNCH;
+}
+
+}  // namespace w4
+
+// More than 16 rows of x (gemv_w4_tc.cu).
+int w4_launch_tc(const W4Launch& L, cudaStream_t stream);
+
+}  // namespace ssp

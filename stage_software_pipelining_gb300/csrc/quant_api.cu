@@ -118,7 +118,9 @@ int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const v
     if (K > 0 && (!ld_ok(M, ldx, K) || !ld_ok(N, ldw, K / 2) || !ld_ok(N, lds, groups)))
         return GEMM_ERR_ARG;
     if (K > 0 && zeros && !ld_ok(N, ldz, groups)) return GEMM_ERR_ARG;
-    if (M > INT_MAX || N > INT_MAX || K > (1 << 30)) return GEMM_ERR_UNSUPPORTED;
+    if (M > INT_MAX || N > INT_MAX || K > (1 << 26)) return GEMM_ERR_UNSUPPORTED;
+    if (N <= 1) lds = ldz = groups;
+    if (lds > (1 << 22) || (zeros && ldz > (1 << 22))) return GEMM_ERR_UNSUPPORTED;
     if (!aligned(C, 2)) return GEMM_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return ssp::scale_launch(M, N, C, ldc, 1, 0.0f, s);  // 16-bit zeros
