@@ -26,6 +26,7 @@ struct NormLaunch {
     void* q;
     int64_t ldq;
     float* scale;
+    float inv_cols;  // 1/cols, set by norm_launch
 };
 int norm_launch(const NormLaunch& L, cudaStream_t stream);
 

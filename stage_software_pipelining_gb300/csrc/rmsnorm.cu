@@ -18,6 +18,9 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+#include <type_traits>
+
 #include "../../include/quant.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -53,10 +56,59 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// VEC adjacent elements, moved as one access where VEC > 1.
+// VEC adjacent elements of a row as they lie in memory: 16 bytes, or one
+// element where rows do not start on 16-byte boundaries.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
+struct Pack {
+    uint4 u;
+    __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    // Every element the same.
+    __device__ __forceinline__ void fill(float v) {
+        T e[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) e[i] = from_f32<T>(v);
+        u.x = u.y = u.z = u.w = *reinterpret_cast<const uint32_t*>(e);
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[2 * i] = v.x, f[2 * i + 1] = v.y;
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[VEC]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            } else {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <typename T>
+struct Pack<T, 1> {
+    T u;
+    __device__ __forceinline__ void load(const T* p) { u = *p; }
+    __device__ __forceinline__ void store(T* p) const { *p = u; }
+    __device__ __forceinline__ void fill(float v) { u = from_f32<T>(v); }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(u); }
+    __device__ __forceinline__ void set(const float (&f)[1]) { u = from_f32<T>(f[0]); }
 };
 
 template <int VEC>
@@ -93,23 +145,40 @@ __device__ __forceinline__ Stats block_join(Stats s, Stats* buf) {
     const int lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x >> 5);
     if (lane == 0) buf[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = lane < warps ? buf[lane] : Stats{0.0f, 0.0f};
-    return warp_join(s);
+    // The warps' Stats once in every run of `run` lanes (warps rounded up to a
+    // power of two), joined within the run.
+    const int run = 1 << (32 - __clz(warps - 1));
+    const int w = lane & (run - 1);
+    s = w < warps ? buf[w] : Stats{0.0f, 0.0f};
+    for (int o = 1; o < run; o *= 2) {
+        s.ss += __shfl_xor_sync(0xffffffffu, s.ss, o);
+        s.am = max_nan(s.am, __shfl_xor_sync(0xffffffffu, s.am, o));
+    }
+    return s;
 }
 
-// rstd and scale of a row from its Stats.
-__device__ __forceinline__ void row_factors(const NormLaunch& p, Stats s, float& rstd, float& scale) {
-    rstd = p.weight ? rsqrtf(s.ss / fmaxf(static_cast<float>(p.cols), 1.0f) + p.eps) : 1.0f;
-    scale = max_nan(rstd * s.am / kE4m3Max, kScaleMin);
+// rstd, scale and 1/scale of a row from its Stats.  (The reciprocals are within
+// an ulp, and a scale lies in [2^-126, 2^120].)
+struct Factors {
+    float rstd, scale, inv;
+};
+__device__ __forceinline__ Factors row_factors(const NormLaunch& p, Stats s) {
+    Factors f;
+    f.rstd = p.weight ? rsqrtf(fmaf(s.ss, p.inv_cols, p.eps)) : 1.0f;
+    f.scale = max_nan(f.rstd * s.am * (1.0f / kE4m3Max), kScaleMin);
+    asm("rcp.approx.f32 %0, %1;" : "=f"(f.inv) : "f"(f.scale));
+    return f;
 }
 
 // A row in registers: thread t of the row's `threads` holds packs t, t +
 // threads, ..., NCH of them.  WARP: a warp a row, blockDim/32 rows a block;
 // otherwise a block a row.
-constexpr int max_threads(int elements) { return elements <= 16 ? 1024 : 512; }
+// Threads a block may have: what its registers leave room for (x, residual,
+// weight and h of VEC * NCH elements a thread).
+constexpr int max_threads(int size, int vec, int nch) { return (vec == 1 ? 4 : size) * vec * nch <= 32 ? 1024 : 512; }
 
 template <typename T, int VEC, int NCH, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : max_threads(VEC * NCH)) row_kernel(const NormLaunch p) {
+__global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH)) row_kernel(const NormLaunch p) {
     using P = Pack<T, VEC>;
     __shared__ Stats buf[WARP ? 1 : 32];
     griddep_launch_dependents();
@@ -120,80 +189,237 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(VEC * NCH)) row_kerne
                                : static_cast<long long>(blockIdx.x);
     if (WARP && row >= p.rows) return;
     const int packs = static_cast<int>(p.cols) / VEC;
-    const P* x = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + row * p.ldx);
-    const P* r = reinterpret_cast<const P*>(static_cast<const T*>(p.residual) + row * p.ldr);
-    const P* w = static_cast<const P*>(p.weight);
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    const T* r = static_cast<const T*>(p.residual) + row * p.ldr;
+    const T* w = static_cast<const T*>(p.weight);
+    // Every load is on its way before the first value is used.  Absent inputs
+    // are neutral ones: a residual of -0 (x + -0 is x, signs of zero included)
+    // and weights of 1.
     P xv[NCH], rv[NCH], wv[NCH];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        const int i = t + c * threads;
-        if (i < packs) xv[c] = x[i];
-    }
+    for (int c = 0; c < NCH; ++c)
+        if (t + c * threads < packs) xv[c].load(x + (t + c * threads) * VEC);
     if (p.residual) {
 #pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int i = t + c * threads;
-            if (i < packs) rv[c] = r[i];
-        }
+        for (int c = 0; c < NCH; ++c)
+            if (t + c * threads < packs) rv[c].load(r + (t + c * threads) * VEC);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) rv[c].fill(-0.0f);
     }
     if (p.weight) {
 #pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int i = t + c * threads;
-            if (i < packs) wv[c] = w[i];
-        }
+        for (int c = 0; c < NCH; ++c)
+            if (t + c * threads < packs) wv[c].load(w + (t + c * threads) * VEC);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) wv[c].fill(1.0f);
     }
     float h[NCH][VEC];
     Stats s = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
         if (t + c * threads < packs) {
+            float a[VEC], b[VEC], g[VEC];
+            xv[c].get(a);
+            rv[c].get(b);
+            wv[c].get(g);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float v = to_f32(xv[c].v[e]);
-                if (p.residual) v += to_f32(rv[c].v[e]);
+                const float v = a[e] + b[e];
                 h[c][e] = v;
                 s.ss = fmaf(v, v, s.ss);
-                s.am = max_nan(s.am, fabsf(p.weight ? v * to_f32(wv[c].v[e]) : v));
+                s.am = max_nan(s.am, fabsf(v * g[e]));
             }
         }
     }
     s = WARP ? warp_join(s) : block_join(s, buf);
-    float rstd, scale;
-    row_factors(p, s, rstd, scale);
-    if (p.scale && t == 0) p.scale[row] = scale;
-    const float inv = 1.0f / scale;
-    P* ro = reinterpret_cast<P*>(static_cast<T*>(p.residual_out) + row * p.ldro);
-    P* yo = reinterpret_cast<P*>(static_cast<T*>(p.y) + row * p.ldy);
+    const Factors f = row_factors(p, s);
+    if (p.scale && t == 0) p.scale[row] = f.scale;
+    T* ro = static_cast<T*>(p.residual_out) + row * p.ldro;
+    T* yo = static_cast<T*>(p.y) + row * p.ldy;
     uint8_t* q = static_cast<uint8_t*>(p.q) + row * p.ldq;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-        const int i = t + c * threads;
-        if (i < packs) {
+        const int i = (t + c * threads) * VEC;
+        if (t + c * threads < packs) {
             P o;
             if (p.residual_out) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o.v[e] = from_f32<T>(h[c][e]);
-                ro[i] = o;
+                o.set(h[c]);
+                o.store(ro + i);
             }
-            float y[VEC];
+            float g[VEC], y[VEC];
+            wv[c].get(g);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = p.weight ? h[c][e] * rstd * to_f32(wv[c].v[e]) : h[c][e];
+            for (int e = 0; e < VEC; ++e) y[e] = h[c][e] * f.rstd * g[e];
             if (p.y) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) o.v[e] = from_f32<T>(y[e]);
-                yo[i] = o;
+                o.set(y);
+                o.store(yo + i);
             }
             if (p.q) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) y[e] *= inv;
-                store_q<VEC>(q + static_cast<long long>(i) * VEC, y);
+                for (int e = 0; e < VEC; ++e) y[e] *= f.inv;
+                store_q<VEC>(q + i, y);
             }
         }
     }
 }
 
-// A row too long for a block's registers: one pass for its Stats, one that
+// Rows that do not start on 16-byte boundaries (an odd width), or too long for
+// a block's registers: the row lies in shared memory as fp32 on the way.  x, the
+// residual and its sum are moved 16 bytes at a time from the first boundary in
+// the row on, where they agree on it (SAME), the weights, q and an aligned y
+// from the row's first element on; shared memory turns one into the other.
+// Each element of an input is read before any thread writes an output over it.
+struct Staged {
+    int same;   // x, residual, residual_out start alike within 16 bytes, row by row
+    int y_same; // y too
+    int w_vec, q_vec, y_vec;  // on 16-byte (q: VEC-byte) boundaries
+};
+
+template <typename T>
+__global__ void __launch_bounds__(512) staged_kernel(const NormLaunch p, const Staged st) {
+    constexpr int VEC = 16 / sizeof(T);
+    extern __shared__ float hb[];
+    __shared__ Stats buf[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long row = blockIdx.x;
+    const int n = static_cast<int>(p.cols), t = static_cast<int>(threadIdx.x), nt = static_cast<int>(blockDim.x);
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
+    const T* w = static_cast<const T*>(p.weight);
+    T* ro = p.residual_out ? static_cast<T*>(p.residual_out) + row * p.ldro : nullptr;
+    T* yo = p.y ? static_cast<T*>(p.y) + row * p.ldy : nullptr;
+    uint8_t* q = p.q ? static_cast<uint8_t*>(p.q) + row * p.ldq : nullptr;
+    auto at = [](int i) { return i + (i >> 3); };  // no bank conflicts for runs of VEC a lane
+    // Whole packs lie in [head, tail).
+    int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / sizeof(T));
+    if (head > n || !st.same) head = n;
+    const int packs = (n - head) / VEC, tail = head + packs * VEC;
+    float ss = 0.0f;
+    auto take = [&](int i) {
+        float h = to_f32(x[i]);
+        if (r) h += to_f32(r[i]);
+        ss = fmaf(h, h, ss);
+        hb[at(i)] = h;
+        if (ro) ro[i] = from_f32<T>(h);
+    };
+    constexpr int U = 2;  // packs on their way at a time
+    for (int j = t; j < packs; j += U * nt) {
+        Pack<T, VEC> xv[U], rv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = head + (j + u * nt) * VEC;
+            if (j + u * nt < packs) {
+                xv[u].load(x + i);
+                if (r) rv[u].load(r + i);
+                else rv[u].fill(-0.0f);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = head + (j + u * nt) * VEC;
+            if (j + u * nt < packs) {
+                float a[VEC], b[VEC];
+                xv[u].get(a);
+                rv[u].get(b);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    a[e] += b[e];
+                    ss = fmaf(a[e], a[e], ss);
+                    hb[at(i + e)] = a[e];
+                }
+                if (ro) {
+                    xv[u].set(a);
+                    xv[u].store(ro + i);
+                }
+            }
+        }
+    }
+    for (int i = t; i < head; i += nt) take(i);
+    for (int i = tail + t; i < n; i += nt) take(i);
+    __syncthreads();
+    // h and the weights of elements [i, i + VEC), 0 past the row.
+    auto both = [&](int i, float (&h)[VEC], float (&g)[VEC]) {
+        const bool whole = i + VEC <= n;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = i + e < n ? hb[at(i + e)] : 0.0f;
+        Pack<T, VEC> wv;
+        if (!w) {
+            wv.fill(1.0f);
+            wv.get(g);
+        } else if (whole && st.w_vec) {
+            wv.load(w + i);
+            wv.get(g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g[e] = i + e < n ? to_f32(w[i + e]) : 0.0f;
+        }
+    };
+    float am = 0.0f;
+    if (p.scale)
+        for (int i = t * VEC; i < n; i += nt * VEC) {
+            float h[VEC], g[VEC];
+            both(i, h, g);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) am = max_nan(am, fabsf(h[e] * g[e]));
+        }
+    const Factors f = row_factors(p, block_join({ss, am}, buf));
+    if (p.scale && t == 0) p.scale[row] = f.scale;
+    if (!yo && !q) return;
+    const bool y_turned = yo && st.y_same && !st.y_vec;  // y leaves by way of shared memory
+    for (int i = t * VEC; i < n; i += nt * VEC) {
+        float h[VEC], g[VEC];
+        both(i, h, g);
+        const bool whole = i + VEC <= n;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = h[e] * f.rstd * g[e];
+        if (yo) {
+            if (y_turned) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (i + e < n) hb[at(i + e)] = h[e];
+            } else if (whole && st.y_vec) {
+                Pack<T, VEC> o;
+                o.set(h);
+                o.store(yo + i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (i + e < n) yo[i + e] = from_f32<T>(h[e]);
+            }
+        }
+        if (q) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) h[e] *= f.inv;
+            if (whole && st.q_vec) {
+                store_q<VEC>(q + i, h);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float one[1] = {h[e]};
+                    if (i + e < n) store_q<1>(q + i + e, one);
+                }
+            }
+        }
+    }
+    if (!y_turned) return;
+    __syncthreads();
+    for (int j = t; j < packs; j += nt) {
+        const int i = head + j * VEC;
+        float y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y[e] = hb[at(i + e)];
+        Pack<T, VEC> o;
+        o.set(y);
+        o.store(yo + i);
+    }
+    for (int i = t; i < head; i += nt) yo[i] = from_f32<T>(hb[at(i)]);
+    for (int i = tail + t; i < n; i += nt) yo[i] = from_f32<T>(hb[at(i)]);
+}
+
+// A row too long for shared memory as well: one pass for its Stats, one that
 // reads it again and writes.  Every element is read and written by the same
 // thread, so outputs may lie over inputs.
 template <typename T>
@@ -213,57 +439,68 @@ __global__ void __launch_bounds__(1024) wide_kernel(const NormLaunch p) {
         s.am = max_nan(s.am, fabsf(w ? h * to_f32(w[i]) : h));
     }
     s = block_join(s, buf);
-    float rstd, scale;
-    row_factors(p, s, rstd, scale);
-    if (p.scale && threadIdx.x == 0) p.scale[row] = scale;
-    const float inv = 1.0f / scale;
+    const Factors f = row_factors(p, s);
+    if (p.scale && threadIdx.x == 0) p.scale[row] = f.scale;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const float h = to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f);
-        const float y = w ? h * rstd * to_f32(w[i]) : h;
+        const float y = w ? h * f.rstd * to_f32(w[i]) : h;
         if (p.residual_out) static_cast<T*>(p.residual_out)[row * p.ldro + i] = from_f32<T>(h);
         if (p.y) static_cast<T*>(p.y)[row * p.ldy + i] = from_f32<T>(y);
-        const float qv[1] = {y * inv};
+        const float qv[1] = {y * f.inv};
         if (p.q) store_q<1>(static_cast<uint8_t*>(p.q) + row * p.ldq + i, qv);
     }
 }
 
 using Kernel = void (*)(const NormLaunch);
 
-int launch(Kernel k, int64_t grid, int threads, const NormLaunch& L, cudaStream_t stream) {
+template <typename... Args>
+int launch(void (*k)(Args...), int64_t grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, L) == cudaSuccess && cudaGetLastError() == cudaSuccess ? GEMM_OK
+    return cudaLaunchKernelEx(&cfg, k, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess ? GEMM_OK
                                                                                               : GEMM_ERR_LAUNCH;
 }
 
+// Rows whose packs (VEC elements) are whole and aligned.  Few threads with
+// several packs each hold more loads in flight for their registers than many
+// with one, and their reductions cost less: 8191 x 8192 bf16 with q takes 68 us
+// with 256 threads of 4 packs (the bytes at 6.87 TB/s), 77 with 512 of 2 and 85
+// with 1024 of 1.  Where rows are fewer than two an SM, one row's time counts:
+// one pack a thread, as many threads as that takes.  False: not for these rows.
 template <typename T, int VEC>
-int launch_rows(const NormLaunch& L, cudaStream_t stream) {
+bool launch_rows(const NormLaunch& L, cudaStream_t stream, int* status) {
     const int64_t packs = (L.cols + VEC - 1) / VEC;
     if (packs <= 128) {  // a warp a row
-        Kernel k = packs <= 32 ? row_kernel<T, VEC, 1, true>
+        Kernel k = packs <= 32   ? row_kernel<T, VEC, 1, true>
                    : packs <= 64 ? row_kernel<T, VEC, 2, true> : row_kernel<T, VEC, 4, true>;
-        return launch(k, (L.rows + 3) / 4, 128, L, stream);
+        *status = launch(k, (L.rows + 3) / 4, 128, 0, stream, L);
+        return true;
     }
-    // A block a row: as many threads as packs where there are few rows (the
-    // time is one row's), several packs a thread where rows queue for the SMs.
-    constexpr int kMost = VEC == 1 ? 8 : 4;  // 16384 elements a block, 8192 one by one
+    constexpr int kMost = VEC == 1 || sizeof(T) == 4 ? 8 : 4;
     const bool few = L.rows <= 2 * tc_current_device_sms();
-    int nch = few ? 1 : VEC == 1 ? 8 : 4;
-    while (nch <= kMost && packs > static_cast<int64_t>(max_threads(VEC * nch)) * nch) nch *= 2;
-    if (nch > kMost) return launch(wide_kernel<T>, L.rows, 1024, L, stream);
+    // One element at a time is too slow for many long rows (4000 x 5001
+    // bf16: 73 us, staged_kernel 37) but ahead of staged_kernel's two more
+    // passes over shared memory up to about 2500 (4000 x 2001: 20.8 and
+    // 20.6; x 1001: 10.2 and 10.8) and for few rows (100 x 5001: 3.2, 6.4).
+    if (VEC == 1 && !few && packs > 2560) return false;
+    int nch = few ? (VEC == 1 ? 4 : 1) : VEC == 1 ? 8 : 4;
+    while (nch <= kMost && packs > static_cast<int64_t>(max_threads(sizeof(T), VEC, nch)) * nch) nch *= 2;
+    if (nch > kMost) return false;
     Kernel k = nch == 1   ? row_kernel<T, VEC, 1, false>
                : nch == 2 ? row_kernel<T, VEC, 2, false> : row_kernel<T, VEC, 4, false>;
-    if constexpr (VEC == 1)
-        if (nch == 8) k = row_kernel<T, 1, 8, false>;
+    if constexpr (kMost >= 8)
+        if (nch == 8) k = row_kernel<T, VEC, 8, false>;
     const int threads = static_cast<int>(((packs + nch - 1) / nch + 31) / 32 * 32);
-    return launch(k, L.rows, threads, L, stream);
+    *status = launch(k, L.rows, threads, 0, stream, L);
+    return true;
 }
 
 // Whether a matrix's rows all start on `to`-byte boundaries.
@@ -272,20 +509,52 @@ bool rows_on(const void* p, int64_t ld, int64_t rows, int64_t size, uintptr_t to
                   (rows <= 1 || (ld * size) % static_cast<int64_t>(to) == 0));
 }
 
+// Whether two matrices' rows start alike within 16 bytes.
+bool alike(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t size) {
+    return !b || ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) % 16 == 0 &&
+                  (rows <= 1 || (lda - ldb) * size % 16 == 0));
+}
+
 template <typename T>
 int launch_type(const NormLaunch& L, cudaStream_t stream) {
     constexpr int VEC = 16 / sizeof(T);
     constexpr int64_t S = sizeof(T);
+    Staged st;
+    st.w_vec = rows_on(L.weight, 0, 1, S, 16);
+    st.q_vec = rows_on(L.q, L.ldq, L.rows, 1, VEC);
+    st.y_vec = rows_on(L.y, L.ldy, L.rows, S, 16);
+    st.same = alike(L.x, L.ldx, L.residual, L.ldr, L.rows, S) && alike(L.x, L.ldx, L.residual_out, L.ldro, L.rows, S);
+    st.y_same = st.same && alike(L.x, L.ldx, L.y, L.ldy, L.rows, S);
     const bool vec = L.cols % VEC == 0 && rows_on(L.x, L.ldx, L.rows, S, 16) &&
-                     rows_on(L.residual, L.ldr, L.rows, S, 16) && rows_on(L.weight, 0, 1, S, 16) &&
-                     rows_on(L.residual_out, L.ldro, L.rows, S, 16) && rows_on(L.y, L.ldy, L.rows, S, 16) &&
-                     rows_on(L.q, L.ldq, L.rows, 1, VEC);
-    return vec ? launch_rows<T, VEC>(L, stream) : launch_rows<T, 1>(L, stream);
+                     rows_on(L.residual, L.ldr, L.rows, S, 16) && rows_on(L.residual_out, L.ldro, L.rows, S, 16) &&
+                     st.w_vec && st.y_vec && st.q_vec;
+    int status = GEMM_OK;
+    if (vec ? launch_rows<T, VEC>(L, stream, &status) : launch_rows<T, 1>(L, stream, &status)) return status;
+    constexpr int64_t kMostStaged = 45000;
+    if (L.cols > kMostStaged) return launch(wide_kernel<T>, L.rows, 1024, 0, stream, L);
+    const size_t smem = static_cast<size_t>(L.cols + L.cols / 8 + 8) * sizeof(float);
+    {
+        static std::mutex mu;
+        static bool done[64] = {};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GEMM_ERR_CUDA;
+        std::lock_guard<std::mutex> g(mu);
+        if (!done[dev]) {
+            if (cudaFuncSetAttribute(staged_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (kMostStaged + kMostStaged / 8 + 8) * sizeof(float)) != cudaSuccess)
+                return GEMM_ERR_LAUNCH;
+            done[dev] = true;
+        }
+    }
+    const int threads = L.cols >= 6144 || L.rows <= tc_current_device_sms() ? 512 : L.cols >= 1536 ? 256 : 128;
+    return launch(staged_kernel<T>, L.rows, threads, smem, stream, L, st);
 }
 
 }  // namespace
 
-int norm_launch(const NormLaunch& L, cudaStream_t stream) {
+int norm_launch(const NormLaunch& given, cudaStream_t stream) {
+    NormLaunch L = given;
+    L.inv_cols = L.cols > 0 ? static_cast<float>(1.0 / static_cast<double>(L.cols)) : 0.0f;
     if (L.dtype == QUANT_F32) return launch_type<float>(L, stream);
     if (L.dtype == QUANT_F16) return launch_type<__half>(L, stream);
     return launch_type<__nv_bfloat16>(L, stream);
