@@ -43,11 +43,11 @@ namespace {
 constexpr int BK = 128;                 // K of a stage: one 128-byte swizzle row of 8-bit values
 constexpr int UMMA_K = 32;              // K per tcgen05.mma (kind::f8f6f4)
 constexpr int ROW_TILE_BYTES = 128 * BK;  // 128 rows of a stage: 16 KB
-constexpr int NUM_THREADS = 192;        // TMA warp, MMA warp, four epilogue warps
+constexpr int FEW_THREADS = 192;        // TMA warp, MMA warp, four epilogue warps
+constexpr int PAIR_THREADS = 320;       // TMA warp, MMA warp, eight epilogue warps
 constexpr int kMaxSmem = 227 * 1024;
-constexpr int kPairStages = 6;
+constexpr int kPairMaxStages = 6;
 constexpr int kPairBoxes = 2;           // output boxes per epilogue warp
-constexpr int EPI_BOX_BYTES = 4096;     // 32 rows x 128 bytes
 constexpr int ROLE_PRODUCER = 0, ROLE_MMA = 1, ROLE_EPILOGUE = 2;
 
 struct Fp8Params {
@@ -57,7 +57,6 @@ struct Fp8Params {
     int split;     // few-row kernel: CTAs of a cluster, each with a part of K
     int stages;
     uint32_t idesc;
-    int out_bf16;
     void* C;
     long long ldc;
     const float* a_scale;
@@ -115,22 +114,31 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity,
         if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
-    if (bf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&v);
+// Two accumulators times a row's scale and their columns' scales, in 16 bits.
+template <bool BF16>
+__device__ __forceinline__ uint32_t scaled16(uint32_t a, uint32_t b, float2 row, float2 col) {
+    uint64_t v, r, c;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(row.x), "f"(row.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(col.x), "f"(col.y));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(r));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(c));
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+    if constexpr (BF16) {
+        const __nv_bfloat162 o = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&o);
+    } else {
+        const __half2 o = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&o);
     }
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // ---------------------------------------------------------------- many rows
 struct PairCtl {
-    unsigned long long bar[2 * kPairStages + 5];  // full, empty, tmem_full[2], tmem_empty[2], drain
+    unsigned long long bar[2 * kPairMaxStages + 5];  // full, empty, tmem_full[2], tmem_empty[2], drain
     uint32_t tmem_base;
     int abort;
-    int epi_ok[2];  // the epilogue's go/abort decision, by tile parity
-    alignas(16) float b_scale[256];
 };
 
 // Output tile of persistent work item t: groups of group_m tile rows walked
@@ -147,24 +155,27 @@ __device__ __forceinline__ void tile_coords(const Fp8Params& p, int t, int& tm, 
     if (g & 1) tn = p.tiles_n - 1 - tn;
 }
 
-__device__ __forceinline__ void epilogue_bar_sync() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
-
 // A cluster of two CTAs computes a 256 x 256 tile.  CTA rank r stages rows
 // 128r.. of the A tile and weight rows 128r.. of the B tile; both CTAs' copies
 // of a stage complete on the leader's full[s]; the leader issues every MMA and
 // its commits free the stage in both CTAs.  Each CTA's TMEM receives its own
 // 128 rows of C.
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+//
+// S stages of 32 KB and output boxes of BOX_COLS columns share the 227 KB: six
+// stages with boxes of 32 columns, or five with boxes of 64, whose tensor
+// stores of whole 128-byte rows are fewer (see launch_pair).
+template <bool BF16, int S, int BOX_COLS>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    constexpr int S = kPairStages;
+    constexpr int EPI_BOX_BYTES = 32 * BOX_COLS * 2;
     uint8_t* a_ring = smem;
     uint8_t* b_ring = smem + S * ROW_TILE_BYTES;
     uint8_t* epi_ring = b_ring + S * ROW_TILE_BYTES;
-    PairCtl* ctl = reinterpret_cast<PairCtl*>(epi_ring + 4 * kPairBoxes * EPI_BOX_BYTES);
+    PairCtl* ctl = reinterpret_cast<PairCtl*>(epi_ring + 8 * kPairBoxes * EPI_BOX_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank() & 1u;
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 8);  // one arrive per epilogue warp of both CTAs
+            mbar_init(tempty_bar(a), 16);  // one arrive per epilogue warp of both CTAs
         }
         mbar_init(drain_bar, 1);
         ctl->abort = 0;
@@ -286,14 +297,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t off = static_cast<uint32_t>(s * ROW_TILE_BYTES) / 16u;
+                    // One election a stage: electing a lane for every product
+                    // costs about as many clocks (108) as the product (128).
+                    if (elect_one_sync()) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-                        if (elect_one_sync())
+                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
                             umma_f8_pair(d_tmem, a_desc0 + off + 2u * kk, b_desc0 + off + 2u * kk, p.idesc,
                                          (kb | kk) != 0);
-                        __syncwarp();
+                        umma_commit_pair_multicast(empty_bar(s), kPairMask);
                     }
-                    if (elect_one_sync()) umma_commit_pair_multicast(empty_bar(s), kPairMask);
                     __syncwarp();
                     ++it;
                     if (++s == S) {
@@ -315,11 +327,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t tempty_leader0 = mapa_shared(tempty_bar(0), 0u);
-        const uint32_t epi_buf0 = smem_addr(epi_ring) + static_cast<uint32_t>(q * kPairBoxes) * EPI_BOX_BYTES;
-        const bool bf16 = p.out_bf16 != 0;
-        const int et = (warp - 2) * 32 + lane;  // 0..127
+        // Two warps a lane quarter: columns 0..127 and 128..255 of the tile.
+        const int half = (warp - 2) >> 2;
+        const uint32_t buf0 =
+            smem_addr(epi_ring) + static_cast<uint32_t>((warp - 2) * kPairBoxes) * EPI_BOX_BYTES;
+        const bool vec_scales = (reinterpret_cast<uintptr_t>(p.b_scale) & 15u) == 0;
         int lt = 0;
-        uint32_t box = 0;  // boxes sent so far: their ring runs on from tile to tile
+        uint32_t box = 0;  // boxes stored so far: their ring runs on from tile to tile
         for (int t = unit; t < tiles; t += units, ++lt) {
             const int acc = lt & 1;
             int tm, tn;
@@ -327,68 +341,84 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int row_base = tm * 256 + static_cast<int>(rank) * 128 + 32 * q;
             const int col0 = tn * 256;
             const float rs = row_base + lane < p.M ? p.a_scale[row_base + lane] : 0.0f;
-            epilogue_bar_sync();  // the previous tile's column scales are read
-            for (int c = et; c < 256; c += 128)
-                ctl->b_scale[c] = col0 + c < p.N ? p.b_scale[col0 + c] : 0.0f;
-            if (warp == 2 && lane == 0)
-                ctl->epi_ok[lt & 1] = bounded_wait<true>(tfull_bar(acc), static_cast<uint32_t>((lt >> 1) & 1),
-                                                         abort_flag, p.wait_limit_ns, ROLE_EPILOGUE, lt);
-            __syncwarp();
-            epilogue_bar_sync();
-            if (!ctl->epi_ok[lt & 1]) break;
+            // The column scales are read as they are used, the same ones by every
+            // lane: bring their lines closer meanwhile.
+            if (lane < 4) prefetch_l1(p.b_scale + min(col0 + half * 128 + lane * 32, p.N - 1));
+            const bool ok = bounded_wait<true>(tfull_bar(acc), static_cast<uint32_t>((lt >> 1) & 1), abort_flag,
+                                               p.wait_limit_ns, ROLE_EPILOGUE, lt);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                                   static_cast<uint32_t>(acc * 256);
+                                   static_cast<uint32_t>(acc * 256 + half * 128);
+            const float2 rs2 = make_float2(rs, rs);
             if (row_base < p.M) {
-                const int boxes = min(4, (p.N - col0 + 63) / 64);
-                for (int ci = 0; ci < boxes; ++ci) {
+#pragma unroll 1
+                for (int ci = 0; ci < 128 / BOX_COLS; ++ci) {
+                    const int n0 = col0 + half * 128 + ci * BOX_COLS;  // the box's first column
+                    if (n0 >= p.N) break;
+                    const uint32_t buf = buf0 + (box % kPairBoxes) * EPI_BOX_BYTES;
+                    uint32_t r[BOX_COLS];
+#pragma unroll
+                    for (int i = 0; i < BOX_COLS; i += 32)
+                        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(ci * BOX_COLS + i),
+                                           *reinterpret_cast<uint32_t(*)[32]>(&r[i]));
+                    // The store that last used this box has read it.
+                    if (lane == 0) bulk_wait_group_read<kPairBoxes - 1>();
+                    float4 cs[BOX_COLS / 4];
+                    if (vec_scales && n0 + BOX_COLS <= p.N) {
+#pragma unroll
+                        for (int i = 0; i < BOX_COLS / 4; ++i)
+                            cs[i] = __ldg(reinterpret_cast<const float4*>(p.b_scale + n0) + i);
+                    } else {
+                        auto at = [&](int e) { return p.b_scale[min(n0 + e, p.N - 1)]; };
+#pragma unroll
+                        for (int i = 0; i < BOX_COLS / 4; ++i)
+                            cs[i] = make_float4(at(4 * i), at(4 * i + 1), at(4 * i + 2), at(4 * i + 3));
+                    }
+                    tmem_ld_wait();
+                    __syncwarp();
+                    uint4 u[BOX_COLS / 8];
+#pragma unroll
+                    for (int jj = 0; jj < BOX_COLS / 8; ++jj) {
+                        const float4 x = cs[2 * jj], y = cs[2 * jj + 1];
+                        const uint32_t* v = &r[8 * jj];
+                        u[jj] = make_uint4(scaled16<BF16>(v[0], v[1], rs2, make_float2(x.x, x.y)),
+                                           scaled16<BF16>(v[2], v[3], rs2, make_float2(x.z, x.w)),
+                                           scaled16<BF16>(v[4], v[5], rs2, make_float2(y.x, y.y)),
+                                           scaled16<BF16>(v[6], v[7], rs2, make_float2(y.z, y.w)));
+                    }
                     // Tensor stores clip rows past M, and columns past N in
                     // units of 16 bytes: a box with part of such a unit is
                     // written by each thread for its row.
-                    const bool ragged = (p.N & 7) != 0 && col0 + ci * 64 + 64 > p.N;
-                    const uint32_t buf = epi_buf0 + (box % kPairBoxes) * EPI_BOX_BYTES;
-                    // The store that last used this box has read it.
-                    if (lane == 0) bulk_wait_group_read<kPairBoxes - 1>();
-                    __syncwarp();
-                    uint32_t r[64];
-                    tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(ci * 64),
-                                       *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-                    tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(ci * 64 + 32),
-                                       *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-                    tmem_ld_wait();
-                    const float4* cs4 = reinterpret_cast<const float4*>(ctl->b_scale + ci * 64);
+                    if ((p.N & 7) == 0 || n0 + BOX_COLS <= p.N) {
+                        // Chunk j of row r lies at j ^ (r & 7), in 64-byte rows at
+                        // j ^ ((r >> 1) & 3).
+                        const int turn = BOX_COLS == 64 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-                    for (int jj = 0; jj < 8; ++jj) {
-                        const float4 c0 = cs4[2 * jj], c1 = cs4[2 * jj + 1];
-                        const uint32_t* v = &r[8 * jj];
-                        auto f = [&](int e, float cs) { return __uint_as_float(v[e]) * rs * cs; };
-                        const uint4 u = make_uint4(pack16(f(0, c0.x), f(1, c0.y), bf16),
-                                                   pack16(f(2, c0.z), f(3, c0.w), bf16),
-                                                   pack16(f(4, c1.x), f(5, c1.y), bf16),
-                                                   pack16(f(6, c1.z), f(7, c1.w), bf16));
-                        if (!ragged) {
-                            st_shared_v4(buf + lane * 128 + ((jj ^ (lane & 7)) << 4), u);
-                        } else if (row_base + lane < p.M) {
-                            const int n = col0 + ci * 64 + jj * 8;
-                            uint16_t* c = static_cast<uint16_t*>(p.C) +
-                                          static_cast<long long>(row_base + lane) * p.ldc + n;
-                            if (n + 8 <= p.N) {
-                                *reinterpret_cast<uint4*>(c) = u;
+                        for (int jj = 0; jj < BOX_COLS / 8; ++jj)
+                            st_shared_v4(buf + lane * (BOX_COLS * 2) + ((jj ^ turn) << 4), u[jj]);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmC, buf, n0, row_base);
+                            bulk_commit_group();
+                        }
+                        ++box;
+                    } else if (row_base + lane < p.M) {
+                        uint16_t* c = static_cast<uint16_t*>(p.C) +
+                                      static_cast<long long>(row_base + lane) * p.ldc + n0;
+#pragma unroll
+                        for (int jj = 0; jj < BOX_COLS / 8; ++jj) {
+                            const uint32_t w[4] = {u[jj].x, u[jj].y, u[jj].z, u[jj].w};
+                            if (n0 + 8 * jj + 8 <= p.N) {
+                                *reinterpret_cast<uint4*>(c + 8 * jj) = u[jj];
                             } else {
-                                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    if (n + e < p.N) c[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+                                    if (n0 + 8 * jj + e < p.N)
+                                        c[8 * jj + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
                             }
                         }
-                    }
-                    if (ragged) continue;
-                    ++box;
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmC, buf, col0 + ci * 64, row_base);
-                        bulk_commit_group();
                     }
                 }
             }
@@ -408,15 +438,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // ---------------------------------------------------------------- few rows
 constexpr int kFewMaxStages = 12;
+constexpr int kFewTwo = 64;  // widest MT of which two CTAs fit an SM
 struct FewCtl {
     unsigned long long bar[2 * kFewMaxStages + 1];  // full, empty, done
     uint32_t tmem_base;
     int abort;
+    alignas(16) float a_scale[256];
+    alignas(16) float b_scale[128];
 };
 
 // One 128 (weight rows) x MT (rows of A) tile, K blocks [k0, k1) of it.
-template <int MT>
-__global__ void __launch_bounds__(NUM_THREADS)
+template <int MT, bool BF16>
+__global__ void __launch_bounds__(FEW_THREADS)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const Fp8Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -515,6 +548,10 @@ __global__ void __launch_bounds__(NUM_THREADS)
         drain_wait(done_bar, 0u, p.wait_limit_ns);
         tc_fence_after();
         tc_fence_before();
+    } else {
+        const int et = static_cast<int>(threadIdx.x) - 64;  // 0..127
+        ctl->b_scale[et] = n0 + et < p.N ? p.b_scale[n0 + et] : 0.0f;
+        for (int m = et; m < MT; m += 128) ctl->a_scale[m] = m0 + m < p.M ? p.a_scale[m0 + m] : 0.0f;
     }
     __syncthreads();  // the accumulator is complete and the ring is read
     tc_fence_after();
@@ -527,49 +564,65 @@ __global__ void __launch_bounds__(NUM_THREADS)
             }
         __syncthreads();
     }
+    const int rows = min(MT, p.M - m0);
     if (warp >= 2) {
         const int q = warp & 3;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         const int n = 32 * q + lane;
-#pragma unroll
+        const float bs = ctl->b_scale[n];
+        uint16_t* out = static_cast<uint16_t*>(p.C) + static_cast<long long>(m0) * p.ldc + n0 + n;
+#pragma unroll 2
         for (int c = 0; c < MT; c += 16) {
+            if (c >= rows) break;
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
             tmem_ld_wait();
+            if (split > 1) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(c + i) * 128 + n] = __uint_as_float(r[i]);
+                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + n] = __uint_as_float(r[i]);
+            } else {  // this thread's output column, 64 bytes of a row a warp
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 as = *reinterpret_cast<const float4*>(ctl->a_scale + c + i);
+                    const uint32_t lo = scaled16<BF16>(r[i], r[i + 1], make_float2(as.x, as.y), make_float2(bs, bs));
+                    const uint32_t hi = scaled16<BF16>(r[i + 2], r[i + 3], make_float2(as.z, as.w), make_float2(bs, bs));
+                    const uint32_t w[2] = {lo, hi};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + i + e < rows && n0 + n < p.N)
+                            out[static_cast<long long>(c + i + e) * p.ldc] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+                }
+            }
         }
         tc_fence_before();
     }
-    if (split > 1) cluster_sync_all();
-    else __syncthreads();
-    // CTA `rank` adds the cluster's partials of its share of the rows, in rank
-    // order, and writes them: a warp takes 128 outputs of one row.
-    {
-        const int rows = min(MT, p.M - m0);
-        const int r0 = rows * rank / split, r1 = rows * (rank + 1) / split;
-        const int n = n0 + 4 * lane;
-        float bs[4];
+    if (split > 1) {
+        cluster_sync_all();
+        // CTA `rank` adds the cluster's partials of its share of the outputs, in
+        // rank order, four adjacent ones a thread.
+        const int total = rows * 32;
+        const uint32_t part_addr = smem_addr(part);
+        for (int i = total * rank / split + static_cast<int>(threadIdx.x); i < total * (rank + 1) / split;
+             i += FEW_THREADS) {
+            const int m = i >> 5, col = (i & 31) * 4, n = n0 + col;
+            float4 u[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) bs[e] = n + e < p.N ? p.b_scale[n + e] : 0.0f;
-        const uint32_t part_addr = smem_addr(part) + 16u * lane;
-        for (int m = r0 + warp; m < r1; m += NUM_THREADS / 32) {
-            const uint32_t at = part_addr + 512u * m;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (split == 1) {
-                v = *reinterpret_cast<const float4*>(part + m * 128 + 4 * lane);
-            } else {
-                for (int c = 0; c < split; ++c) {
-                    const float4 u = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
-                    v.x += u.x;
-                    v.y += u.y;
-                    v.z += u.z;
-                    v.w += u.w;
+            for (int c = 0; c < 8; ++c)
+                if (c < split) u[c] = ld_cluster_f4(mapa_shared(part_addr + 16u * i, static_cast<uint32_t>(c)));
+            float4 v = u[0];
+#pragma unroll
+            for (int c = 1; c < 8; ++c)
+                if (c < split) {
+                    v.x += u[c].x;
+                    v.y += u[c].y;
+                    v.z += u[c].z;
+                    v.w += u[c].w;
                 }
-            }
-            const float as = p.a_scale[m0 + m];
-            const uint32_t lo = pack16(v.x * as * bs[0], v.y * as * bs[1], p.out_bf16);
-            const uint32_t hi = pack16(v.z * as * bs[2], v.w * as * bs[3], p.out_bf16);
+            const float as = ctl->a_scale[m];
+            const float4 bs = *reinterpret_cast<const float4*>(ctl->b_scale + col);
+            const float2 as2 = make_float2(as, as);
+            const uint32_t lo = scaled16<BF16>(__float_as_uint(v.x), __float_as_uint(v.y), as2, make_float2(bs.x, bs.y));
+            const uint32_t hi = scaled16<BF16>(__float_as_uint(v.z), __float_as_uint(v.w), as2, make_float2(bs.z, bs.w));
             uint16_t* c = static_cast<uint16_t*>(p.C) + static_cast<long long>(m0 + m) * p.ldc + n;
             if (n + 4 <= p.N) {
                 *reinterpret_cast<uint2*>(c) = make_uint2(lo, hi);
@@ -604,9 +657,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // Tensor map over a row-major matrix of `rows` x `cols` elements with row
-// pitch ld_bytes: boxes of 128 bytes x box_rows, 128-byte swizzle, zero fill.
-bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t cols,
-                 uint64_t ld_bytes, uint32_t box_cols, uint32_t box_rows) {
+// pitch ld_bytes: boxes of box_cols x box_rows, swizzled, zero fill.
+bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base,
+                 uint64_t rows, uint64_t cols, uint64_t ld_bytes, uint32_t box_cols, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {cols, rows};
@@ -614,12 +667,13 @@ bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, u
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_e4m3(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
-    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rows, cols, ld, BK, box_rows);
+    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, base, rows, cols, ld, BK,
+                       box_rows);
 }
 
 // Instruction descriptor (kind::f8f6f4): D fp32 (bit 4), A and B e4m3 (0 at
@@ -631,7 +685,7 @@ uint32_t instruction(int m, int n) {
 // The kernels' dynamic shared-memory limit is set once a device.
 bool allow_smem(const void* kernel, int slot) {
     static std::mutex mu;
-    static bool done[64][8] = {};
+    static bool done[64][16] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> g(mu);
@@ -644,7 +698,7 @@ bool allow_smem(const void* kernel, int slot) {
 struct Config {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    Config(int64_t grid, int cluster, size_t smem, cudaStream_t stream) {
+    Config(int64_t grid, int cluster, int threads, size_t smem, cudaStream_t stream) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -652,7 +706,7 @@ struct Config {
         attr[1].val.clusterDim.y = 1;
         attr[1].val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(grid));
-        cfg.blockDim = dim3(NUM_THREADS);
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cfg.attrs = attr;
@@ -660,17 +714,18 @@ struct Config {
     }
 };
 
-int resident_pairs() {
+// CTA pairs that are resident at once (the pair kernel's instances alike).
+int resident_pairs(const void* kernel) {
     static std::mutex mu;
     static int n[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     std::lock_guard<std::mutex> g(mu);
     if (n[dev] == 0) {
-        Config c(2, 2, kMaxSmem, nullptr);
+        Config c(2, 2, PAIR_THREADS, kMaxSmem, nullptr);
         c.cfg.attrs = &c.attr[1];  // the cluster alone
         c.cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n[dev], fp8_pair_kernel, &c.cfg) != cudaSuccess) n[dev] = 0;
+        if (cudaOccupancyMaxActiveClusters(&n[dev], kernel, &c.cfg) != cudaSuccess) n[dev] = 0;
     }
     return n[dev];
 }
@@ -685,7 +740,6 @@ Fp8Params params_of(const Fp8Launch& L) {
     p.N = static_cast<int>(L.N);
     p.K = static_cast<int>(L.K);
     p.k_blocks = static_cast<int>((L.K + BK - 1) / BK);
-    p.out_bf16 = L.out_bf16;
     p.C = L.C;
     p.ldc = L.ldc;
     p.a_scale = L.a_scale;
@@ -696,7 +750,8 @@ Fp8Params params_of(const Fp8Launch& L) {
     return p;
 }
 
-int launch_pair(const Fp8Launch& L, cudaStream_t stream) {
+template <bool BF16, int S, int BOX_COLS>
+int launch_pair_as(const Fp8Launch& L, int slot, cudaStream_t stream) {
     Fp8Params p = params_of(L);
     p.tiles_m = static_cast<int>((L.M + 255) / 256);
     p.tiles_n = static_cast<int>((L.N + 255) / 256);
@@ -706,63 +761,148 @@ int launch_pair(const Fp8Launch& L, cudaStream_t stream) {
     // L2 while the group walks its columns.
     const int64_t g = (32ll << 20) / (256 * L.K);
     p.group_m = static_cast<int>(g < 8 ? 8 : g > 16 ? 16 : g);
-    p.stages = kPairStages;
+    p.stages = S;
     p.idesc = instruction(256, 256);
     CUtensorMap tmA, tmB, tmC;
     if (!encode_e4m3(&tmA, L.A, L.M, L.K, L.lda, 128) || !encode_e4m3(&tmB, L.B, L.N, L.K, L.ldb, 128) ||
-        !encode_rows(&tmC, L.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, L.C,
-                     L.M, L.N, L.ldc * 2, 64, 32))
+        !encode_rows(&tmC, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     BOX_COLS == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, L.C, L.M, L.N, L.ldc * 2,
+                     BOX_COLS, 32))
         return GEMM_ERR_LAUNCH;
-    if (!allow_smem(reinterpret_cast<const void*>(fp8_pair_kernel), 0)) return GEMM_ERR_LAUNCH;
-    const int units = resident_pairs();
+    auto kernel = fp8_pair_kernel<BF16, S, BOX_COLS>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
+    const int units = resident_pairs(reinterpret_cast<const void*>(kernel));
     if (units <= 0) return GEMM_ERR_LAUNCH;
-    static_assert(1024 + 2 * kPairStages * ROW_TILE_BYTES + 4 * kPairBoxes * EPI_BOX_BYTES + sizeof(PairCtl) <=
-                      kMaxSmem,
+    static_assert(1024 + 2 * S * ROW_TILE_BYTES + 8 * kPairBoxes * 64 * BOX_COLS + sizeof(PairCtl) <= kMaxSmem,
                   "the pair kernel's shared memory");
-    Config c(2 * (tiles < units ? tiles : units), 2, kMaxSmem, stream);
-    return finish(cudaLaunchKernelEx(&c.cfg, fp8_pair_kernel, tmA, tmB, tmC, p));
+    Config c(2 * (tiles < units ? tiles : units), 2, PAIR_THREADS, kMaxSmem, stream);
+    return finish(cudaLaunchKernelEx(&c.cfg, kernel, tmA, tmB, tmC, p));
+}
+
+int launch_pair(const Fp8Launch& L, cudaStream_t stream) {
+    // A short K ends in an epilogue sooner than a ring can run ahead: wider
+    // boxes.  3000 x 5001 x 300: 17.7 us with five stages and 64 columns, 22.5
+    // with six and 32; 2048^3 10.0 and 10.2; 4096^3 45.0 and 43.0;
+    // 8191 x 28672 x 4096 509 and 496.
+    if (L.K <= 2048)
+        return L.out_bf16 ? launch_pair_as<true, 5, 64>(L, 0, stream) : launch_pair_as<false, 5, 64>(L, 1, stream);
+    return L.out_bf16 ? launch_pair_as<true, 6, 32>(L, 12, stream) : launch_pair_as<false, 6, 32>(L, 13, stream);
 }
 
 template <int MT>
-int launch_few(const Fp8Launch& L, int slot, cudaStream_t stream) {
+int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t stream) {
     Fp8Params p = params_of(L);
     constexpr int STAGE = ROW_TILE_BYTES + MT * BK;
-    // Two CTAs an SM where a ring of four stages and the partials fit twice.
-    constexpr bool kTwo = MT <= 64;
-    constexpr int kBudget = (kTwo ? 112 : 226) * 1024;
-    constexpr int kStages = (kBudget - 1024 - static_cast<int>(sizeof(FewCtl))) / STAGE;
-    static_assert(kStages * STAGE >= MT * 128 * 4, "the partials lie over the ring");
-    p.stages = kStages < kFewMaxStages ? kStages : kFewMaxStages;
     p.tiles_m = static_cast<int>((L.M + MT - 1) / MT);
     p.tiles_n = static_cast<int>((L.N + 127) / 128);
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    const int sms = tc_current_device_sms();
-    if (sms <= 0) return GEMM_ERR_CUDA;
-    // Cut K over up to 8 CTAs while the grid stays within what is resident
-    // at once and every CTA keeps four K blocks.
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms * (kTwo ? 2 : 1) && p.k_blocks / (2 * split) >= 4) split *= 2;
     p.split = split;
     if (tiles * split > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
+    // Two CTAs an SM with half of shared memory each, or a ring as deep as one
+    // CTA's room.
+    const int budget = (two ? 112 : 226) * 1024;
+    const int stages = (budget - 1024 - static_cast<int>(sizeof(FewCtl))) / STAGE;
+    constexpr bool kTwo = MT <= kFewTwo;
+    static_assert((112 * 1024 - 1024 - static_cast<int>(sizeof(FewCtl))) / STAGE * STAGE >= (kTwo ? MT * 512 : 0) &&
+                      4 * STAGE >= MT * 512,
+                  "the partials lie over the ring");
+    p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
     p.idesc = instruction(128, MT);
     CUtensorMap tmW, tmX;
     if (!encode_e4m3(&tmW, L.B, L.N, L.K, L.ldb, 128) || !encode_e4m3(&tmX, L.A, L.M, L.K, L.lda, MT))
         return GEMM_ERR_LAUNCH;
-    auto kernel = fp8_few_kernel<MT>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
-    Config c(tiles * split, split, 1024 + static_cast<size_t>(p.stages) * STAGE + sizeof(FewCtl), stream);
+    auto kernel = L.out_bf16 ? fp8_few_kernel<MT, true> : fp8_few_kernel<MT, false>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 2 * slot + L.out_bf16)) return GEMM_ERR_LAUNCH;
+    Config c(tiles * split, split, FEW_THREADS, 1024 + static_cast<size_t>(p.stages) * STAGE + sizeof(FewCtl), stream);
     return finish(cudaLaunchKernelEx(&c.cfg, kernel, tmW, tmX, p));
+}
+
+// Which kernel, tile and cut of K: the one with the least time by a model whose
+// constants (microseconds) were fitted to every choice measured on 32 shapes of
+// 1 to 3000 rows, 128 to 28672 columns and 256 to 8192 of K.  Its choices are
+// 2.6 % slower than the best one of each shape on average, 16 % at most
+// (1 x 8192 x 8192: 13.8 us for 13.2; 4 x 2048 x 8192: 6.0 for 6.0;
+// 600 x 300 x 8192: 8.0 for 8.0, in CTA pairs 21.7; 512 x 8192 x 8192: pairs
+// 25.7, few-row tiles 35.7).
+//   * few rows: a round of resident CTAs takes each one's K blocks and an
+//     epilogue that grows with MT, twice where two share an SM; a cut K adds the
+//     partials' way through distributed shared memory, and rounds of clusters
+//     after the first wait for whole clusters' room.
+//   * pairs: a round takes its K blocks at the tensor pipe's rate.
+struct Choice {
+    int mt = 0;  // 0: the pair kernel
+    int split = 1;
+    bool two = false;  // two CTAs an SM
+};
+
+// CTAs (one an SM) that the current device holds at once, by cluster size 1..8.
+bool resident_ctas(int (&out)[9]) {
+    static std::mutex mu;
+    static bool known[64] = {};
+    static int n[64][9] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const void* kernel = reinterpret_cast<const void*>(fp8_few_kernel<128, true>);
+    if (!allow_smem(kernel, 9)) return false;
+    std::lock_guard<std::mutex> g(mu);
+    if (!known[dev]) {
+        for (int c = 1; c <= 8; ++c) {
+            Config cfg(c, c, FEW_THREADS, 200 * 1024, nullptr);
+            cfg.cfg.attrs = &cfg.attr[1];  // the cluster alone
+            cfg.cfg.numAttrs = 1;
+            int k = 0;
+            if (cudaOccupancyMaxActiveClusters(&k, kernel, &cfg.cfg) != cudaSuccess) {
+                cudaGetLastError();
+                k = 0;
+            }
+            n[dev][c] = k * c;
+        }
+        if (n[dev][1] <= 0) return false;
+        known[dev] = true;
+    }
+    for (int c = 0; c <= 8; ++c) out[c] = n[dev][c];
+    return true;
+}
+
+bool choose(const Fp8Launch& L, Choice* best) {
+    int resident[9];
+    if (!resident_ctas(resident)) return false;
+    const int64_t kb = (L.K + BK - 1) / BK;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t pairs = up(L.M, 256) * up(L.N, 256);
+    double least = 4.3 + static_cast<double>(up(pairs, resident[2] > 1 ? resident[2] / 2 : 1)) * (0.29 * kb + 1.32);
+    for (int mt = 16; mt <= 256 && (mt == 16 || mt < 2 * L.M); mt *= 2) {
+        const int64_t tiles = up(L.M, mt) * up(L.N, 128);
+        for (int c = 1; c <= 8 && c <= kb; ++c) {
+            if (resident[c] <= 0) continue;
+            const int64_t ctas = tiles * c;
+            const bool two = mt <= kFewTwo && ctas > resident[c];
+            const double rounds = static_cast<double>(up(ctas, resident[c] * (two ? 2 : 1)));
+            const double shared = two ? 2.0 : 1.0;
+            const double us = 3.0 + rounds * shared * (up(kb, c) * (0.18 + 0.0009 * mt) + 0.02 * mt) +
+                              (c > 1 ? 0.01 + 0.0009 * mt + 0.23 * (rounds - 1.0) * c : 0.0);
+            if (us < least) {
+                least = us;
+                *best = {mt, c, two};
+            }
+        }
+    }
+    return true;
 }
 
 }  // namespace
 
 int fp8_launch(const Fp8Launch& L, cudaStream_t stream) {
-    if (L.M <= 16) return launch_few<16>(L, 1, stream);
-    if (L.M <= 32) return launch_few<32>(L, 2, stream);
-    if (L.M <= 64) return launch_few<64>(L, 3, stream);
-    if (L.M <= 128) return launch_few<128>(L, 4, stream);
-    if (L.M <= 256) return launch_few<256>(L, 5, stream);
-    return launch_pair(L, stream);
+    Choice c;
+    if (!choose(L, &c)) return GEMM_ERR_CUDA;
+    switch (c.mt) {
+        case 16: return launch_few<16>(L, 1, c.split, c.two, stream);
+        case 32: return launch_few<32>(L, 2, c.split, c.two, stream);
+        case 64: return launch_few<64>(L, 3, c.split, c.two, stream);
+        case 128: return launch_few<128>(L, 4, c.split, c.two, stream);
+        case 256: return launch_few<256>(L, 5, c.split, c.two, stream);
+        default: return launch_pair(L, stream);
+    }
 }
 
 int fp8_read_and_clear_status(GemmDeviceStatus* out) {

@@ -358,6 +358,10 @@ __device__ __forceinline__ void cluster_sync_all() {
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // L2 policy: keep the lines of the following accesses in L2 in preference
 // to others (fraction 1.0 of the accesses).
 __device__ __forceinline__ uint64_t l2_policy_evict_last() {

@@ -210,8 +210,10 @@ def fp8_case(M, N, K, dtype, seed=20):
     return C.view
 
 
-FP8_SHAPES = [(300, 700, 8), (2000, 900, 512), (1300, 2600, 300), (1, 1, 1), (1, 64, 128), (1, 4096, 512), (2, 130, 33), (8, 256, 1000), (15, 17, 129), (16, 384, 2048),
-              (17, 100, 256), (33, 1000, 640), (48, 2048, 512), (64, 129, 127), (65, 512, 384), (100, 260, 512),
+FP8_SHAPES = [(600, 300, 2048), (2000, 400, 1024), (400, 2000, 1500), (1, 40000, 256), (40, 40000, 300),
+              (90, 20000, 130), (300, 700, 8), (2000, 900, 512), (1300, 2600, 300), (1, 1, 1), (1, 64, 128),
+              (1, 4096, 512), (2, 130, 33), (8, 256, 1000), (15, 17, 129), (16, 384, 2048), (17, 100, 256),
+              (33, 1000, 640), (48, 2048, 512), (64, 129, 127), (65, 512, 384), (100, 260, 512),
               (128, 128, 128), (129, 129, 129), (200, 520, 192), (255, 777, 1040), (256, 256, 2048),
               (300, 4096, 256), (513, 1025, 257), (1000, 1504, 1000), (2048, 512, 64), (1, 3, 2000)]
 
@@ -264,7 +266,7 @@ def test_gemm_fp8_stuck_pipeline_is_reported(M, N, K):
     W, sb = fp8_rows(rand(43, N, K))
     C = torch.empty(M, (N + 7) // 8 * 8, dtype=BF16, device="cuda")[:, :N]
     try:
-        G.debug_set(wait_limit_ns=50_000_000, withhold_arrive=1)
+        G.debug_set(wait_limit_ns=50_000_000, withhold_arrive=0)
         with pytest.raises(G.GemmError, match="TIMEOUT"):
             Q.gemm_fp8(A, W.t(), C, sa, sb, checked=True)
     finally:
