@@ -16,7 +16,7 @@
  * Memory, streams and errors are gemm.h's: all pointers are device pointers
  * owned by the caller, no pointer is kept after a call, nothing is allocated,
  * `stream` is a cudaStream_t (NULL = the legacy default stream), every entry
- * point but gemm_fp8_checked enqueues its work and returns without
+ * point but the two that end in _checked enqueues its work and returns without
  * synchronising, and every entry point gives a gemm_status_t.  Argument checks are made on the host before
  * anything is enqueued.  Leading dimensions are in elements (bytes for the
  * packed 4-bit weights) and may exceed the row length; a single row's leading
@@ -125,6 +125,11 @@ int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
 int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
             int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
             int group, void* C, int64_t ldc, int dtype, void* stream);
+
+/* gemv_w4_checked -- gemv_w4 as gemm_fp8_checked is gemm_fp8. */
+int gemv_w4_checked(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
+                    int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
+                    int group, void* C, int64_t ldc, int dtype, void* stream);
 
 /*
  * quantize_w4 -- a weight matrix (N x K, row-major, any quant_type_t) in the

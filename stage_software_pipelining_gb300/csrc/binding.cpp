@@ -202,7 +202,7 @@ int gemm_fp8_(PyObject* const* a) {
     return gemm_fp8(M, N, K, RA.p, RA.ld, RB.p, RB.ld, RC.p, RC.ld, sa, sb, code, stream);
 }
 
-// x, W, scales, C, zeros, stream
+// x, W, scales, C, zeros, stream, checked
 int gemv_w4_(PyObject* const* a) {
     const Tensor& x = matrix(a[0], "x");
     const Tensor& W = matrix(a[1], "W");
@@ -217,7 +217,15 @@ int gemv_w4_(PyObject* const* a) {
     const Rows C = rows_of(*tensor(a[3], "C"), "C", dt, M, N, x);
     const Rows Z = rows_or_none(a[4], "zeros", at::kByte, N, groups, x);
     void* stream = stream_of(a[5], x);
+    const int checked = PyObject_IsTrue(a[6]);
     const c10::cuda::CUDAGuard guard(x.device());
+    if (checked) {
+        int st;
+        Py_BEGIN_ALLOW_THREADS
+        st = gemv_w4_checked(M, N, K, X.p, X.ld, RW.p, RW.ld, S.p, S.ld, Z.p, Z.ld, group, C.p, C.ld, code, stream);
+        Py_END_ALLOW_THREADS
+        return st;
+    }
     return gemv_w4(M, N, K, X.p, X.ld, RW.p, RW.ld, S.p, S.ld, Z.p, Z.ld, group, C.p, C.ld, code, stream);
 }
 
@@ -256,7 +264,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define ENTRY(name, args) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<name##_, args>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(add_rmsnorm, 9), ENTRY(quantize_fp8, 4), ENTRY(gemm_fp8, 7), ENTRY(gemv_w4, 6),
+PyMethodDef methods[] = {ENTRY(add_rmsnorm, 9), ENTRY(quantize_fp8, 4), ENTRY(gemm_fp8, 7), ENTRY(gemv_w4, 7),
                          ENTRY(quantize_w4, 5), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_quant", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -137,10 +137,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             int s = 0;
             uint32_t ph = 0;
             for (int kb = k0; kb < k1; ++kb, ++issued) {
-                if (!wait_for(empty_bar(s), ph ^ 1u, abort_flag)) break;
-                mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(W_BYTES + x_bytes));
-                tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
-                tma_load_3d(smem_addr(x_ring + s * x_slot), &tmX, full_bar(s), 0, m0, kb * (KS / 32));
+                if (!wait_for(empty_bar(s), ph ^ 1u, abort_flag, p.wait_limit_ns)) break;
+                if (!(issued == p.withhold && blockIdx.x == 0)) {
+                    mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(W_BYTES + x_bytes));
+                    tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
+                    tma_load_3d(smem_addr(x_ring + s * x_slot), &tmX, full_bar(s), 0, m0, kb * (KS / 32));
+                }
                 if (++s == S) {
                     s = 0;
                     ph ^= 1u;
@@ -152,8 +154,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (*abort_flag) {
             // Copies that nobody waited for land before the ring is reused.
             if (lane == 0)
-                for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j)
-                    drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1));
+                for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j) {
+                    if (j == p.withhold && blockIdx.x == 0) continue;
+                    drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1), p.wait_limit_ns);
+                }
             __syncthreads();
         }
     } else {
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if constexpr (ZEROS && SLOTS != 8) zero[u][i] = zero_of<BF16>(zv[u][i]);
-            if (!wait_for(full_bar(s), ph, abort_flag)) break;
+            if (!warp_wait(full_bar(s), ph, abort_flag, p.wait_limit_ns)) break;
             if constexpr (SLOTS != 8) fetch_scales(kb + WK);
             fetch_zeros(kb + WK);
             const uint32_t w_at = w_row + static_cast<uint32_t>(s * W_BYTES);
@@ -518,6 +522,15 @@ int w4_launch(const W4Launch& L, cudaStream_t stream) {
     if (L.M <= 8) return launch_group<1, 1>(L, stream);
     if (L.M <= 16) return launch_group<2, 1>(L, stream);
     return w4_launch_tc(L, stream);
+}
+
+int w4_read_and_clear_status(GemmDeviceStatus* out) {
+    GemmDeviceStatus tc;
+    int st = w4::read_and_clear_status(out);
+    if (st != GEMM_OK) return st;
+    st = w4_tc_read_and_clear_status(&tc);
+    if (out->code == 0) *out = tc;
+    return st;
 }
 
 int w4_quantize_launch(const W4QuantLaunch& L, cudaStream_t stream) {

@@ -34,7 +34,9 @@ __device__ __forceinline__ __nv_bfloat16 of_f32(float v) { return __float2bfloat
 
 constexpr int KS = 256;        // K of a stage: one 128-byte swizzle row of nibbles
 constexpr int kMaxStages = 8;
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+
+// Written by a wait that ran out; one a source file.
+static __device__ GemmDeviceStatus g_status;
 
 struct Params {
     int M, N, K;
@@ -50,16 +52,26 @@ struct Params {
     long long ldz;
     void* C;
     long long ldc;
+    unsigned long long wait_limit_ns;
+    int withhold;         // block 0 leaves out this stage's copies (test hook), -1: none
 };
 
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+// Wait for the phase of `bar` with parity `parity`; false after limit_ns or
+// once another warp has raised the abort flag.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort,
+                                         unsigned long long limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((n & 15u) == 0) {
             if (*abort) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (globaltimer_ns() - t0 > limit_ns) {
+                if (atomicCAS(&g_status.code, 0, GEMM_ERR_TIMEOUT) == 0) {
+                    g_status.block = blockIdx.x;
+                    g_status.role = static_cast<int>(threadIdx.x >> 5);  // the warp
+                    __threadfence();
+                }
                 *abort = 1;
                 return false;
             }
@@ -68,15 +80,16 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 }
 
 // The same for a whole warp: true if the phase completed for every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait_for(bar, parity, abort)) != 0;
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          unsigned long long limit_ns) {
+    return __all_sync(0xffffffffu, wait_for(bar, parity, abort, limit_ns)) != 0;
 }
 
 // Bounded wait without a look at the abort flag.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
     const unsigned long long t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+        if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
 // (a & mask) | magic in one instruction.
@@ -259,6 +272,9 @@ inline Params params_of(const W4Launch& L) {
     p.z_vec = reinterpret_cast<uintptr_t>(L.zeros) % 8 == 0 && (L.N == 1 || L.ldz % 8 == 0);
     p.C = L.C;
     p.ldc = L.ldc;
+    const DebugHooks d = debug_hooks();
+    p.wait_limit_ns = static_cast<unsigned long long>(d.wait_limit_ns);
+    p.withhold = d.withhold_arrive;
     return p;
 }
 
@@ -286,9 +302,18 @@ int launch(Kernel kernel, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
                : GEMM_ERR_LAUNCH;
 }
 
+// The file's status word, read and reset (synchronous).
+inline int read_and_clear_status(GemmDeviceStatus* out) {
+    const GemmDeviceStatus zero = {0, 0, 0, 0};
+    if (cudaMemcpyFromSymbol(out, g_status, sizeof(GemmDeviceStatus)) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (cudaMemcpyToSymbol(g_status, &zero, sizeof(GemmDeviceStatus)) != cudaSuccess) return GEMM_ERR_CUDA;
+    return GEMM_OK;
+}
+
 }  // namespace w4
 
 // More than 16 rows of x (gemv_w4_tc.cu).
 int w4_launch_tc(const W4Launch& L, cudaStream_t stream);
+int w4_tc_read_and_clear_status(GemmDeviceStatus* out);
 
 }  // namespace ssp

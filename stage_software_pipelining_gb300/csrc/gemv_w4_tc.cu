@@ -128,13 +128,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             int s = 0;
             uint32_t ph = 0;
             for (int kb = k0; kb < k1; ++kb, ++issued) {
-                if (!wait_for(empty_bar(s), ph ^ 1u, abort_flag)) break;
-                mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(W_BYTES + (KS / 64) * p.x_rows * 128));
-                tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
+                if (!wait_for(empty_bar(s), ph ^ 1u, abort_flag, p.wait_limit_ns)) break;
+                if (!(issued == p.withhold && blockIdx.x == 0)) {
+                    mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(W_BYTES + (KS / 64) * p.x_rows * 128));
+                    tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
 #pragma unroll
-                for (int a = 0; a < KS / 64; ++a)
-                    tma_load_2d(smem_addr(x_ring + s * X_BYTES + a * ATOM), &tmX, full_bar(s), kb * KS + a * 64,
-                                m0);
+                    for (int a = 0; a < KS / 64; ++a)
+                        tma_load_2d(smem_addr(x_ring + s * X_BYTES + a * ATOM), &tmX, full_bar(s), kb * KS + a * 64,
+                                    m0);
+                }
                 if (++s == S) {
                     s = 0;
                     ph ^= 1u;
@@ -147,11 +149,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t ph = 0;
         bool ok = true;
         for (int kb = k0; ok && kb < k1; ++kb) {
-            if (!warp_wait(full_bar(s), ph, abort_flag)) break;
+            if (!warp_wait(full_bar(s), ph, abort_flag, p.wait_limit_ns)) break;
             const uint64_t x_desc = smem_desc(smem_addr(x_ring + s * X_BYTES));
             for (int ch = 0; ch < CPS; ++ch, ++i) {
                 const int b = i % NB;
-                if (!warp_wait(afull_bar(b), static_cast<uint32_t>(i / NB) & 1u, abort_flag)) {
+                if (!warp_wait(afull_bar(b), static_cast<uint32_t>(i / NB) & 1u, abort_flag, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // Every product this warp issued ends before TMEM is freed.
         if (elect_one_sync()) umma_commit(drain_bar);
         __syncwarp();
-        drain_wait(drain_bar, 0u);
+        drain_wait(drain_bar, 0u, p.wait_limit_ns);
         tc_fence_after();
         tc_fence_before();
     } else {
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // Adds chunk i's sums, scaled; false after an abort.
         auto add_chunk = [&](int i, const float (&scale)[SUB]) -> bool {
             const int b = i % NB;
-            if (!warp_wait(done_bar(b), static_cast<uint32_t>(i / NB) & 1u, abort_flag)) return false;
+            if (!warp_wait(done_bar(b), static_cast<uint32_t>(i / NB) & 1u, abort_flag, p.wait_limit_ns)) return false;
             tc_fence_after();
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         int i = 0;
         for (; i < chunks; ++i) {
             const int ch = i % CPS, b = i % NB;
-            if (ch == 0 && !(ok = warp_wait(full_bar(s), ph, abort_flag))) break;
+            if (ch == 0 && !(ok = warp_wait(full_bar(s), ph, abort_flag, p.wait_limit_ns))) break;
             const int gi = g0 + i * SUB;
             if (gi / 8 != octet) {  // at most one octet on: a chunk has up to four groups
                 octet = gi / 8;
@@ -324,8 +326,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (*abort_flag) {
         // Copies that nobody waited for land before the ring is reused.
         if (threadIdx.x == 0)
-            for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j)
-                drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1));
+            for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j) {
+                if (j == p.withhold && blockIdx.x == 0) continue;
+                drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1), p.wait_limit_ns);
+            }
         __syncthreads();
     }
     if (warp >= 2) {
@@ -394,5 +398,7 @@ int w4_launch_tc(const W4Launch& L, cudaStream_t stream) {
     if (L.group == 64) return launch_group<64>(L, stream);
     return launch_group<128>(L, stream);
 }
+
+int w4_tc_read_and_clear_status(GemmDeviceStatus* out) { return w4::read_and_clear_status(out); }
 
 }  // namespace ssp

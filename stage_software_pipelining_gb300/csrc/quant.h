@@ -7,6 +7,8 @@
 
 namespace ssp {
 
+struct GemmDeviceStatus;
+
 // One row-wise pass: the residual's addition, the norm and the 8-bit rows
 // (rmsnorm.cu).  Null pointers are inputs that are absent and outputs that
 // are not wanted; weight == nullptr: no norm (y = h).
@@ -44,7 +46,6 @@ struct Fp8Launch {
     int out_bf16;  // 0 fp16, 1 bf16
 };
 int fp8_launch(const Fp8Launch& L, cudaStream_t stream);
-struct GemmDeviceStatus;
 // The fp8 kernels' device status word, read and reset (synchronous).
 int fp8_read_and_clear_status(GemmDeviceStatus* out);
 
@@ -65,6 +66,7 @@ struct W4Launch {
     int bf16;  // 0 fp16, 1 bf16
 };
 int w4_launch(const W4Launch& L, cudaStream_t stream);
+int w4_read_and_clear_status(GemmDeviceStatus* out);
 
 struct W4QuantLaunch {
     int64_t N, K;

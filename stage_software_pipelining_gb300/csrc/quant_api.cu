@@ -43,6 +43,15 @@ int norm_checked(ssp::NormLaunch L, void* stream) {
     return ssp::norm_launch(L, static_cast<cudaStream_t>(stream));
 }
 
+// After a launch: wait for the stream and look at the kernels' status word.
+int checked(int (*status)(ssp::GemmDeviceStatus*), void* stream) {
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
+    ssp::GemmDeviceStatus ds;
+    const int st = status(&ds);
+    if (st != GEMM_OK) return st;
+    return ds.code != 0 ? GEMM_ERR_TIMEOUT : GEMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -95,13 +104,8 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
 int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                      int64_t ldb, void* C, int64_t ldc, const float* a_scale, const float* b_scale,
                      int dtype, void* stream) {
-    int st = gemm_fp8(M, N, K, A, lda, B, ldb, C, ldc, a_scale, b_scale, dtype, stream);
-    if (st != GEMM_OK) return st;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
-    ssp::GemmDeviceStatus ds;
-    st = ssp::fp8_read_and_clear_status(&ds);
-    if (st != GEMM_OK) return st;
-    return ds.code != 0 ? GEMM_ERR_TIMEOUT : GEMM_OK;
+    const int st = gemm_fp8(M, N, K, A, lda, B, ldb, C, ldc, a_scale, b_scale, dtype, stream);
+    return st != GEMM_OK ? st : checked(ssp::fp8_read_and_clear_status, stream);
 }
 
 int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
@@ -133,6 +137,13 @@ int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const v
                            static_cast<const uint8_t*>(zeros), ldz, group, C, ldc,
                            dtype == QUANT_BF16},
                           s);
+}
+
+int gemv_w4_checked(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
+                    int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
+                    int group, void* C, int64_t ldc, int dtype, void* stream) {
+    const int st = gemv_w4(M, N, K, x, ldx, W, ldw, scales, lds, zeros, ldz, group, C, ldc, dtype, stream);
+    return st != GEMM_OK ? st : checked(ssp::w4_read_and_clear_status, stream);
 }
 
 int quantize_w4(int64_t N, int64_t K, const void* w, int64_t ld, int dtype, int group, void* W,

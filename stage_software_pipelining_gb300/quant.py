@@ -35,7 +35,8 @@ GROUPS = (32, 64, 128)          # K per scale of the 4-bit weights
 E4M3_MAX = 448.0                # largest e4m3 value
 
 # Every extern "C" symbol include/quant.h declares.
-EXPORTS = ("add_rmsnorm", "quantize_fp8", "gemm_fp8", "gemm_fp8_checked", "gemv_w4", "quantize_w4")
+EXPORTS = ("add_rmsnorm", "quantize_fp8", "gemm_fp8", "gemm_fp8_checked", "gemv_w4",
+           "gemv_w4_checked", "quantize_w4")
 
 _lock = threading.Lock()
 _lib = None
@@ -58,6 +59,7 @@ def load_library():
             lib.gemm_fp8_checked.argtypes = lib.gemm_fp8.argtypes
             lib.gemv_w4.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, i32, p, i64,
                                     i32, p]
+            lib.gemv_w4_checked.argtypes = lib.gemv_w4.argtypes
             lib.quantize_w4.argtypes = [i64, i64, p, i64, i32, i32, p, i64, p, i64, i32, p, i64, p]
             for name in EXPORTS:
                 getattr(lib, name).restype = i32
@@ -137,16 +139,17 @@ def gemm_fp8(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, a_scale: torch.T
 
 
 def gemv_w4(x: torch.Tensor, W: torch.Tensor, scales: torch.Tensor, C: torch.Tensor,
-            zeros: torch.Tensor | None = None, *,
-            stream: torch.cuda.Stream | None = None) -> torch.Tensor:
-    """C = x @ ((w - zeros) * scales)^T with 4-bit weights w (libgemm.so gemv_w4).
+            zeros: torch.Tensor | None = None, *, stream: torch.cuda.Stream | None = None,
+            checked: bool = False) -> torch.Tensor:
+    """C = x @ ((w - zeros) * scales)^T with 4-bit weights w (libgemm.so gemv_w4,
+    or gemv_w4_checked, which synchronises and reports a wait that ran out).
 
     x: M x K fp16 or bf16; W: N x K/2 uint8, the even k in the low four bits;
     scales: N x K/group of x's type, group 32, 64 or 128; zeros: N x K/group
     uint8 (None: 8 everywhere); C: M x N of x's type.  x and W start on
     16-byte boundaries and so do their rows.  Returns C.
     """
-    st = (_ext or load_binding()).gemv_w4(x, W, scales, C, zeros, stream)
+    st = (_ext or load_binding()).gemv_w4(x, W, scales, C, zeros, stream, checked)
     if st:
         raise GemmError(st, "gemv_w4")
     return C

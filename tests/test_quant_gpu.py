@@ -363,6 +363,25 @@ def test_gemv_w4_fp16_range():
     assert torch.allclose(C.double(), torch.full_like(C, exact).double(), rtol=2.0 ** -11)
 
 
+@pytest.mark.parametrize("M", [1, 3, 7, 12, 20])
+def test_gemv_w4_stuck_pipeline_is_reported(M):
+    K, N = 2048, 200
+    g = torch.Generator().manual_seed(61)
+    x = torch.randn(M, K, generator=g).to(BF16).cuda()
+    W = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8).cuda()
+    s = (torch.rand(N, K // 64, generator=g) * 0.01).to(BF16).cuda()
+    C = torch.empty(M, N, dtype=BF16, device="cuda")
+    try:
+        G.debug_set(wait_limit_ns=50_000_000, withhold_arrive=0)
+        with pytest.raises(G.GemmError, match="TIMEOUT"):
+            Q.gemv_w4(x, W, s, C, checked=True)
+    finally:
+        G.debug_set()
+    Q.gemv_w4(x, W, s, C, checked=True)
+    ref, absb = R.gemv_w4(x, W, s, None, 64)
+    R.check_rounded(C, ref, 2.0 ** -22, R.W4_REL * absb, "after a timeout")
+
+
 def test_gemv_w4_empty():
     C = torch.full((2, 8), 3.0, dtype=BF16, device="cuda")
     Q.gemv_w4(torch.empty(2, 0, dtype=BF16, device="cuda"), torch.empty(8, 0, dtype=torch.uint8, device="cuda"),
