@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 
 // ---------------------------------------------------------------- few rows
 constexpr int kFewMaxStages = 12;
-constexpr int kFewTwo = 64;  // widest MT of which two CTAs fit an SM
+constexpr int kFewTwo = 64;   // widest MT of which two CTAs fit an SM
+constexpr int kFewPush = 32;  // widest MT with room of its own for the cluster's partials
 struct FewCtl {
     unsigned long long bar[2 * kFewMaxStages + 1];  // full, empty, done
     uint32_t tmem_base;
@@ -446,6 +447,7 @@ struct FewCtl {
     alignas(16) float a_scale[256];
     alignas(16) float b_scale[128];
 };
+static_assert(sizeof(FewCtl) % 16 == 0, "pushed partials follow");
 
 // One 128 (weight rows) x MT (rows of A) tile, K blocks [k0, k1) of it.
 template <int MT, bool BF16>
@@ -461,7 +463,13 @@ __global__ void __launch_bounds__(FEW_THREADS)
     uint8_t* w_ring = smem;
     uint8_t* x_ring = smem + S * ROW_TILE_BYTES;
     FewCtl* ctl = reinterpret_cast<FewCtl*>(x_ring + S * X_BYTES);
-    float* part = reinterpret_cast<float*>(smem);  // [MT][128], over the ring once it is read
+    // Partials of a cut K.  PUSH: every CTA writes its share of each output to
+    // the CTA that owns the output, in room of its own; a row's 32 quads (four
+    // outputs) are dealt to the CTAs in runs.  Else they lie over the ring once
+    // it is read and are fetched, with a second barrier until they have been.
+    constexpr bool PUSH = MT <= kFewPush;
+    float* part = reinterpret_cast<float*>(smem);  // [MT][128]
+    const uint32_t recv = smem_addr(ctl + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = p.split;
@@ -493,6 +501,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
         tc_fence_before();
     }
     __syncthreads();
+    if (PUSH && split > 1) cluster_arrive_relaxed();  // this CTA has started: its shared memory may be written to
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
     griddep_launch_dependents();
@@ -565,19 +574,32 @@ __global__ void __launch_bounds__(FEW_THREADS)
         __syncthreads();
     }
     const int rows = min(MT, p.M - m0);
+    const int most = (32 + split - 1) / split;  // quads of an owner
+    auto first = [&](int r) { return (32 * r + split - 1) / split; };
+    if (PUSH && split > 1) cluster_wait();  // every CTA has started
     if (warp >= 2) {
         const int q = warp & 3;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         const int n = 32 * q + lane;
         const float bs = ctl->b_scale[n];
         uint16_t* out = static_cast<uint16_t*>(p.C) + static_cast<long long>(m0) * p.ldc + n0 + n;
+        const int owner = (n >> 2) * split >> 5;
+        const uint32_t push = PUSH && split > 1 ? mapa_shared(recv, static_cast<uint32_t>(owner)) +
+                                                      16u * static_cast<uint32_t>(rank * rows * most + (n >> 2) - first(owner)) +
+                                                      4u * (n & 3)
+                                                : 0u;
 #pragma unroll 2
         for (int c = 0; c < MT; c += 16) {
             if (c >= rows) break;
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
             tmem_ld_wait();
-            if (split > 1) {
+            if (PUSH && split > 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < rows)
+                        st_cluster_f32(push + 16u * static_cast<uint32_t>((c + i) * most), __uint_as_float(r[i]));
+            } else if (split > 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) part[(c + i) * 128 + n] = __uint_as_float(r[i]);
             } else {  // this thread's output column, 64 bytes of a row a warp
@@ -597,18 +619,22 @@ __global__ void __launch_bounds__(FEW_THREADS)
         tc_fence_before();
     }
     if (split > 1) {
+        __syncwarp();
         cluster_sync_all();
-        // CTA `rank` adds the cluster's partials of its share of the outputs, in
-        // rank order, four adjacent ones a thread.
-        const int total = rows * 32;
+        // CTA `rank` adds the partials of its outputs in rank order, four
+        // adjacent ones a thread.
+        const int d0 = PUSH ? first(rank) : 0, count = PUSH ? first(rank + 1) - d0 : 32;
+        const int i0 = PUSH ? 0 : rows * 32 * rank / split, i1 = PUSH ? rows * count : rows * 32 * (rank + 1) / split;
         const uint32_t part_addr = smem_addr(part);
-        for (int i = total * rank / split + static_cast<int>(threadIdx.x); i < total * (rank + 1) / split;
-             i += FEW_THREADS) {
-            const int m = i >> 5, col = (i & 31) * 4, n = n0 + col;
+        for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += FEW_THREADS) {
+            const int m = i / count, d = d0 + i % count, n = n0 + 4 * d;
             float4 u[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (c < split) u[c] = ld_cluster_f4(mapa_shared(part_addr + 16u * i, static_cast<uint32_t>(c)));
+                if (c < split)
+                    u[c] = ld_cluster_f4(PUSH ? mapa_shared(recv + 16u * static_cast<uint32_t>((c * rows + m) * most + d - d0),
+                                                            static_cast<uint32_t>(rank))
+                                              : mapa_shared(part_addr + 16u * i, static_cast<uint32_t>(c)));
             float4 v = u[0];
 #pragma unroll
             for (int c = 1; c < 8; ++c)
@@ -619,7 +645,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
                     v.w += u[c].w;
                 }
             const float as = ctl->a_scale[m];
-            const float4 bs = *reinterpret_cast<const float4*>(ctl->b_scale + col);
+            const float4 bs = *reinterpret_cast<const float4*>(ctl->b_scale + 4 * d);
             const float2 as2 = make_float2(as, as);
             const uint32_t lo = scaled16<BF16>(__float_as_uint(v.x), __float_as_uint(v.y), as2, make_float2(bs.x, bs.y));
             const uint32_t hi = scaled16<BF16>(__float_as_uint(v.z), __float_as_uint(v.w), as2, make_float2(bs.z, bs.w));
@@ -633,7 +659,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
             }
         }
     }
-    if (split > 1) cluster_sync_all();  // the peers have read this CTA's partials
+    if (!PUSH && split > 1) cluster_sync_all();  // the peers have read this CTA's partials
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
@@ -801,11 +827,10 @@ int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t s
     // Two CTAs an SM with half of shared memory each, or a ring as deep as one
     // CTA's room.
     const int budget = (two ? 112 : 226) * 1024;
-    const int stages = (budget - 1024 - static_cast<int>(sizeof(FewCtl))) / STAGE;
-    constexpr bool kTwo = MT <= kFewTwo;
-    static_assert((112 * 1024 - 1024 - static_cast<int>(sizeof(FewCtl))) / STAGE * STAGE >= (kTwo ? MT * 512 : 0) &&
-                      4 * STAGE >= MT * 512,
-                  "the partials lie over the ring");
+    // Room for pushed partials: ceil(32/c) quads of a row from each of c CTAs.
+    const int recv = MT <= kFewPush && split > 1 ? static_cast<int>(L.M < MT ? L.M : MT) * (32 + split) * 16 : 0;
+    const int stages = (budget - 1024 - static_cast<int>(sizeof(FewCtl)) - recv) / STAGE;
+    static_assert(4 * STAGE >= MT * 512, "other partials lie over the ring");
     p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
     p.idesc = instruction(128, MT);
     CUtensorMap tmW, tmX;
@@ -813,7 +838,7 @@ int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t s
         return GEMM_ERR_LAUNCH;
     auto kernel = L.out_bf16 ? fp8_few_kernel<MT, true> : fp8_few_kernel<MT, false>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), 2 * slot + L.out_bf16)) return GEMM_ERR_LAUNCH;
-    Config c(tiles * split, split, FEW_THREADS, 1024 + static_cast<size_t>(p.stages) * STAGE + sizeof(FewCtl), stream);
+    Config c(tiles * split, split, FEW_THREADS, 1024 + static_cast<size_t>(p.stages) * STAGE + sizeof(FewCtl) + recv, stream);
     return finish(cudaLaunchKernelEx(&c.cfg, kernel, tmW, tmX, p));
 }
 

@@ -66,6 +66,8 @@ constexpr int kThreads = 32 * (CW + 1);
 constexpr int kBudget = 100 * 1024; // dynamic shared memory
 constexpr int W_BYTES = R * KS / 2;
 constexpr int PITCH = R + 4;        // of a partial's rows: no bank conflicts when written
+constexpr int QUADS = R / 4;        // of a row's outputs
+constexpr int kRecvRow = (QUADS + 8) * 16;  // bytes for a row's partials: at most ceil(QUADS/c) from each of c <= 8
 
 // SLOTS: one row of x (SLOTS = 8) or up to four (2) leave columns of the
 // 16 x 8 x 16 product empty.  They hold other groups: column `slot * 8/SLOTS +
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int x_slot = (x_bytes + 127) & ~127;
     uint8_t* x_ring = smem + S * W_BYTES;
     float* part = reinterpret_cast<float*>(smem);  // over the ring once it is read
+    const uint32_t recv = smem_addr(x_ring + S * x_slot);  // the cluster's partials of this CTA's outputs
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = p.split;
@@ -128,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (SLOTS > 1 && threadIdx.x < 32) no_x[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
+    if (split > 1) cluster_arrive_relaxed();  // this CTA has started: its shared memory may be written to
     griddep_launch_dependents();
     griddep_wait();
 
@@ -399,16 +403,47 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
     }
-    if (split > 1) cluster_sync_all();
-    else __syncthreads();
-    // CTA `rank` adds the cluster's partials of its share of the outputs, in
-    // order, four adjacent ones a thread.
-    const int total = min(MT, p.M - m0) * (R / 4);
-    for (int i = total * rank / split + static_cast<int>(threadIdx.x); i < total * (rank + 1) / split; i += kThreads) {
-        const int m = i / (R / 4), col = i % (R / 4) * 4;
-        store4<T>(p, m0 + m, n0 + col, add_partials(smem_addr(part), m * PITCH + col, WK, MT * PITCH, split));
+    __syncthreads();
+    // Sums over the groups of warps, four adjacent outputs a thread.
+    const int rows = min(MT, p.M - m0);
+    const float4* part4 = reinterpret_cast<const float4*>(part);
+    auto own = [&](int i) {
+        const int at = (i / QUADS) * (PITCH / 4) + i % QUADS;
+        float4 v = part4[at];
+#pragma unroll
+        for (int k = 1; k < WK; ++k) add4(v, part4[k * MT * (PITCH / 4) + at]);
+        return v;
+    };
+    if (split == 1) {
+        for (int i = static_cast<int>(threadIdx.x); i < rows * QUADS; i += kThreads)
+            store4<T>(p, m0 + i / QUADS, n0 + i % QUADS * 4, own(i));
+        return;
     }
-    if (split > 1) cluster_sync_all();  // the peers have read this CTA's partials
+    // Quad d of a row belongs to CTA d * split / QUADS, to whose shared memory
+    // every CTA of the cluster writes its share; the owner adds them in rank
+    // order.  (Written by their makers, they need no second barrier to outlive
+    // their readers.)
+    const int most = (QUADS + split - 1) / split;  // quads of an owner
+    auto first = [&](int r) { return (QUADS * r + split - 1) / split; };
+    cluster_wait();  // every CTA has started
+    for (int i = static_cast<int>(threadIdx.x); i < rows * QUADS; i += kThreads) {
+        const int m = i / QUADS, d = i % QUADS, owner = d * split / QUADS;
+        st_cluster_f4(mapa_shared(recv, static_cast<uint32_t>(owner)) +
+                          16u * static_cast<uint32_t>((rank * rows + m) * most + d - first(owner)),
+                      own(i));
+    }
+    __syncwarp();
+    cluster_sync_all();
+    const int d0 = first(rank), count = first(rank + 1) - d0;
+    for (int i = static_cast<int>(threadIdx.x); i < rows * count; i += kThreads) {
+        const int m = i / count, d = i % count;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int r = 0; r < split; ++r) {
+            const uint4 u = ld_shared_v4(recv + 16u * static_cast<uint32_t>((r * rows + m) * most + d));
+            add4(v, make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)));
+        }
+        store4<T>(p, m0 + m, n0 + 4 * (d0 + d), v);
+    }
 }
 
 // Eight weights (one 32-bit word) a thread, group/8 threads a group.
@@ -473,9 +508,9 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     p.tiles_m = 1;
     p.x_rows = static_cast<int>(L.M);
     const int slot = W_BYTES + ((p.x_rows * KS * 2 + 127) & ~127);
-    const int stages = (kBudget - 1024) / slot;
+    const int stages = (kBudget - 1024 - p.x_rows * kRecvRow) / slot;
     p.stages = stages < kMaxStages ? stages : kMaxStages;
-    static_assert(WK * 8 * NT * PITCH * 4 <= 5 * W_BYTES && 5 * (W_BYTES + 8 * NT * KS * 2) <= kBudget - 1024,
+    static_assert(WK * 8 * NT * PITCH * 4 <= 5 * W_BYTES && 5 * (W_BYTES + 8 * NT * KS * 2) + 8 * NT * kRecvRow <= kBudget - 1024,
                   "the partials lie over the ring, which has five stages at least");
     auto kernel = w4_kernel<BF16, NT, SLOTS, GROUP, ZEROS>;
     static Residency res;
@@ -487,7 +522,7 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
         !encode_x(&tmX, L, p.x_rows))
         return GEMM_ERR_LAUNCH;
-    return launch(kernel, tmW, tmX, p, tiles, kThreads, 1024 + p.stages * slot, stream);
+    return launch(kernel, tmW, tmX, p, tiles, kThreads, 1024 + p.stages * slot + p.x_rows * kRecvRow, stream);
 }
 
 template <bool BF16, int NT, int SLOTS, int GROUP>

@@ -137,21 +137,11 @@ __device__ __forceinline__ uint32_t zero16_of(uint32_t zero) {
     return BF16 ? 0u : (zero - 0x64006400u) * 16u + 0xd400d400u;
 }
 
-// The cluster's partial sums of outputs [4 i, 4 i + 4) of a tile, added in
-// rank order, `parts` of them a CTA, `stride` floats apart.
-__device__ __forceinline__ float4 add_partials(uint32_t part_addr, int at, int parts, int stride, int split) {
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = 0; c < split; ++c) {
-        const uint32_t base = split == 1 ? part_addr : mapa_shared(part_addr, static_cast<uint32_t>(c));
-        for (int k = 0; k < parts; ++k) {
-            const float4 u = ld_cluster_f4(base + 4u * static_cast<uint32_t>(k * stride + at));
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
-        }
-    }
-    return v;
+__device__ __forceinline__ void add4(float4& v, float4 u) {
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
 }
 
 // Four adjacent outputs of a row, those below N.

@@ -342,9 +342,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     // CTA `rank` adds the cluster's partials of its share of the outputs, in
     // order, four adjacent ones a thread.
     const int total = min(NC, p.M - m0) * (R / 4);
+    const uint32_t part_addr = smem_addr(part);
     for (int i = total * rank / split + static_cast<int>(threadIdx.x); i < total * (rank + 1) / split; i += kThreads) {
-        const int m = i / (R / 4), col = i % (R / 4) * 4;
-        store4<T>(p, m0 + m, n0 + col, add_partials(smem_addr(part), m * R + col, 1, 0, split));
+        float4 u[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < split)
+                u[c] = split == 1 ? *reinterpret_cast<const float4*>(part + 4 * i)
+                                  : ld_cluster_f4(mapa_shared(part_addr + 16u * i, static_cast<uint32_t>(c)));
+#pragma unroll
+        for (int c = 1; c < 8; ++c)
+            if (c < split) add4(u[0], u[c]);
+        store4<T>(p, m0 + i / (R / 4), n0 + i % (R / 4) * 4, u[0]);
     }
     if (split > 1) cluster_sync_all();  // the peers have read this CTA's partials
     else __syncthreads();
