@@ -21,7 +21,8 @@
  * anything is enqueued.  Leading dimensions are in elements (bytes for the
  * packed 4-bit weights) and may exceed the row length; a single row's leading
  * dimension is not looked at.  Outputs must not overlap inputs or each other
- * unless an entry point says so.  Every result is the same, bit for bit, from
+ * unless an entry point says so.  Rows, columns, M, N and K above 2^31 - 4097
+ * are GEMM_ERR_UNSUPPORTED.  Every result is the same, bit for bit, from
  * call to call.
  */
 #ifndef SSP_QUANT_H
@@ -90,7 +91,6 @@ int quantize_fp8(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dty
  * Alignment (GEMM_ERR_ALIGN otherwise): A, B and C start on 16-byte
  * boundaries and lda, ldb and ldc*2 are multiples of 16; a_scale and b_scale
  * are 4-byte aligned.
- * M, N and K above 2^31 - 1 are GEMM_ERR_UNSUPPORTED.
  */
 int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
              int64_t ldb, void* C, int64_t ldc, const float* a_scale, const float* b_scale,
@@ -119,8 +119,7 @@ int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  * are fp32.  K = 0 gives C = 0.
  * Alignment (GEMM_ERR_ALIGN otherwise): x and W start on 16-byte boundaries,
  * ldx*2 and ldw are multiples of 16; the others are aligned to their element.
- * M and N above 2^31 - 1, K above 2^26 and lds or ldz above 2^22 are
- * GEMM_ERR_UNSUPPORTED.
+ * K above 2^26 and lds or ldz above 2^22 are GEMM_ERR_UNSUPPORTED.
  */
 int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
             int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,

@@ -11,6 +11,9 @@
 
 namespace {
 
+// Largest rows and columns: indices of a last tile's end stay 32-bit integers.
+constexpr int64_t kMost = INT_MAX - 4096;
+
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 bool known(int dtype) { return dtype >= QUANT_F32 && dtype <= QUANT_BF16; }
@@ -27,7 +30,7 @@ int norm_checked(ssp::NormLaunch L, void* stream) {
     }
     if (!(L.eps >= 0.0f)) return GEMM_ERR_ARG;
     if (L.rows == 0) return GEMM_OK;
-    if (L.rows > INT_MAX || L.cols > INT_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (L.rows > kMost || L.cols > kMost) return GEMM_ERR_UNSUPPORTED;
     if (L.cols == 0 && L.scale == nullptr) return GEMM_OK;
     if (L.cols > 0 && L.x == nullptr) return GEMM_ERR_ARG;
     const uintptr_t es = static_cast<uintptr_t>(size_of(L.dtype));
@@ -87,7 +90,7 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
     if (K > 0 && (A == nullptr || B == nullptr || a_scale == nullptr || b_scale == nullptr))
         return GEMM_ERR_ARG;
     if (K > 0 && (!ld_ok(M, lda, K) || !ld_ok(N, ldb, K))) return GEMM_ERR_ARG;
-    if (M > INT_MAX || N > INT_MAX || K > INT_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (M > kMost || N > kMost || K > kMost) return GEMM_ERR_UNSUPPORTED;
     // A single row's leading dimension is never used, but the tensor maps
     // hold one: the row length on a 16-byte boundary.
     if (M <= 1) lda = (K + 15) / 16 * 16;
@@ -122,7 +125,7 @@ int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const v
     if (K > 0 && (!ld_ok(M, ldx, K) || !ld_ok(N, ldw, K / 2) || !ld_ok(N, lds, groups)))
         return GEMM_ERR_ARG;
     if (K > 0 && zeros && !ld_ok(N, ldz, groups)) return GEMM_ERR_ARG;
-    if (M > INT_MAX || N > INT_MAX || K > (1 << 26)) return GEMM_ERR_UNSUPPORTED;
+    if (M > kMost || N > kMost || K > (1 << 26)) return GEMM_ERR_UNSUPPORTED;
     if (N <= 1) lds = ldz = groups;
     if (lds > (1 << 22) || (zeros && ldz > (1 << 22))) return GEMM_ERR_UNSUPPORTED;
     if (!aligned(C, 2)) return GEMM_ERR_ALIGN;
@@ -158,7 +161,7 @@ int quantize_w4(int64_t N, int64_t K, const void* w, int64_t ld, int dtype, int 
     if (w == nullptr || W == nullptr || scales == nullptr) return GEMM_ERR_ARG;
     if (!ld_ok(N, ld, K) || !ld_ok(N, ldw, K / 2) || !ld_ok(N, lds, groups)) return GEMM_ERR_ARG;
     if (zeros && !ld_ok(N, ldz, groups)) return GEMM_ERR_ARG;
-    if (N > INT_MAX || K > (1 << 30)) return GEMM_ERR_UNSUPPORTED;
+    if (N > kMost || K > (1 << 26)) return GEMM_ERR_UNSUPPORTED;
     if (!aligned(w, static_cast<uintptr_t>(size_of(dtype))) || !aligned(scales, 2)) return GEMM_ERR_ALIGN;
     return ssp::w4_quantize_launch({N, K, w, ld, dtype, group, static_cast<uint8_t*>(W), ldw, scales,
                                     lds, scale_dtype == QUANT_BF16, static_cast<uint8_t*>(zeros), ldz},
