@@ -519,7 +519,7 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     const int64_t tiles = (L.N + R - 1) / R;
     p.split = choose_split(tiles, p.blocks, 2, resident);
     CUtensorMap tmW, tmX;
-    if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
+    if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
         !encode_x(&tmX, L, p.x_rows))
         return GEMM_ERR_LAUNCH;
     return launch(kernel, tmW, tmX, p, tiles, kThreads, 1024 + p.stages * slot + p.x_rows * kRecvRow, stream);

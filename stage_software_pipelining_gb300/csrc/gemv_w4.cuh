@@ -85,6 +85,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, wait_for(bar, parity, abort, limit_ns)) != 0;
 }
 
+// A warp's wait in two halves: a look at the barrier, whose latency (some 150
+// clocks) passes under what stands between, and the wait for those that it
+// found incomplete.
+struct Wait {
+    uint32_t bar, parity;
+    bool ready;
+    __device__ __forceinline__ Wait(uint32_t b, uint32_t ph) : bar(b), parity(ph), ready(mbar_test_wait(b, ph)) {}
+    __device__ __forceinline__ bool done(volatile int* abort, unsigned long long limit_ns) const {
+        return __all_sync(0xffffffffu, ready) || warp_wait(bar, parity, abort, limit_ns);
+    }
+};
+
 // Bounded wait without a look at the abort flag.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
     const unsigned long long t0 = globaltimer_ns();
@@ -169,9 +181,9 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// A row-major matrix in boxes of 128 bytes of a row by box_rows rows, 128-byte
-// swizzled; zeros outside it.
-inline bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
+// A row-major matrix in boxes of box_cols of a row by box_rows rows, swizzled;
+// zeros outside it.
+inline bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int64_t rows, int64_t cols,
                  int64_t ld_bytes, int box_cols, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
@@ -180,7 +192,7 @@ inline bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, const void* 
     cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
