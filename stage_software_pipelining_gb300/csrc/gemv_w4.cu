@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ unsigned long long bars[2 * kMaxStages];
+    __shared__ unsigned long long bars[3 * kMaxStages];
     __shared__ uint4 no_x[SLOTS > 1 ? 32 : 1];  // zeros, as long as one row of x in a stage
     __shared__ int abort_word;
     const int S = p.stages;
@@ -115,15 +115,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int k0 = static_cast<int>(static_cast<long long>(p.blocks) * rank / split);
     const int k1 = static_cast<int>(static_cast<long long>(p.blocks) * (rank + 1) / split);
     const uint32_t bar0 = smem_addr(bars);
-    auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    // A slot has two full barriers, for its even and odd turns.  A warp waits for
+    // every WK-th stage, and the slot's stage before the one it waits for may be
+    // another warp's and not have landed yet: the parity of a single barrier
+    // could not tell that stage's phase from the one after the next.  With two,
+    // the phase before the awaited one belongs to a stage that was read before
+    // the last stage this warp took was copied.
+    auto full_bar = [&](int s, int turn) { return bar0 + 8u * (2 * s + (turn & 1)); };
+    auto full_phase = [](int turn) { return static_cast<uint32_t>(turn >> 1) & 1u; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
     volatile int* abort_flag = &abort_word;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s, 0), 1);
+            mbar_init(full_bar(s, 1), 1);
             mbar_init(empty_bar(s), WR);
         }
         abort_word = 0;
@@ -138,18 +146,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     int issued = 0;  // the producing thread's stages
     if (warp == CW) {
         if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
+            int s = 0, turn = 0;
             for (int kb = k0; kb < k1; ++kb, ++issued) {
-                if (!wait_for(empty_bar(s), ph ^ 1u, abort_flag, p.wait_limit_ns)) break;
+                if (!wait_for(empty_bar(s), (turn & 1) ^ 1, abort_flag, p.wait_limit_ns)) break;
                 if (!(issued == p.withhold && blockIdx.x == 0)) {
-                    mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(W_BYTES + x_bytes));
-                    tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, full_bar(s), kb * (KS / 2), n0);
-                    tma_load_3d(smem_addr(x_ring + s * x_slot), &tmX, full_bar(s), 0, m0, kb * (KS / 32));
+                    const uint32_t bar = full_bar(s, turn);
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(W_BYTES + x_bytes));
+                    tma_load_2d(smem_addr(smem + s * W_BYTES), &tmW, bar, kb * (KS / 2), n0);
+                    tma_load_3d(smem_addr(x_ring + s * x_slot), &tmX, bar, 0, m0, kb * (KS / 32));
                 }
                 if (++s == S) {
                     s = 0;
-                    ph ^= 1u;
+                    ++turn;
                 }
             }
         }
@@ -160,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (lane == 0)
                 for (int j = issued - S > 0 ? issued - S : 0; j < issued; ++j) {
                     if (j == p.withhold && blockIdx.x == 0) continue;
-                    drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1), p.wait_limit_ns);
+                    drain_wait(full_bar(j % S, j / S), full_phase(j / S), p.wait_limit_ns);
                 }
             __syncthreads();
         }
@@ -238,8 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int b = 0; b < NT; ++b)
             x_off[b] = smem_addr(x_ring) + static_cast<uint32_t>(min(8 * b + g % XM, x_rows - 1) * 64 + 16 * c);
         const uint32_t no_x_at = smem_addr(no_x) + 16u * c;
-        int s = wk;
-        uint32_t ph = 0;
+        int s = wk, turn = 0;
         for (int kb = k0 + wk; kb < k1; kb += WK) {
             float scale[SV][4];
             uint32_t zero[LG][4];
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if constexpr (ZEROS && SLOTS != 8) zero[u][i] = zero_of<BF16>(zv[u][i]);
-            if (!warp_wait(full_bar(s), ph, abort_flag, p.wait_limit_ns)) break;
+            if (!warp_wait(full_bar(s, turn), full_phase(turn), abort_flag, p.wait_limit_ns)) break;
             if constexpr (SLOTS != 8) fetch_scales(kb + WK);
             fetch_zeros(kb + WK);
             const uint32_t w_at = w_row + static_cast<uint32_t>(s * W_BYTES);
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             s += WK;
             if (s >= S) {
                 s -= S;
-                ph ^= 1u;
+                ++turn;
             }
             if constexpr (SLOTS == 8) {
                 pos += GPS;

@@ -87,7 +87,7 @@ struct Geo {
     static constexpr int kThreads = 64 + 128 * SETS + 128;  // TMA warp, MMA warp, unpacking, adding
     static constexpr int kAdd = 2 + 4 * SETS;               // first adding warp
     static constexpr int LD = SETS == 1 ? NC : NC / 2;      // sums an adding thread reads at once
-    static_assert(NB % SETS == 0 && (SETS == 1 || CPS == 1) && SETS * SUB <= 8, "the sets' turns");
+    static_assert(NB % SETS == 0 && kStages % SETS == 0 && (SETS == 1 || CPS == 1) && SETS * SUB <= 8, "the sets' turns");
     static_assert(KC >= GROUP && NB * SUB * NC <= static_cast<int>(kDCols), "TMEM");
 };
 
