@@ -34,21 +34,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The same eight weights without their zero point: bf16 128 + w; fp16 the
-// bare bits, w 2^-24 in pairs 0 and 2 and w 2^-20 in pairs 1 and 3.
-template <bool BF16>
-__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
-    if constexpr (BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
-    } else {
-        p[0] = w & 0x000f000fu;
-        p[1] = w & 0x00f000f0u;
-        p[2] = (w >> 8) & 0x000f000fu;
-        p[3] = (w >> 8) & 0x00f000f0u;
-    }
-}
-
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -64,6 +49,7 @@ constexpr int CW = WK * WR;
 constexpr int R = 32 * WR;          // weight rows of a tile
 constexpr int kThreads = 32 * (CW + 1);
 constexpr int kBudget = 100 * 1024; // dynamic shared memory
+constexpr int kLeast = 77 * 1024;   // a third CTA does not fit: see launch_one
 constexpr int W_BYTES = R * KS / 2;
 constexpr int PITCH = R + 4;        // of a partial's rows: no bank conflicts when written
 constexpr int QUADS = R / 4;        // of a row's outputs
@@ -75,16 +61,6 @@ constexpr int kRecvRow = (QUADS + 8) * 16;  // bytes for a row's partials: at mo
 // groups accumulate side by side and are scaled together, each by the lane
 // that holds its column, where one slot would have all four lanes of a row
 // scale the same group.
-//
-// With SLOTS = 8 that makes a group's end cheap enough to move the zero point
-// there as well: sum x (w - z) = sum x w' - z' sum x with w' a nibble as it
-// lies under its mask, and sum x from one more product whose weights are all
-// alike, summed in the same order.  fp16 takes the bare nibble, a subnormal
-// w 2^-24 (or w 2^-20, four bits up: sums of their own), bf16 128 + w under an
-// exponent.  That is 5 (fp16) or 7 (bf16) instructions for 8 weights in place
-// of 9 or 11.  All of it is fp32; the difference of the two sums has about 2
-// (fp16) or 30 (bf16) times the rounding of sum x (w - z), far below a 16-bit
-// result's own.  Weights that all equal the zero point 8 give exactly 0.
 template <bool BF16, int NT, int SLOTS, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 2)
     w4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
@@ -200,10 +176,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         //   SLOTS = 1: [u] group 4u + c (a lane a group; the others ask for it)
         constexpr int SV = SLOTS == 8 ? 2 : SLOTS == 2 ? GPS / 2 : LG;
         T sv[SV][4];
-        // Zero points: SLOTS = 8 as the scales, else [u] group 4u + c.
-        constexpr int ZV = SLOTS == 8 ? 2 : LG;
-        uint32_t zv[ZV][4];
+        uint32_t zv[LG][4];  // zero points: [u] group 4u + c of the stage
+        // SLOTS = 8: a lane's two groups lie side by side, and where rows of
+        // groups allow it one load takes both.
+        const bool pairs = SLOTS == 8 && GPS > 1 && p.s_vec && p.groups % 2 == 0;
         auto fetch_scales = [&](int kb) {
+            if (SLOTS == 8 && pairs) {
+                const int stage = kb + WK * (2 * c / GPS), gi = stage * GPS + 2 * c % GPS;
+                const bool in = stage < k1 && gi < p.groups;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t v = in ? *reinterpret_cast<const uint32_t*>(s_tile + s_off[i] + gi) : 0u;
+                    const uint16_t h[2] = {static_cast<uint16_t>(v), static_cast<uint16_t>(v >> 16)};
+                    sv[0][i] = *reinterpret_cast<const T*>(&h[0]);
+                    sv[SV - 1][i] = *reinterpret_cast<const T*>(&h[1]);
+                }
+                return;
+            }
 #pragma unroll
             for (int u = 0; u < SV; ++u)
 #pragma unroll
@@ -211,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if constexpr (SLOTS == 8) {
                         const int slot = 2 * c + u, stage = kb + WK * (slot / GPS);
                         sv[u][i] = scale_at(i, stage, slot % GPS);
-                        if constexpr (ZEROS) zv[u][i] = zero_at(i, stage, slot % GPS);
                     } else if constexpr (SLOTS == 2) {
                         sv[u][i] = scale_at(i, kb, 2 * u + (c >> 1));
                     } else {
@@ -220,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
         };
         auto fetch_zeros = [&](int kb) {
-            if constexpr (ZEROS && SLOTS != 8) {
+            if constexpr (ZEROS) {
 #pragma unroll
                 for (int u = 0; u < LG; ++u)
 #pragma unroll
@@ -232,11 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
         float acc[2][NT][4] = {};  // scaled sums (SLOTS = 8: [.][.][0], [2] of rows g, g + 8)
         float sub[2][NT][4] = {};  // sums of the running groups
-        // SLOTS = 8: groups so far; fp16's sums of w 2^-20; sum x (fp16: of k in
-        // sub, of k in sub16) times the weight that stands for it
-        int pos = 0;
-        float sub16[2][4] = {}, xsum[4] = {}, xsum16[4] = {};
-        constexpr uint32_t kAlike = !BF16 ? 0x3c003c00u : ZEROS ? 0x43004300u : 0x43084308u;  // 1; 128; 136
+        int pos = 0;                   // SLOTS = 8: groups so far
         // This lane's word of 16-byte chunk 0 in a 128-byte swizzled row: chunk j
         // of row r lies at chunk j ^ (r & 7).
         const uint32_t w_row = smem_addr(smem) + static_cast<uint32_t>((32 * wr + g) * 128 + 16 * g + 4 * c);
@@ -262,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int u = 0; u < LG; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if constexpr (ZEROS && SLOTS != 8) zero[u][i] = zero_of<BF16>(zv[u][i]);
+                    if constexpr (ZEROS) zero[u][i] = zero_of<BF16>(zv[u][i]);
             if (!warp_wait(full_bar(s, turn), full_phase(turn), abort_flag, p.wait_limit_ns)) break;
             if constexpr (SLOTS != 8) fetch_scales(kb + WK);
             fetch_zeros(kb + WK);
@@ -273,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 uint32_t z0[4], z16[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (!ZEROS || SLOTS == 8) z0[i] = zero_of<BF16>(8u);
+                    if constexpr (!ZEROS) z0[i] = zero_of<BF16>(8u);
                     else z0[i] = GPS == 1 ? zero[0][i] : __shfl_sync(0xffffffffu, zero[u / 4][i], u % 4, 4);
                     z16[i] = zero16_of<BF16>(z0[i]);
                 }
@@ -295,16 +279,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                         xb[b][2] = __byte_perm(v.y, v.w, 0x5410);
                         xb[b][3] = __byte_perm(v.y, v.w, 0x7632);
                     }
-                    if constexpr (SLOTS == 8) {
-                        const uint32_t alike[4] = {kAlike, kAlike, kAlike, kAlike};
-                        if constexpr (BF16) {
-                            mma16816<BF16>(xsum, alike, xb[0][0], xb[0][1]);
-                            mma16816<BF16>(xsum, alike, xb[0][2], xb[0][3]);
-                        } else {
-                            mma16816<BF16>(xsum, alike, xb[0][0], xb[0][2]);
-                            mma16816<BF16>(xsum16, alike, xb[0][1], xb[0][3]);
-                        }
-                    }
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {  // 16 weight rows
                         uint32_t q[2][4];
@@ -313,15 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             const int i = 2 * a + h;
                             const uint32_t w = ld_shared_u32((w_at ^ static_cast<uint32_t>(16 * j)) +
                                                              static_cast<uint32_t>(8 * i * (KS / 2)));
-                            if constexpr (SLOTS == 8) nibbles<BF16>(w, q[h]);
-                            else unpack<BF16>(w, z0[i], z16[i], q[h]);
-                        }
-                        if constexpr (SLOTS == 8 && !BF16) {
-                            const uint32_t even[4] = {q[0][0], q[1][0], q[0][2], q[1][2]};
-                            const uint32_t odd[4] = {q[0][1], q[1][1], q[0][3], q[1][3]};
-                            mma16816<BF16>(sub[a][0], even, xb[0][0], xb[0][2]);
-                            mma16816<BF16>(sub16[a], odd, xb[0][1], xb[0][3]);
-                            continue;
+                            unpack<BF16>(w, z0[i], z16[i], q[h]);
                         }
                         const uint32_t lo[4] = {q[0][0], q[1][0], q[0][1], q[1][1]};
                         const uint32_t hi[4] = {q[0][2], q[1][2], q[0][3], q[1][3]};
@@ -369,19 +335,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int i = 2 * a + (e >> 1), u = e & 1;
-                            const float z = ZEROS ? static_cast<float>(zv[u][i]) : 8.0f;
-                            float t;
-                            if constexpr (BF16) {
-                                t = ZEROS ? fmaf(-fmaf(z, 0x1p-7f, 1.0f), xsum[u], sub[a][0][e]) : sub[a][0][e] - xsum[u];
-                            } else {
-                                t = fmaf(-z, xsum[u], sub[a][0][e] * 0x1p24f) +
-                                    fmaf(-z, xsum16[u], sub16[a][e] * 0x1p20f);
-                            }
-                            acc[a][0][e & 2] = fmaf(f32_of(sv[u][i]), t, acc[a][0][e & 2]);
-                            sub[a][0][e] = sub16[a][e] = 0.0f;
+                            acc[a][0][e & 2] = fmaf(f32_of(sv[u][i]), sub[a][0][e], acc[a][0][e & 2]);
+                            sub[a][0][e] = 0.0f;
                         }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) xsum[e] = xsum16[e] = 0.0f;
                 }
             }
         }
@@ -529,7 +485,11 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
         !encode_x(&tmX, L, p.x_rows))
         return GEMM_ERR_LAUNCH;
-    return launch(kernel, tmW, tmX, p, tiles, kThreads, 1024 + p.stages * slot + p.x_rows * kRecvRow, stream);
+    // Two CTAs an SM, as the split counts on, also where registers would let a
+    // third in: with three on some SMs and one on others 1 x 8192 x 28672 (bf16,
+    // groups of 128) took 42.8 us, with two on each 30.1.
+    const int smem = 1024 + p.stages * slot + p.x_rows * kRecvRow;
+    return launch(kernel, tmW, tmX, p, tiles, kThreads, smem > kLeast ? smem : kLeast, stream);
 }
 
 template <bool BF16, int NT, int SLOTS, int GROUP>

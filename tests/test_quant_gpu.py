@@ -351,6 +351,57 @@ def test_gemv_w4_special_values_stay_in_their_row(M):
     assert torch.equal(nan, expect)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("M", [1, 2, 6, 12, 20])
+def test_gemv_w4_infinite_and_large_x(M, group, zeros, dtype):
+    """An infinity takes the sign of its weight less the zero point (NaN where
+    they are equal); the largest finite values do not overflow on the way."""
+    K, N = 1600 // group * group, 150
+    g = torch.Generator().manual_seed(62)
+    x = torch.randn(M, K, generator=g).to(dtype)
+    W = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    z = torch.full((N, K // group), 7 if zeros else 8, dtype=torch.uint8)
+    W[:, 20] = 0x10 * (z[:, 0] + 1) + torch.randint(0, 3, (N,), generator=g, dtype=torch.uint8) + z[:, 0] - 1
+    s = torch.full((N, K // group), 2.0 ** -12, dtype=dtype)
+    C = torch.empty(M, N, dtype=dtype, device="cuda")
+    dev = (W.cuda(), s.cuda(), C)
+    huge = float(torch.finfo(dtype).max)
+    x[M - 1, 40] = huge  # weights z - 1, z, z + 1
+    Q.gemv_w4(x.cuda(), *dev, zeros=z.cuda() if zeros else None)
+    ref, absb = R.gemv_w4(x, W, s, z, group)
+    R.check_rounded(C, ref, 2.0 ** -22, R.W4_REL * absb, "the largest finite value")
+    x[M - 1, 40] = float("inf")
+    Q.gemv_w4(x.cuda(), *dev, zeros=z.cuda() if zeros else None)
+    d = (W[:, 20] & 15).double() - z[:, 0].double()
+    assert torch.equal(C[M - 1].isnan().cpu(), d == 0)
+    assert torch.equal(C[M - 1].isinf().cpu(), d != 0)
+    assert torch.equal(C[M - 1].cpu()[d != 0].sign().double(), d[d != 0].sign())
+    assert C[:M - 1].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("groups", [1, 7, 8, 13, 26, 40])
+def test_gemv_w4_rows_of_groups_on_their_boundaries(groups, group, dtype):
+    """One row of x; scales and zero points in rows of a multiple of eight."""
+    N, K, pitch = 77, groups * group, (groups + 7) // 8 * 8
+    g = torch.Generator().manual_seed(63)
+    x = torch.randn(1, K, generator=g).to(dtype)
+    W = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    s = (torch.rand(N, groups, generator=g) * 0.02 - 0.005).to(dtype)
+    z = torch.randint(0, 16, (N, groups), generator=g, dtype=torch.uint8)
+    ds = wide(s, pitch - groups)
+    dz = torch.full((N, pitch), 99, dtype=torch.uint8, device="cuda")[:, :groups]
+    dz.copy_(z)
+    for dz, hz in ((None, None), (dz, z)):
+        C = GuardedC(1, N, dtype)
+        Q.gemv_w4(x.cuda(), W.cuda(), ds, C.view, zeros=dz)
+        C.check()
+        ref, absb = R.gemv_w4(x, W, s, hz, group)
+        R.check_rounded(C.view, ref, 2.0 ** -22, R.W4_REL * absb, f"{groups} groups of {group}")
+
+
 def test_gemv_w4_fp16_range():
     """Group sums past fp16's range are not lost before a small scale brings them back."""
     K, N = 1024, 16
