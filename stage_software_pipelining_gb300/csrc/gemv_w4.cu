@@ -55,28 +55,30 @@ constexpr int PITCH = R + 4;        // of a partial's rows: no bank conflicts wh
 constexpr int QUADS = R / 4;        // of a row's outputs
 constexpr int kRecvRow = (QUADS + 8) * 16;  // bytes for a row's partials: at most ceil(QUADS/c) from each of c <= 8
 
-// SLOTS: one row of x (SLOTS = 8) or up to four (2) leave columns of the
-// 16 x 8 x 16 product empty.  They hold other groups: column `slot * 8/SLOTS +
-// row` sees x only in the K of group `slot` and zeros elsewhere, so SLOTS
-// groups accumulate side by side and are scaled together, each by the lane
-// that holds its column, where one slot would have all four lanes of a row
-// scale the same group.
-template <bool BF16, int NT, int SLOTS, int GROUP, bool ZEROS>
+// LONE: a single row of x leaves seven of the eight columns of the product
+// empty.  They hold other groups: column j sees x only in the K of the j-th of
+// eight running groups and zeros elsewhere, so that eight groups accumulate
+// side by side and are scaled together, each by the lane that holds its column,
+// where otherwise all four lanes of a row scale the same group.  Taken for
+// groups of 32 and 64: 1 x 8192 x 28672 with zero points takes 37.2 us (fp16,
+// groups of 32) and 30.2 (64) against 40.5 and 31.3 without; with groups of 128
+// 30.7 against 29.6.
+template <bool BF16, int NT, bool LONE, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 2)
     w4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-    static_assert(SLOTS == 1 || NT == 1, "slots fill the columns of a single tile");
     constexpr int MT = 8 * NT;
     constexpr int GPS = KS / GROUP;      // groups of a stage
+    static_assert(!LONE || (NT == 1 && GPS >= 4), "a lane's two groups are of one stage");
     constexpr int LG = (GPS + 3) / 4;    // values a lane loads where four lanes share a row's groups
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ unsigned long long bars[3 * kMaxStages];
-    __shared__ uint4 no_x[SLOTS > 1 ? 32 : 1];  // zeros, as long as one row of x in a stage
+    __shared__ uint4 no_x[LONE ? 32 : 1];  // zeros, as long as one row of x in a stage
     __shared__ int abort_word;
     const int S = p.stages;
-    const int x_rows = SLOTS == 8 ? 1 : p.x_rows;
+    const int x_rows = LONE ? 1 : p.x_rows;
     const int x_bytes = x_rows * KS * 2;
     const int x_slot = (x_bytes + 127) & ~127;
     uint8_t* x_ring = smem + S * W_BYTES;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         abort_word = 0;
         fence_barrier_init();
     }
-    if (SLOTS > 1 && threadIdx.x < 32) no_x[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    if (LONE && threadIdx.x < 32) no_x[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     if (split > 1) cluster_arrive_relaxed();  // this CTA has started: its shared memory may be written to
     griddep_launch_dependents();
@@ -170,18 +172,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int gi = kb * GPS + group;
             return kb < k1 && gi < p.groups ? z_tile[z_off[i] + static_cast<uint32_t>(gi)] : 0u;
         };
-        // Scales, a stage ahead (SLOTS = 8: those of the running SLOTS groups).
-        //   SLOTS = 8: [0], [1] the two columns of this lane, groups 2c and 2c + 1
-        //   SLOTS = 2: [u] group 2u + c/2 of the stage
-        //   SLOTS = 1: [u] group 4u + c (a lane a group; the others ask for it)
-        constexpr int SV = SLOTS == 8 ? 2 : SLOTS == 2 ? GPS / 2 : LG;
+        // Scales, a stage ahead: [u] group 4u + c of the stage (a lane a group; the
+        // others ask for it).  LONE: [0], [1] the columns 2c and 2c + 1 of this
+        // lane, fetched where eight groups begin.
+        constexpr int SV = LONE ? 2 : LG;
         T sv[SV][4];
         uint32_t zv[LG][4];  // zero points: [u] group 4u + c of the stage
-        // SLOTS = 8: a lane's two groups lie side by side, and where rows of
-        // groups allow it one load takes both.
-        const bool pairs = SLOTS == 8 && GPS > 1 && p.s_vec && p.groups % 2 == 0;
+        const bool pairs = LONE && p.s_vec && p.groups % 2 == 0;  // one load takes a lane's two
         auto fetch_scales = [&](int kb) {
-            if (SLOTS == 8 && pairs) {
+            if (LONE && pairs) {
                 const int stage = kb + WK * (2 * c / GPS), gi = stage * GPS + 2 * c % GPS;
                 const bool in = stage < k1 && gi < p.groups;
 #pragma unroll
@@ -197,14 +196,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int u = 0; u < SV; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (SLOTS == 8) {
-                        const int slot = 2 * c + u, stage = kb + WK * (slot / GPS);
-                        sv[u][i] = scale_at(i, stage, slot % GPS);
-                    } else if constexpr (SLOTS == 2) {
-                        sv[u][i] = scale_at(i, kb, 2 * u + (c >> 1));
-                    } else {
-                        sv[u][i] = scale_at(i, kb, min(4 * u + c, GPS - 1));
-                    }
+                    const int slot = 2 * c + u;
+                    if constexpr (LONE) sv[u][i] = scale_at(i, kb + WK * (slot / GPS), slot % GPS);
+                    else sv[u][i] = scale_at(i, kb, min(4 * u + c, GPS - 1));
                 }
         };
         auto fetch_zeros = [&](int kb) {
@@ -215,26 +209,25 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int i = 0; i < 4; ++i) zv[u][i] = zero_at(i, kb, min(4 * u + c, GPS - 1));
             }
         };
-        if constexpr (SLOTS != 8) fetch_scales(k0 + wk);
+        if constexpr (!LONE) fetch_scales(k0 + wk);
         fetch_zeros(k0 + wk);
 
-        float acc[2][NT][4] = {};  // scaled sums (SLOTS = 8: [.][.][0], [2] of rows g, g + 8)
+        float acc[2][NT][4] = {};  // scaled sums (LONE: [.][.][0], [2] of rows g, g + 8)
         float sub[2][NT][4] = {};  // sums of the running groups
-        int pos = 0;                   // SLOTS = 8: groups so far
+        int pos = 0;               // LONE: groups so far
         // This lane's word of 16-byte chunk 0 in a 128-byte swizzled row: chunk j
         // of row r lies at chunk j ^ (r & 7).
         const uint32_t w_row = smem_addr(smem) + static_cast<uint32_t>((32 * wr + g) * 128 + 16 * g + 4 * c);
-        constexpr int XM = 8 / SLOTS;  // rows of x side by side in the columns
         uint32_t x_off[NT];
 #pragma unroll
         for (int b = 0; b < NT; ++b)
-            x_off[b] = smem_addr(x_ring) + static_cast<uint32_t>(min(8 * b + g % XM, x_rows - 1) * 64 + 16 * c);
+            x_off[b] = smem_addr(x_ring) + static_cast<uint32_t>(min(8 * b + (LONE ? 0 : g), x_rows - 1) * 64 + 16 * c);
         const uint32_t no_x_at = smem_addr(no_x) + 16u * c;
         int s = wk, turn = 0;
         for (int kb = k0 + wk; kb < k1; kb += WK) {
             float scale[SV][4];
             uint32_t zero[LG][4];
-            if constexpr (SLOTS == 8) {
+            if constexpr (LONE) {
                 if (pos == 0) fetch_scales(kb);
             } else {
 #pragma unroll
@@ -248,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int i = 0; i < 4; ++i)
                     if constexpr (ZEROS) zero[u][i] = zero_of<BF16>(zv[u][i]);
             if (!warp_wait(full_bar(s, turn), full_phase(turn), abort_flag, p.wait_limit_ns)) break;
-            if constexpr (SLOTS != 8) fetch_scales(kb + WK);
+            if constexpr (!LONE) fetch_scales(kb + WK);
             fetch_zeros(kb + WK);
             const uint32_t w_at = w_row + static_cast<uint32_t>(s * W_BYTES);
             const uint32_t x_at = static_cast<uint32_t>(s * x_slot);
@@ -261,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     else z0[i] = GPS == 1 ? zero[0][i] : __shfl_sync(0xffffffffu, zero[u / 4][i], u % 4, 4);
                     z16[i] = zero16_of<BF16>(z0[i]);
                 }
-                const bool mine = SLOTS == 1 || g / XM == (SLOTS == 8 ? pos + u : u % SLOTS);
+                const bool mine = !LONE || g == pos + u;
 #pragma unroll
                 for (int jj = 0; jj < GROUP / 32; ++jj) {  // 32 of K
                     const int j = u * (GROUP / 32) + jj;
@@ -270,9 +263,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
                         uint32_t at;
-                        if constexpr (SLOTS == 8) at = (mine ? x_at + x_off[b] : no_x_at) + 64u * j;
+                        if constexpr (LONE) at = (mine ? x_at + x_off[b] : no_x_at) + 64u * j;
                         else at = x_at + x_off[b] + static_cast<uint32_t>(j * x_rows * 64);
-                        if (SLOTS == 2 && !mine) at = no_x_at;
                         const uint4 v = ld_shared_v4(at);
                         xb[b][0] = __byte_perm(v.x, v.z, 0x5410);
                         xb[b][1] = __byte_perm(v.x, v.z, 0x7632);
@@ -298,25 +290,22 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                 }
-                if constexpr (SLOTS != 8) {
-                    if (u % SLOTS == SLOTS - 1) {  // the groups are complete: scale their sums
+                if constexpr (!LONE) {  // the group is complete: scale its sums
 #pragma unroll
-                        for (int a = 0; a < 2; ++a)
+                    for (int a = 0; a < 2; ++a)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int i = 2 * a + h;
-                                const float f = SLOTS == 2 ? scale[u / 2 % SV][i]
-                                                : GPS == 1 ? scale[0][i]
-                                                           : __shfl_sync(0xffffffffu, scale[u / 4 % SV][i], u % 4, 4);
+                        for (int h = 0; h < 2; ++h) {
+                            const int i = 2 * a + h;
+                            const float f =
+                                GPS == 1 ? scale[0][i] : __shfl_sync(0xffffffffu, scale[u / 4 % SV][i], u % 4, 4);
 #pragma unroll
-                                for (int b = 0; b < NT; ++b)
+                            for (int b = 0; b < NT; ++b)
 #pragma unroll
-                                    for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                                        acc[a][b][e] = fmaf(f, sub[a][b][e], acc[a][b][e]);
-                                        sub[a][b][e] = 0.0f;
-                                    }
-                            }
-                    }
+                                for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                                    acc[a][b][e] = fmaf(f, sub[a][b][e], acc[a][b][e]);
+                                    sub[a][b][e] = 0.0f;
+                                }
+                        }
                 }
             }
             __syncwarp();
@@ -326,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 s -= S;
                 ++turn;
             }
-            if constexpr (SLOTS == 8) {
+            if constexpr (LONE) {
                 pos += GPS;
                 if (pos == 8 || kb + WK >= k1) {
                     pos = 0;
@@ -353,14 +342,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int e = 0; e < 4; ++e) {
                     const int n = 32 * wr + 16 * a + 8 * (e >> 1) + g;
                     float v = acc[a][b][e];
-                    if constexpr (SLOTS == 8) {  // the eight slots are in four lanes
+                    if constexpr (LONE) {  // the eight columns are in four lanes
                         if (e & 1) continue;
                         v += __shfl_xor_sync(0xffffffffu, v, 1);
                         v += __shfl_xor_sync(0xffffffffu, v, 2);
                         if (c == 0) mine[n] = v;
-                    } else if constexpr (SLOTS == 2) {  // column 4 slot + row
-                        v += __shfl_xor_sync(0xffffffffu, v, 2);
-                        if (c < 2) mine[(2 * c + (e & 1)) * PITCH + n] = v;
                     } else {
                         mine[(8 * b + 2 * c + (e & 1)) * PITCH + n] = v;
                     }
@@ -465,7 +451,7 @@ bool encode_x(CUtensorMap* map, const W4Launch& L, int x_rows) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16, int NT, int SLOTS, int GROUP, bool ZEROS>
+template <bool BF16, int NT, bool LONE, int GROUP, bool ZEROS>
 int launch_one(const W4Launch& L, cudaStream_t stream) {
     Params p = params_of(L);
     p.tiles_m = 1;
@@ -475,7 +461,7 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     p.stages = stages < kMaxStages ? stages : kMaxStages;
     static_assert(WK * 8 * NT * PITCH * 4 <= 5 * W_BYTES && 5 * (W_BYTES + 8 * NT * KS * 2) + 8 * NT * kRecvRow <= kBudget - 1024,
                   "the partials lie over the ring, which has five stages at least");
-    auto kernel = w4_kernel<BF16, NT, SLOTS, GROUP, ZEROS>;
+    auto kernel = w4_kernel<BF16, NT, LONE, GROUP, ZEROS>;
     static Residency res;
     int resident[9];
     if (!res.get(reinterpret_cast<const void*>(kernel), kThreads, kBudget, resident)) return GEMM_ERR_LAUNCH;
@@ -492,22 +478,23 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     return launch(kernel, tmW, tmX, p, tiles, kThreads, smem > kLeast ? smem : kLeast, stream);
 }
 
-template <bool BF16, int NT, int SLOTS, int GROUP>
+template <bool BF16, int NT, bool LONE, int GROUP>
 int launch_zeros(const W4Launch& L, cudaStream_t stream) {
-    return L.zeros ? launch_one<BF16, NT, SLOTS, GROUP, true>(L, stream)
-                   : launch_one<BF16, NT, SLOTS, GROUP, false>(L, stream);
+    return L.zeros ? launch_one<BF16, NT, LONE, GROUP, true>(L, stream)
+                   : launch_one<BF16, NT, LONE, GROUP, false>(L, stream);
 }
 
-template <int NT, int SLOTS, int GROUP>
+template <int NT, bool LONE, int GROUP>
 int launch_type(const W4Launch& L, cudaStream_t stream) {
-    return L.bf16 ? launch_zeros<true, NT, SLOTS, GROUP>(L, stream) : launch_zeros<false, NT, SLOTS, GROUP>(L, stream);
+    return L.bf16 ? launch_zeros<true, NT, LONE, GROUP>(L, stream) : launch_zeros<false, NT, LONE, GROUP>(L, stream);
 }
 
-template <int NT, int SLOTS>
+template <int NT>
 int launch_group(const W4Launch& L, cudaStream_t stream) {
-    if (L.group == 32) return launch_type<NT, SLOTS, 32>(L, stream);
-    if (L.group == 64) return launch_type<NT, SLOTS, 64>(L, stream);
-    return launch_type<NT, SLOTS, 128>(L, stream);
+    const bool lone = NT == 1 && L.M == 1;
+    if (L.group == 32) return lone ? launch_type<1, true, 32>(L, stream) : launch_type<NT, false, 32>(L, stream);
+    if (L.group == 64) return lone ? launch_type<1, true, 64>(L, stream) : launch_type<NT, false, 64>(L, stream);
+    return launch_type<NT, false, 128>(L, stream);
 }
 
 template <typename T>
@@ -519,10 +506,8 @@ void quantize_of(const W4QuantLaunch& L, unsigned grid, cudaStream_t stream) {
 }  // namespace
 
 int w4_launch(const W4Launch& L, cudaStream_t stream) {
-    if (L.M == 1) return launch_group<1, 8>(L, stream);
-    if (L.M <= 4) return launch_group<1, 2>(L, stream);
-    if (L.M <= 8) return launch_group<1, 1>(L, stream);
-    if (L.M <= 16) return launch_group<2, 1>(L, stream);
+    if (L.M <= 8) return launch_group<1>(L, stream);
+    if (L.M <= 16) return launch_group<2>(L, stream);
     return w4_launch_tc(L, stream);
 }
 
