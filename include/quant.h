@@ -17,8 +17,8 @@
  * owned by the caller, no pointer is kept after a call, nothing is allocated,
  * `stream` is a cudaStream_t (NULL = the legacy default stream), every entry
  * point but the two that end in _checked enqueues its work and returns without
- * synchronising, and every entry point gives a gemm_status_t.  Argument checks are made on the host before
- * anything is enqueued.  Leading dimensions are in elements (bytes for the
+ * synchronising, and every entry point gives a gemm_status_t.  Argument checks
+ * are made on the host before anything is enqueued.  Leading dimensions are in elements (bytes for the
  * packed 4-bit weights) and may exceed the row length; a single row's leading
  * dimension is not looked at.  Outputs must not overlap inputs or each other
  * unless an entry point says so.  Rows, columns, M, N and K above 2^31 - 4097
