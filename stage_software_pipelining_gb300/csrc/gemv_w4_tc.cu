@@ -1,7 +1,7 @@
 // gemv_w4_tc.cu -- the 4-bit product for more than 16 rows of x, on tcgen05.
 //
 // Taken where the warp-level products of gemv_w4.cu fill too much of the tensor
-// pipe: 32 x 8192 x 28672 (groups of 128, fp16) takes 41 us here and 64 us with
+// pipe: 32 x 8192 x 28672 (groups of 128, fp16) takes 40 us here and 64 us with
 // mma.sync, of which 25 us are the 16 x 8 x 16 products alone; 16 x 8192 x 8192
 // takes 15 us here and 14 us there.  The weights' bytes alone are 18 us of the
 // first; what bounds it is the instructions that unpack (two thirds of the issue
@@ -72,6 +72,16 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
     return BF16 ? z * 0x00010001u + 0x43004300u : z * 0x00100001u + 0xd400e400u;
 }
 
+// x += scale * a and y += scale * b in one instruction, rounded as fmaf.
+__device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b, float scale) {
+    uint64_t v, s, c;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(scale));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(x), "f"(y));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(v), "l"(s));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(c));
+}
+
 template <int GROUP>
 struct Geo {
     // K of a chunk, the unit handed from the unpacking warps to the MMA warp: NB
@@ -80,14 +90,15 @@ struct Geo {
     static constexpr int SUB = KC / GROUP;  // groups of a chunk
     static constexpr int CPS = KT / KC;     // chunks of a stage
     // Sets of four unpacking warps, which take chunks in turn.  With groups of 128
-    // a second one pays: 20 x 28672 x 8192 takes 38.5 us against 42.3 (24 x 4096^2
+    // a second one pays: 20 x 28672 x 8192 takes 38.4 us against 42.3 (24 x 4096^2
     // 8.0 against 7.9).  With groups of 32 it does not, 66.9 against 62.0: the
     // adding warps are the slower ones, and are left fewer registers.
     static constexpr int SETS = GROUP == 128 ? 2 : 1;
     static constexpr int kThreads = 64 + 128 * SETS + 128;  // TMA warp, MMA warp, unpacking, adding
     static constexpr int kAdd = 2 + 4 * SETS;               // first adding warp
     static constexpr int LD = SETS == 1 ? NC : NC / 2;      // sums an adding thread reads at once
-    static_assert(NB % SETS == 0 && kStages % SETS == 0 && (SETS == 1 || CPS == 1) && SETS * SUB <= 8, "the sets' turns");
+    static constexpr int RUN = SETS == 1 ? 8 : 4;           // scales or zero points of a row fetched at once
+    static_assert(NB % SETS == 0 && kStages % SETS == 0 && (SETS == 1 || CPS == 1) && SETS * SUB <= RUN, "the sets' turns");
     static_assert(KC >= GROUP && NB * SUB * NC <= static_cast<int>(kDCols), "TMEM");
 };
 
@@ -106,7 +117,7 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     constexpr int SUB = Geo<GROUP>::SUB, KC = Geo<GROUP>::KC, CPS = Geo<GROUP>::CPS;
     constexpr int S = kStages, SETS = Geo<GROUP>::SETS, kAdd = Geo<GROUP>::kAdd, LD = Geo<GROUP>::LD;
-    constexpr int kThreads = Geo<GROUP>::kThreads;
+    constexpr int kThreads = Geo<GROUP>::kThreads, RUN = Geo<GROUP>::RUN;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -232,18 +243,18 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
         const uint8_t* zp = ZEROS ? p.zeros + static_cast<long long>(min(n0 + r, p.N - 1)) * p.ldz : nullptr;
         const int g0 = k0 * (KT / GROUP), chunks = (k1 - k0) * CPS;
         const int set = SETS == 1 ? 0 : (warp - 2) >> 2;
-        // This row's zero points, eight groups (an octet) at a time and one octet
-        // ahead: a load a group would touch 32 lines for 32 values.
-        uint32_t z_now[2] = {}, z_next[2] = {};
-        auto fetch = [&](int octet) {  // into z_next; 0 past the last group
+        // This row's zero points, RUN groups at a time and a run ahead: a load a
+        // group would touch 32 lines for 32 values.
+        uint32_t z_now[RUN / 4] = {}, z_next[RUN / 4] = {};
+        auto fetch = [&](int run) {  // into z_next; 0 past the last group
             if constexpr (ZEROS) {
-                const int gi = 8 * octet;
-                if (gi + 8 <= p.groups && p.z_vec) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(zp + gi));
-                    z_next[0] = v.x, z_next[1] = v.y;
+                const int gi = RUN * run;
+                if (gi + RUN <= p.groups && p.z_vec) {
+#pragma unroll
+                    for (int h = 0; h < RUN / 4; ++h) z_next[h] = __ldg(reinterpret_cast<const uint32_t*>(zp + gi) + h);
                 } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < RUN / 4; ++h) {
                         z_next[h] = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -252,19 +263,22 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
                 }
             }
         };
-        auto zero_at = [&](int gi) -> uint32_t { return (gi & 4 ? z_now[1] : z_now[0]) >> (8 * (gi & 3)) & 0xffu; };
-        int octet = (g0 + set * SUB) / 8 - 1;
-        fetch(octet + 1);
+        auto zero_at = [&](int gi) -> uint32_t {
+            return (RUN == 8 && gi & 4 ? z_now[RUN / 4 - 1] : z_now[0]) >> (8 * (gi & 3)) & 0xffu;
+        };
+        int run = (g0 + set * SUB) / RUN - 1;
+        fetch(run + 1);
         int s = set;
         uint32_t ph = 0;
         for (int i = set; i < chunks; i += SETS) {
             const int ch = i % CPS, b = i % NB;
             const Wait full(full_bar(s), ph), done(done_bar(b), (static_cast<uint32_t>(i / NB) & 1u) ^ 1u);
             const int gi = g0 + i * SUB;
-            if (ZEROS && gi / 8 != octet) {  // at most one octet on: a turn is up to four groups
-                octet = gi / 8;
-                z_now[0] = z_next[0], z_now[1] = z_next[1];
-                fetch(octet + 1);
+            if (ZEROS && gi / RUN != run) {  // at most one run on: a turn is up to four groups
+                run = gi / RUN;
+#pragma unroll
+                for (int h = 0; h < RUN / 4; ++h) z_now[h] = z_next[h];
+                fetch(run + 1);
             }
             uint32_t zero[SUB];
 #pragma unroll
@@ -308,39 +322,45 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
         const uint16_t* sp =
             static_cast<const uint16_t*>(p.scales) + static_cast<long long>(min(n0 + r, p.N - 1)) * p.lds;
         const int g0 = k0 * (KT / GROUP);
-        uint32_t s_now[4] = {}, s_next[4];  // scales, by octets as the zero points
-        auto fetch = [&](int octet) {
-            const int gi = 8 * octet;
-            if (gi + 8 <= p.groups && p.s_vec) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp + gi));
-                s_next[0] = v.x, s_next[1] = v.y, s_next[2] = v.z, s_next[3] = v.w;
+        uint32_t s_now[RUN / 2] = {}, s_next[RUN / 2];  // scales, by runs as the zero points
+        auto fetch = [&](int run) {
+            const int gi = RUN * run;
+            if (gi + RUN <= p.groups && p.s_vec) {
+                if constexpr (RUN == 8) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp + gi));
+                    s_next[0] = v.x, s_next[1] = v.y, s_next[2] = v.z, s_next[3] = v.w;
+                } else {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp + gi));
+                    s_next[0] = v.x, s_next[1] = v.y;
+                }
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < RUN / 2; ++e) {
                     const uint32_t lo = gi + 2 * e < p.groups ? sp[gi + 2 * e] : 0u;
                     const uint32_t hi = gi + 2 * e + 1 < p.groups ? sp[gi + 2 * e + 1] : 0u;
                     s_next[e] = lo | hi << 16;
                 }
             }
         };
-        // Group gi's scale, gi in the octet at hand.
+        // Group gi's scale, gi in the run at hand.
         auto scale_of = [&](int gi) -> float {
-            const uint32_t v = gi & 4 ? (gi & 2 ? s_now[3] : s_now[2]) : (gi & 2 ? s_now[1] : s_now[0]);
+            uint32_t v = gi & 2 ? s_now[1] : s_now[0];
+            if constexpr (RUN == 8) v = gi & 4 ? (gi & 2 ? s_now[3] : s_now[2]) : v;
             const uint16_t h = static_cast<uint16_t>(gi & 1 ? v >> 16 : v);
             return f32_of(*reinterpret_cast<const T*>(&h));
         };
-        int octet = g0 / 8 - 1;
-        fetch(octet + 1);
+        int run = g0 / RUN - 1;
+        fetch(run + 1);
         const int chunks = (k1 - k0) * CPS;
         for (int i = 0; i < chunks; ++i) {
             const int b = i % NB;
             const Wait done(done_bar(b), static_cast<uint32_t>(i / NB) & 1u);
             const int gi = g0 + i * SUB;
-            if (gi / 8 != octet) {
-                octet = gi / 8;
+            if (gi / RUN != run) {
+                run = gi / RUN;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s_now[e] = s_next[e];
-                fetch(octet + 1);
+                for (int e = 0; e < RUN / 2; ++e) s_now[e] = s_next[e];
+                fetch(run + 1);
             }
             float scale[SUB];
 #pragma unroll
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
                         if (lane == 0) mbar_arrive(dread_bar(b));
                     }
 #pragma unroll
-                    for (int m = 0; m < LD; ++m) acc[h + m] = fmaf(scale[u], __uint_as_float(d[m]), acc[h + m]);
+                    for (int m = 0; m < LD; m += 2) fma2(acc[h + m], acc[h + m + 1], d[m], d[m + 1], scale[u]);
                 }
             }
         }
