@@ -299,12 +299,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                             const float f =
                                 GPS == 1 ? scale[0][i] : __shfl_sync(0xffffffffu, scale[u / 4 % SV][i], u % 4, 4);
 #pragma unroll
-                            for (int b = 0; b < NT; ++b)
-#pragma unroll
-                                for (int e = 2 * h; e < 2 * h + 2; ++e) {
-                                    acc[a][b][e] = fmaf(f, sub[a][b][e], acc[a][b][e]);
-                                    sub[a][b][e] = 0.0f;
-                                }
+                            for (int b = 0; b < NT; ++b) {
+                                fma2(acc[a][b][2 * h], acc[a][b][2 * h + 1], sub[a][b][2 * h], sub[a][b][2 * h + 1], f);
+                                sub[a][b][2 * h] = sub[a][b][2 * h + 1] = 0.0f;
+                            }
                         }
                 }
             }

@@ -149,6 +149,16 @@ __device__ __forceinline__ uint32_t zero16_of(uint32_t zero) {
     return BF16 ? 0u : (zero - 0x64006400u) * 16u + 0xd400d400u;
 }
 
+// x += scale * a and y += scale * b in one instruction, rounded as fmaf.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float scale) {
+    uint64_t v, s, c;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(scale));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(x), "f"(y));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(v), "l"(s));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(c));
+}
+
 __device__ __forceinline__ void add4(float4& v, float4 u) {
     v.x += u.x;
     v.y += u.y;

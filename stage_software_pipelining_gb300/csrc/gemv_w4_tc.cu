@@ -72,16 +72,6 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
     return BF16 ? z * 0x00010001u + 0x43004300u : z * 0x00100001u + 0xd400e400u;
 }
 
-// x += scale * a and y += scale * b in one instruction, rounded as fmaf.
-__device__ __forceinline__ void fma2(float& x, float& y, uint32_t a, uint32_t b, float scale) {
-    uint64_t v, s, c;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(a), "r"(b));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(scale));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(x), "f"(y));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(v), "l"(s));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(c));
-}
-
 template <int GROUP>
 struct Geo {
     // K of a chunk, the unit handed from the unpacking warps to the MMA warp: NB
@@ -382,7 +372,7 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
                         if (lane == 0) mbar_arrive(dread_bar(b));
                     }
 #pragma unroll
-                    for (int m = 0; m < LD; m += 2) fma2(acc[h + m], acc[h + m + 1], d[m], d[m + 1], scale[u]);
+                    for (int m = 0; m < LD; m += 2) fma2(acc[h + m], acc[h + m + 1], __uint_as_float(d[m]), __uint_as_float(d[m + 1]), scale[u]);
                 }
             }
         }
