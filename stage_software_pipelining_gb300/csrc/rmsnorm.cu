@@ -486,11 +486,14 @@ bool launch_rows(const NormLaunch& L, cudaStream_t stream, int* status) {
     }
     constexpr int kMost = VEC == 1 || sizeof(T) == 4 ? 8 : 4;
     const bool few = L.rows <= 2 * tc_current_device_sms();
-    // One element at a time is too slow for many long rows (4000 x 5001
-    // bf16: 73 us, staged_kernel 37) but ahead of staged_kernel's two more
-    // passes over shared memory up to about 2500 (4000 x 2001: 20.8 and
-    // 20.6; x 1001: 10.2 and 10.8) and for few rows (100 x 5001: 3.2, 6.4).
-    if (VEC == 1 && !few && packs > 2560) return false;
+    // One element at a time costs more instructions the longer the row, staged_kernel
+    // two more passes over shared memory and their barriers.  16-bit, with q: 400 x
+    // 3501 5.1 us to 6.4 of staged_kernel, 1000 x 2001 5.9 to 6.5, x 3001 9.5 to 7.8,
+    // 8000 x 1201 25.0 to 23.1, x 2541 52.1 to 36.6.  fp32: 2000 x 4001 24.6 to 25.4,
+    // 4000 x 2001 22.5 to 24.4, x 3001 38.3 to 34.1.
+    const bool many = L.rows > 12 * tc_current_device_sms();
+    const int64_t longest = sizeof(T) == 4 ? (many ? 2560 : 4096) : many ? 1280 : 2560;
+    if (VEC == 1 && !few && packs > longest) return false;
     int nch = few ? (VEC == 1 ? 4 : 1) : VEC == 1 ? 8 : 4;
     while (nch <= kMost && packs > static_cast<int64_t>(max_threads(sizeof(T), VEC, nch)) * nch) nch *= 2;
     if (nch > kMost) return false;
@@ -546,7 +549,12 @@ int launch_type(const NormLaunch& L, cudaStream_t stream) {
             done[dev] = true;
         }
     }
-    const int threads = L.cols >= 6144 || L.rows <= tc_current_device_sms() ? 512 : L.cols >= 1536 ? 256 : 128;
+    // Few threads a row with more rows an SM until a row fills them: 8000 x 2541
+    // bf16 takes 37.4 us with 128 threads and 45.8 with 256, x 5001 72.9 with 128,
+    // 65.0 with 192 and 69.9 with 256, x 12001 200 with 256 and 185 with 512.
+    const int threads = L.cols >= 7168 || L.rows <= tc_current_device_sms() ? 512
+                        : L.cols >= 5376 || sizeof(T) == 4                  ? 256
+                        : L.cols >= 2560                                    ? 192 : 128;
     return launch(staged_kernel<T>, L.rows, threads, smem, stream, L, st);
 }
 

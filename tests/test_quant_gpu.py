@@ -101,6 +101,12 @@ def test_norm_strides_and_offsets(cols, extra, offset, dtype):
     assert not qb[outside].any(), "a write landed outside q"
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,cols", [(2000, 1277), (2000, 1503), (1900, 2999), (400, 3501), (1900, 6001)])
+def test_norm_many_rows_of_odd_width(rows, cols, dtype):
+    test_norm_all_outputs(rows, cols, dtype)
+
+
 @pytest.mark.parametrize("cols", [256, 4096, 33000])
 def test_norm_in_place_on_x(cols):
     x, w = rand(10, 4, cols).to(BF16), rand(11, cols).to(BF16)
