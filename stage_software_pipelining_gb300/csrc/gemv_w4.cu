@@ -1,6 +1,6 @@
 // gemv_w4.cu -- C[i,j] = sum_groups scales[j,g] * sum_{k in g} x[i,k] * (w[j,k] - zeros[j,g])
-// with 4-bit weights w, for up to 16 rows of x, and the kernel that makes such
-// weights.  (More rows: gemv_w4_tc.cu.)
+// with 4-bit weights w, for up to 16 rows of x and for more where the weights are
+// few, and the kernel that makes such weights.  (Else: gemv_w4_tc.cu.)
 //
 // w4_kernel is bound by reading the weights.  A warp of the CTA copies blocks
 // of them (64 rows by 256 of K) and of x through a ring of shared-memory stages
@@ -452,8 +452,8 @@ bool encode_x(CUtensorMap* map, const W4Launch& L, int x_rows) {
 template <bool BF16, int NT, bool LONE, int GROUP, bool ZEROS>
 int launch_one(const W4Launch& L, cudaStream_t stream) {
     Params p = params_of(L);
-    p.tiles_m = 1;
-    p.x_rows = static_cast<int>(L.M);
+    p.tiles_m = static_cast<int>((L.M + 8 * NT - 1) / (8 * NT));
+    p.x_rows = static_cast<int>(L.M < 8 * NT ? L.M : 8 * NT);
     const int slot = W_BYTES + ((p.x_rows * KS * 2 + 127) & ~127);
     const int stages = (kBudget - 1024 - p.x_rows * kRecvRow) / slot;
     p.stages = stages < kMaxStages ? stages : kMaxStages;
@@ -463,7 +463,7 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     static Residency res;
     int resident[9];
     if (!res.get(reinterpret_cast<const void*>(kernel), kThreads, kBudget, resident)) return GEMM_ERR_LAUNCH;
-    const int64_t tiles = (L.N + R - 1) / R;
+    const int64_t tiles = p.tiles_m * ((L.N + R - 1) / R);
     p.split = choose_split(tiles, p.blocks, 2, resident);
     CUtensorMap tmW, tmX;
     if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
@@ -506,6 +506,14 @@ void quantize_of(const W4QuantLaunch& L, unsigned grid, cudaStream_t stream) {
 int w4_launch(const W4Launch& L, cudaStream_t stream) {
     if (L.M <= 8) return launch_group<1>(L, stream);
     if (L.M <= 16) return launch_group<2>(L, stream);
+    // More rows than a tile's 16: tiles of them side by side read and unpack the
+    // weights again each, but start and end sooner than w4_tc_kernel.  Where the
+    // GPU is not full that is less: 24 x 128 x 4096 takes 3.5 us against 5.2, 24 x
+    // 1024 x 8192 5.8 against 7.9, 24 x 8192 x 1024 5.4 against 6.4; 17 x 8192 x 2048
+    // 8.2 against 7.0, 24 x 4096 x 8192 12.9 against 11.1.
+    const int64_t tiles_m = (L.M + 15) / 16, tiles = tiles_m * ((L.N + R - 1) / R);
+    const int64_t work = tiles_m * L.N * L.K, sms = tc_current_device_sms();
+    if ((tiles <= sms && work <= 1 << 25) || (tiles <= 2 * sms && work <= 1 << 24)) return launch_group<2>(L, stream);
     return w4_launch_tc(L, stream);
 }
 

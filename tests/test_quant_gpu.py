@@ -327,6 +327,50 @@ def test_gemv_w4(M, N, K, group, zeros, dtype):
     w4_case(M, N, K, group, zeros, dtype)
 
 
+# More than 16 rows with more weights than the few-row kernel's tiles are taken for.
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("M,N,K", [(17, 13001, 128), (31, 12999, 384), (32, 13008, 1152), (33, 8900, 640),
+                                   (70, 5100, 512), (20, 1030, 24576), (64, 1100, 9216), (24, 300, 81920)])
+def test_gemv_w4_many_weights(M, N, K, group, zeros, dtype):
+    w4_case(M, N, K, group, zeros, dtype)
+
+
+@pytest.mark.parametrize("M,N,K,group", [(17, 13001, 32, 32), (24, 13001, 2080, 32), (32, 13001, 192, 64)])
+def test_gemv_w4_many_weights_k_that_is_not_a_multiple_of_128(M, N, K, group):
+    w4_case(M, N, K, group, True, BF16)
+
+
+@pytest.mark.parametrize("M", [20, 40])
+def test_gemv_w4_many_weights_is_repeatable(M):
+    a = w4_case(M, 8200, 4096, 64, True, F16).clone()
+    assert torch.equal(a, w4_case(M, 8200, 4096, 64, True, F16))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+def test_gemv_w4_many_weights_infinite_and_large_x(group, zeros, dtype):
+    test_gemv_w4_infinite_and_large_x(20, group, zeros, dtype, N=13001)
+
+
+def test_gemv_w4_many_weights_stuck_pipeline_is_reported():
+    M, N, K = 20, 13001, 2048
+    g = torch.Generator().manual_seed(64)
+    x = torch.randn(M, K, generator=g).to(BF16).cuda()
+    W = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8).cuda()
+    s = (torch.rand(N, K // 64, generator=g) * 0.01).to(BF16).cuda()
+    C = torch.empty(M, N, dtype=BF16, device="cuda")
+    try:
+        G.debug_set(wait_limit_ns=50_000_000, withhold_arrive=0)
+        with pytest.raises(G.GemmError, match="TIMEOUT"):
+            Q.gemv_w4(x, W, s, C, checked=True)
+    finally:
+        G.debug_set()
+    Q.gemv_w4(x, W, s, C, checked=True)
+    ref, absb = R.gemv_w4(x, W, s, None, 64)
+    R.check_rounded(C, ref, 2.0 ** -22, R.W4_REL * absb, "after a timeout")
+
+
 @pytest.mark.parametrize("M,N,K,group", [(1, 40, 32, 32), (3, 40, 96, 32), (1, 50, 192, 64), (12, 20, 2080, 32),
                                          (32, 64, 1056, 32)])
 def test_gemv_w4_k_that_is_not_a_multiple_of_128(M, N, K, group):
@@ -360,10 +404,10 @@ def test_gemv_w4_special_values_stay_in_their_row(M):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, True), (128, False), (128, True)])
 @pytest.mark.parametrize("M", [1, 2, 6, 12, 20])
-def test_gemv_w4_infinite_and_large_x(M, group, zeros, dtype):
+def test_gemv_w4_infinite_and_large_x(M, group, zeros, dtype, N=150):
     """An infinity takes the sign of its weight less the zero point (NaN where
     they are equal); the largest finite values do not overflow on the way."""
-    K, N = 1600 // group * group, 150
+    K = 1600 // group * group
     g = torch.Generator().manual_seed(62)
     x = torch.randn(M, K, generator=g).to(dtype)
     W = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
