@@ -134,6 +134,17 @@ __device__ __forceinline__ uint32_t scaled16(uint32_t a, uint32_t b, float2 row,
     }
 }
 
+// Four adjacent outputs of a row, of which `left` lie in it.
+__device__ __forceinline__ void store_quad(uint16_t* c, int left, uint32_t lo, uint32_t hi) {
+    if (left >= 4) {
+        *reinterpret_cast<uint2*>(c) = make_uint2(lo, hi);
+    } else {
+        if (left > 0) c[0] = static_cast<uint16_t>(lo);
+        if (left > 1) c[1] = static_cast<uint16_t>(lo >> 16);
+        if (left > 2) c[2] = static_cast<uint16_t>(hi);
+    }
+}
+
 // ---------------------------------------------------------------- many rows
 struct PairCtl {
     unsigned long long bar[2 * kPairMaxStages + 5];  // full, empty, tmem_full[2], tmem_empty[2], drain
@@ -581,8 +592,9 @@ __global__ void __launch_bounds__(FEW_THREADS)
         const int q = warp & 3;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         const int n = 32 * q + lane;
-        const float bs = ctl->b_scale[n];
-        uint16_t* out = static_cast<uint16_t*>(p.C) + static_cast<long long>(m0) * p.ldc + n0 + n;
+        const int quad = 8 * q + (lane & 7);  // split = 1: this thread's four columns
+        const float4 bs = *reinterpret_cast<const float4*>(ctl->b_scale + 4 * quad);
+        uint16_t* out = static_cast<uint16_t*>(p.C) + static_cast<long long>(m0) * p.ldc + n0 + 4 * quad;
         const int owner = (n >> 2) * split >> 5;
         const uint32_t push = PUSH && split > 1 ? mapa_shared(recv, static_cast<uint32_t>(owner)) +
                                                       16u * static_cast<uint32_t>(rank * rows * most + (n >> 2) - first(owner)) +
@@ -602,17 +614,23 @@ __global__ void __launch_bounds__(FEW_THREADS)
             } else if (split > 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) part[(c + i) * 128 + n] = __uint_as_float(r[i]);
-            } else {  // this thread's output column, 64 bytes of a row a warp
+            } else {
+                // By way of shared memory, a warp its own, from a column a thread
+                // to four adjacent outputs of four rows a thread.
+                const uint32_t turn = smem_addr(part) + static_cast<uint32_t>(q * 4096 + (c & 16) * 128);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 as = *reinterpret_cast<const float4*>(ctl->a_scale + c + i);
-                    const uint32_t lo = scaled16<BF16>(r[i], r[i + 1], make_float2(as.x, as.y), make_float2(bs, bs));
-                    const uint32_t hi = scaled16<BF16>(r[i + 2], r[i + 3], make_float2(as.z, as.w), make_float2(bs, bs));
-                    const uint32_t w[2] = {lo, hi};
+                for (int i = 0; i < 16; ++i) st_shared_u32(turn + static_cast<uint32_t>(i * 128 + lane * 4), r[i]);
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + i + e < rows && n0 + n < p.N)
-                            out[static_cast<long long>(c + i + e) * p.ldc] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+                for (int i = 0; i < 4; ++i) {
+                    const int m = c + 4 * i + (lane >> 3);
+                    const uint4 v = ld_shared_v4(turn + static_cast<uint32_t>(i * 512 + lane * 16));
+                    const float as = ctl->a_scale[m];
+                    const float2 as2 = make_float2(as, as);
+                    if (m < rows)
+                        store_quad(out + static_cast<long long>(m) * p.ldc, p.N - n0 - 4 * quad,
+                                   scaled16<BF16>(v.x, v.y, as2, make_float2(bs.x, bs.y)),
+                                   scaled16<BF16>(v.z, v.w, as2, make_float2(bs.z, bs.w)));
                 }
             }
         }
@@ -650,13 +668,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
             const uint32_t lo = scaled16<BF16>(__float_as_uint(v.x), __float_as_uint(v.y), as2, make_float2(bs.x, bs.y));
             const uint32_t hi = scaled16<BF16>(__float_as_uint(v.z), __float_as_uint(v.w), as2, make_float2(bs.z, bs.w));
             uint16_t* c = static_cast<uint16_t*>(p.C) + static_cast<long long>(m0 + m) * p.ldc + n;
-            if (n + 4 <= p.N) {
-                *reinterpret_cast<uint2*>(c) = make_uint2(lo, hi);
-            } else {
-                if (n < p.N) c[0] = static_cast<uint16_t>(lo);
-                if (n + 1 < p.N) c[1] = static_cast<uint16_t>(lo >> 16);
-                if (n + 2 < p.N) c[2] = static_cast<uint16_t>(hi);
-            }
+            store_quad(c, p.N - n, lo, hi);
         }
     }
     if (!PUSH && split > 1) cluster_sync_all();  // the peers have read this CTA's partials
