@@ -855,16 +855,17 @@ int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t s
 }
 
 // Which kernel, tile and cut of K: the one with the least time by a model whose
-// constants (microseconds) were fitted to every choice measured on 32 shapes of
-// 1 to 3000 rows, 128 to 28672 columns and 256 to 8192 of K.  Its choices are
-// 2.6 % slower than the best one of each shape on average, 16 % at most
-// (1 x 8192 x 8192: 13.8 us for 13.2; 4 x 2048 x 8192: 6.0 for 6.0;
-// 600 x 300 x 8192: 8.0 for 8.0, in CTA pairs 21.7; 512 x 8192 x 8192: pairs
-// 25.7, few-row tiles 35.7).
+// constants (microseconds) were fitted to every choice measured on 40 shapes of
+// 1 to 5536 rows, 153 to 28672 columns and 82 to 8192 of K.  On 60 other shapes,
+// drawn, its choices are 0.5 % slower than the best one of each on average, 16 %
+// at most (541 x 1332 x 966: 6.9 us for 5.9).
 //   * few rows: a round of resident CTAs takes each one's K blocks and an
 //     epilogue that grows with MT, twice where two share an SM; a cut K adds the
 //     partials' way through distributed shared memory, and rounds of clusters
-//     after the first wait for whole clusters' room.
+//     after the first wait for whole clusters' room.  With half an SM a CTA
+//     starts while the kernel before it ends, but its ring is half as deep:
+//     4 x 2048 x 8192 takes 5.0 us so and 5.7 with a whole SM a CTA, 64 x 8192 x
+//     8192 (K cut in two, one CTA an SM) 17.5 and 15.1.
 //   * pairs: a round takes its K blocks at the tensor pipe's rate.
 struct Choice {
     int mt = 0;  // 0: the pair kernel
@@ -907,20 +908,23 @@ bool choose(const Fp8Launch& L, Choice* best) {
     const int64_t kb = (L.K + BK - 1) / BK;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t pairs = up(L.M, 256) * up(L.N, 256);
-    double least = 4.3 + static_cast<double>(up(pairs, resident[2] > 1 ? resident[2] / 2 : 1)) * (0.29 * kb + 1.32);
+    double least = 3.4 + static_cast<double>(up(pairs, resident[2] > 1 ? resident[2] / 2 : 1)) * (0.3 * kb + 1.98);
     for (int mt = 16; mt <= 256 && (mt == 16 || mt < 2 * L.M); mt *= 2) {
         const int64_t tiles = up(L.M, mt) * up(L.N, 128);
         for (int c = 1; c <= 8 && c <= kb; ++c) {
             if (resident[c] <= 0) continue;
             const int64_t ctas = tiles * c;
-            const bool two = mt <= kFewTwo && ctas > resident[c];
-            const double rounds = static_cast<double>(up(ctas, resident[c] * (two ? 2 : 1)));
-            const double shared = two ? 2.0 : 1.0;
-            const double us = 3.0 + rounds * shared * (up(kb, c) * (0.18 + 0.0009 * mt) + 0.02 * mt) +
-                              (c > 1 ? 0.01 + 0.0009 * mt + 0.23 * (rounds - 1.0) * c : 0.0);
-            if (us < least) {
-                least = us;
-                *best = {mt, c, two};
+            for (int t = 0; t <= (mt <= kFewTwo ? 1 : 0); ++t) {
+                const double rounds = static_cast<double>(up(ctas, resident[c] * (1 + t)));
+                const bool alone = ctas <= resident[c];  // one CTA an SM at most
+                const double block = (t && alone ? 0.29 : 0.163) + 0.0009 * mt;
+                const double us = (t ? 0.74 : 1.93) +
+                                  rounds * (t && !alone ? 2.0 : 1.0) * (up(kb, c) * block + 0.69 + 0.012 * mt) +
+                                  (c > 1 ? 1.17 + 0.0023 * mt + 0.08 * (rounds - 1.0) * c : 0.0);
+                if (us < least) {
+                    least = us;
+                    *best = {mt, c, t == 1};
+                }
             }
         }
     }
