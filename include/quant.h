@@ -116,7 +116,8 @@ int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
  *   group    32, 64 or 128; K is a multiple of it (GEMM_ERR_ARG otherwise)
  *   C        M x N of x's type, ldc >= N
  * Made for few rows: the weights are read once for every 16 or 32 rows of x.
- * Sums are fp32.  K = 0 gives C = 0.
+ * Sums are fp32.  K = 0 gives C = 0.  A NaN or an infinity in x stays in its
+ * row of C and acts as the formula says; one in scales stays in its column.
  * Alignment (GEMM_ERR_ALIGN otherwise): x and W start on 16-byte boundaries,
  * ldx*2 and ldw are multiples of 16; the others are aligned to their element.
  * K above 2^26 and lds or ldz above 2^22 are GEMM_ERR_UNSUPPORTED.
