@@ -16,7 +16,8 @@
  * Memory, streams and errors are gemm.h's: all pointers are device pointers
  * owned by the caller, no pointer is kept after a call, nothing is allocated,
  * `stream` is a cudaStream_t (NULL = the legacy default stream), every entry
- * point but the two that end in _checked enqueues its work and returns without
+ * point but the two that end in _checked and the two that end in _plan
+ * (host code alone) enqueues its work and returns without
  * synchronising, and every entry point gives a gemm_status_t.  Argument checks
  * are made on the host before anything is enqueued.  Leading dimensions are in elements (bytes for the
  * packed 4-bit weights) and may exceed the row length; a single row's leading
@@ -41,6 +42,24 @@ typedef enum {
     QUANT_F16 = 1,
     QUANT_BF16 = 2
 } quant_type_t;
+
+/* The kernels of the products, as the plan queries name them. */
+typedef enum {
+    QUANT_KERNEL_FP8_FEW = 0,  /* gemm_fp8: tiles of 16 to 256 rows of A */
+    QUANT_KERNEL_FP8_PAIR = 1, /* gemm_fp8: tiles of 256 rows on CTA pairs */
+    QUANT_KERNEL_W4_WARP = 2,  /* gemv_w4: tiles of 8 or 16 rows of x, warp-level products */
+    QUANT_KERNEL_W4_TC = 3     /* gemv_w4: tiles of 32 rows of x, tcgen05 */
+} quant_kernel_t;
+
+/* A launch that a product would make. */
+typedef struct {
+    int kernel;     /* a quant_kernel_t */
+    int tile_rows;  /* rows of A (of x) a tile */
+    int split;      /* CTAs that share a tile's K, a cluster */
+    int stages;     /* depth of the operand ring */
+    int grid;       /* CTAs */
+    int smem_bytes; /* dynamic shared memory a CTA */
+} quant_plan_t;
 
 /*
  * add_rmsnorm -- for each of `rows` rows of `cols` elements
@@ -107,6 +126,14 @@ int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
                      int dtype, void* stream);
 
 /*
+ * gemm_fp8_plan -- the launch gemm_fp8 would make for these sizes and this
+ * dtype of C, without making it.  Needs a current CUDA device (it asks the
+ * runtime how many clusters can be resident).  GEMM_ERR_ARG for sizes below 1,
+ * an unknown dtype or a NULL plan; GEMM_ERR_UNSUPPORTED as gemm_fp8.
+ */
+int gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int dtype, quant_plan_t* plan);
+
+/*
  * gemv_w4 -- C[i,j] = sum_k x[i,k] * scales[j,k/group] * (w[j,k] - zeros[j,k/group])
  *   x        M x K, dtype QUANT_F16 or QUANT_BF16, ldx >= K
  *   W        N x K 4-bit values 0..15, two a byte, the even k in the low four
@@ -130,6 +157,10 @@ int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const v
 int gemv_w4_checked(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
                     int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
                     int group, void* C, int64_t ldc, int dtype, void* stream);
+
+/* gemv_w4_plan -- for gemv_w4 what gemm_fp8_plan is for gemm_fp8; `zeros` says
+ * whether there are zero points (0 or 1). */
+int gemv_w4_plan(int64_t M, int64_t N, int64_t K, int group, int zeros, int dtype, quant_plan_t* plan);
 
 /*
  * quantize_w4 -- a weight matrix (N x K, row-major, any quant_type_t) in the

@@ -801,19 +801,24 @@ int launch_pair_as(const Fp8Launch& L, int slot, cudaStream_t stream) {
     p.group_m = static_cast<int>(g < 8 ? 8 : g > 16 ? 16 : g);
     p.stages = S;
     p.idesc = instruction(256, 256);
+    auto kernel = fp8_pair_kernel<BF16, S, BOX_COLS>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
+    const int units = resident_pairs(reinterpret_cast<const void*>(kernel));
+    if (units <= 0) return GEMM_ERR_LAUNCH;
+    const int grid = static_cast<int>(2 * (tiles < units ? tiles : units));
+    if (L.plan) {
+        *L.plan = {QUANT_KERNEL_FP8_PAIR, 256, 1, S, grid, kMaxSmem};
+        return GEMM_OK;
+    }
     CUtensorMap tmA, tmB, tmC;
     if (!encode_e4m3(&tmA, L.A, L.M, L.K, L.lda, 128) || !encode_e4m3(&tmB, L.B, L.N, L.K, L.ldb, 128) ||
         !encode_rows(&tmC, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                      BOX_COLS == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, L.C, L.M, L.N, L.ldc * 2,
                      BOX_COLS, 32))
         return GEMM_ERR_LAUNCH;
-    auto kernel = fp8_pair_kernel<BF16, S, BOX_COLS>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
-    const int units = resident_pairs(reinterpret_cast<const void*>(kernel));
-    if (units <= 0) return GEMM_ERR_LAUNCH;
     static_assert(1024 + 2 * S * ROW_TILE_BYTES + 8 * kPairBoxes * 64 * BOX_COLS + sizeof(PairCtl) <= kMaxSmem,
                   "the pair kernel's shared memory");
-    Config c(2 * (tiles < units ? tiles : units), 2, PAIR_THREADS, kMaxSmem, stream);
+    Config c(grid, 2, PAIR_THREADS, kMaxSmem, stream);
     return finish(cudaLaunchKernelEx(&c.cfg, kernel, tmA, tmB, tmC, p));
 }
 
@@ -845,12 +850,17 @@ int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t s
     static_assert(4 * STAGE >= MT * 512, "other partials lie over the ring");
     p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
     p.idesc = instruction(128, MT);
+    const int smem = 1024 + p.stages * STAGE + static_cast<int>(sizeof(FewCtl)) + recv;
+    if (L.plan) {
+        *L.plan = {QUANT_KERNEL_FP8_FEW, MT, split, p.stages, static_cast<int>(tiles * split), smem};
+        return GEMM_OK;
+    }
     CUtensorMap tmW, tmX;
     if (!encode_e4m3(&tmW, L.B, L.N, L.K, L.ldb, 128) || !encode_e4m3(&tmX, L.A, L.M, L.K, L.lda, MT))
         return GEMM_ERR_LAUNCH;
     auto kernel = L.out_bf16 ? fp8_few_kernel<MT, true> : fp8_few_kernel<MT, false>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), 2 * slot + L.out_bf16)) return GEMM_ERR_LAUNCH;
-    Config c(tiles * split, split, FEW_THREADS, 1024 + static_cast<size_t>(p.stages) * STAGE + sizeof(FewCtl) + recv, stream);
+    Config c(tiles * split, split, FEW_THREADS, smem, stream);
     return finish(cudaLaunchKernelEx(&c.cfg, kernel, tmW, tmX, p));
 }
 

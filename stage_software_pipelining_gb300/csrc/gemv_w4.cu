@@ -465,15 +465,17 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     if (!res.get(reinterpret_cast<const void*>(kernel), kThreads, kBudget, resident)) return GEMM_ERR_LAUNCH;
     const int64_t tiles = p.tiles_m * ((L.N + R - 1) / R);
     p.split = choose_split(tiles, p.blocks, 2, resident);
+    // Two CTAs an SM, as the split counts on, also where registers would let a
+    // third in: with three on some SMs and one on others 1 x 8192 x 28672 (bf16,
+    // groups of 128) took 42.8 us, with two on each 30.1.
+    int smem = 1024 + p.stages * slot + p.x_rows * kRecvRow;
+    if (smem < kLeast) smem = kLeast;
+    if (L.plan) return planned(L, QUANT_KERNEL_W4_WARP, 8 * NT, p, tiles, smem);
     CUtensorMap tmW, tmX;
     if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, L.W, L.N, L.K / 2, L.ldw, KS / 2, R) ||
         !encode_x(&tmX, L, p.x_rows))
         return GEMM_ERR_LAUNCH;
-    // Two CTAs an SM, as the split counts on, also where registers would let a
-    // third in: with three on some SMs and one on others 1 x 8192 x 28672 (bf16,
-    // groups of 128) took 42.8 us, with two on each 30.1.
-    const int smem = 1024 + p.stages * slot + p.x_rows * kRecvRow;
-    return launch(kernel, tmW, tmX, p, tiles, kThreads, smem > kLeast ? smem : kLeast, stream);
+    return launch(kernel, tmW, tmX, p, tiles, kThreads, smem, stream);
 }
 
 template <bool BF16, int NT, bool LONE, int GROUP>

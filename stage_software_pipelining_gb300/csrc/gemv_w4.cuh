@@ -290,6 +290,13 @@ inline Params params_of(const W4Launch& L) {
     return p;
 }
 
+// Fill a plan query's answer in place of a launch.
+inline int planned(const W4Launch& L, int kernel, int tile_rows, const Params& p, int64_t tiles, int smem) {
+    if (tiles * p.split > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
+    *L.plan = {kernel, tile_rows, p.split, p.stages, static_cast<int>(tiles * p.split), smem};
+    return GEMM_OK;
+}
+
 // Launch with clusters of p.split CTAs, overlapping the previous kernel's end.
 template <typename Kernel>
 int launch(Kernel kernel, const CUtensorMap& tmW, const CUtensorMap& tmX, const Params& p, int64_t tiles, int threads,

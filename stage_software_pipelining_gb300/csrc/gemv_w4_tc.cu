@@ -440,6 +440,7 @@ int launch_one(const W4Launch& L, cudaStream_t stream) {
     for (int& n : resident) n *= 2;
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * ((L.N + R - 1) / R);
     p.split = choose_split(tiles, p.blocks, 4, resident);
+    if (L.plan) return planned(L, QUANT_KERNEL_W4_TC, NC, p, tiles, kSmem);
     CUtensorMap tmW, tmX;
     if (!encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_64B, L.W, L.N, L.K / 2, L.ldw, KT / 2, R) ||
         !encode_rows(&tmX, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "../../include/quant.h"
+
 namespace ssp {
 
 struct GemmDeviceStatus;
@@ -44,6 +46,7 @@ struct Fp8Launch {
     const float* a_scale;
     const float* b_scale;
     int out_bf16;  // 0 fp16, 1 bf16
+    quant_plan_t* plan = nullptr;  // filled instead of launching, if given
 };
 int fp8_launch(const Fp8Launch& L, cudaStream_t stream);
 // The fp8 kernels' device status word, read and reset (synchronous).
@@ -64,6 +67,7 @@ struct W4Launch {
     void* C;
     int64_t ldc;
     int bf16;  // 0 fp16, 1 bf16
+    quant_plan_t* plan = nullptr;  // filled instead of launching, if given
 };
 int w4_launch(const W4Launch& L, cudaStream_t stream);
 int w4_read_and_clear_status(GemmDeviceStatus* out);

@@ -111,6 +111,18 @@ int gemm_fp8_checked(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
     return st != GEMM_OK ? st : checked(ssp::fp8_read_and_clear_status, stream);
 }
 
+int gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int dtype, quant_plan_t* plan) {
+    if (M < 1 || N < 1 || K < 1 || !known(dtype) || plan == nullptr) return GEMM_ERR_ARG;
+    if (dtype == QUANT_F32 || M > kMost || N > kMost || K > kMost) return GEMM_ERR_UNSUPPORTED;
+    ssp::Fp8Launch L{};
+    L.M = M;
+    L.N = N;
+    L.K = K;
+    L.out_bf16 = dtype == QUANT_BF16;
+    L.plan = plan;
+    return ssp::fp8_launch(L, nullptr);
+}
+
 int gemv_w4(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const void* W,
             int64_t ldw, const void* scales, int64_t lds, const void* zeros, int64_t ldz,
             int group, void* C, int64_t ldc, int dtype, void* stream) {
@@ -147,6 +159,23 @@ int gemv_w4_checked(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
                     int group, void* C, int64_t ldc, int dtype, void* stream) {
     const int st = gemv_w4(M, N, K, x, ldx, W, ldw, scales, lds, zeros, ldz, group, C, ldc, dtype, stream);
     return st != GEMM_OK ? st : checked(ssp::w4_read_and_clear_status, stream);
+}
+
+int gemv_w4_plan(int64_t M, int64_t N, int64_t K, int group, int zeros, int dtype, quant_plan_t* plan) {
+    if (M < 1 || N < 1 || K < 1 || !known(dtype) || plan == nullptr) return GEMM_ERR_ARG;
+    if ((group != 32 && group != 64 && group != 128) || K % group != 0 || (zeros != 0 && zeros != 1))
+        return GEMM_ERR_ARG;
+    if (dtype == QUANT_F32 || M > kMost || N > kMost || K > (1 << 26)) return GEMM_ERR_UNSUPPORTED;
+    ssp::W4Launch L{};
+    L.M = M;
+    L.N = N;
+    L.K = K;
+    L.group = group;
+    // The choice asks whether there are zero points, not what they are.
+    L.zeros = zeros ? reinterpret_cast<const uint8_t*>(static_cast<uintptr_t>(256)) : nullptr;
+    L.bf16 = dtype == QUANT_BF16;
+    L.plan = plan;
+    return ssp::w4_launch(L, nullptr);
 }
 
 int quantize_w4(int64_t N, int64_t K, const void* w, int64_t ld, int dtype, int group, void* W,

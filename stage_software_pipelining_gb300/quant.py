@@ -15,6 +15,7 @@ other than GEMM_OK raises GemmError.  There is no CPU fallback.
 """
 from __future__ import annotations
 
+import ctypes
 import importlib.util
 import os
 import threading
@@ -35,8 +36,15 @@ GROUPS = (32, 64, 128)          # K per scale of the 4-bit weights
 E4M3_MAX = 448.0                # largest e4m3 value
 
 # Every extern "C" symbol include/quant.h declares.
-EXPORTS = ("add_rmsnorm", "quantize_fp8", "gemm_fp8", "gemm_fp8_checked", "gemv_w4",
-           "gemv_w4_checked", "quantize_w4")
+EXPORTS = ("add_rmsnorm", "quantize_fp8", "gemm_fp8", "gemm_fp8_checked", "gemm_fp8_plan", "gemv_w4",
+           "gemv_w4_checked", "gemv_w4_plan", "quantize_w4")
+
+# The products' kernels, in quant_kernel_t's order.
+KERNELS = ("fp8_few", "fp8_pair", "w4_warp", "w4_tc")
+
+
+class _Plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("kernel", "tile_rows", "split", "stages", "grid", "smem_bytes")]
 
 _lock = threading.Lock()
 _lib = None
@@ -49,7 +57,6 @@ def load_library():
     global _lib
     with _lock:
         if _lib is None:
-            import ctypes
             lib = G.load_library()
             i64, p, i32, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
             lib.add_rmsnorm.argtypes = [i64, i64, p, i64, p, i64, p, f32, i32, p, i64, p, i64, p,
@@ -60,6 +67,8 @@ def load_library():
             lib.gemv_w4.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, i32, p, i64,
                                     i32, p]
             lib.gemv_w4_checked.argtypes = lib.gemv_w4.argtypes
+            lib.gemm_fp8_plan.argtypes = [i64, i64, i64, i32, p]
+            lib.gemv_w4_plan.argtypes = [i64, i64, i64, i32, i32, i32, p]
             lib.quantize_w4.argtypes = [i64, i64, p, i64, i32, i32, p, i64, p, i64, i32, p, i64, p]
             for name in EXPORTS:
                 getattr(lib, name).restype = i32
@@ -166,3 +175,30 @@ def quantize_w4(w: torch.Tensor, W: torch.Tensor, scales: torch.Tensor,
     if st:
         raise GemmError(st, "quantize_w4")
     return W
+
+
+def _plan(name: str, *args) -> dict:
+    plan = _Plan()
+    st = getattr(load_library(), name)(*args, ctypes.byref(plan))
+    if st:
+        raise GemmError(st, name)
+    out = {n: getattr(plan, n) for n, _ in _Plan._fields_}
+    out["kernel"] = KERNELS[plan.kernel]
+    return out
+
+
+_TYPES = {torch.float32: QUANT_F32, torch.float16: QUANT_F16, torch.bfloat16: QUANT_BF16}
+
+
+def gemm_fp8_plan(M: int, N: int, K: int, dtype: torch.dtype = torch.bfloat16) -> dict:
+    """The launch gemm_fp8 would make on the current device for an M x N result
+    of `dtype`: its kernel (one of KERNELS), the rows of A a tile, the CTAs that
+    share a tile's K, the ring's stages, the CTAs and their dynamic shared memory."""
+    return _plan("gemm_fp8_plan", int(M), int(N), int(K), _TYPES.get(dtype, -1))
+
+
+def gemv_w4_plan(M: int, N: int, K: int, group: int, zeros: bool = False,
+                 dtype: torch.dtype = torch.bfloat16) -> dict:
+    """The same for gemv_w4 with groups of `group`, with or without zero points."""
+    return _plan("gemv_w4_plan", int(M), int(N), int(K), int(group), int(bool(zeros)),
+                 _TYPES.get(dtype, -1))
