@@ -850,7 +850,9 @@ int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t s
     static_assert(4 * STAGE >= MT * 512, "other partials lie over the ring");
     p.stages = stages < kFewMaxStages ? stages : kFewMaxStages;
     p.idesc = instruction(128, MT);
-    const int smem = 1024 + p.stages * STAGE + static_cast<int>(sizeof(FewCtl)) + recv;
+    int smem = 1024 + p.stages * STAGE + static_cast<int>(sizeof(FewCtl)) + recv;
+    if (smem < kTmemPairedSmem) smem = kTmemPairedSmem;
+    static_assert(2 * kFewTwo <= 512 && MT <= 256, "two CTAs' tensor memory");
     if (L.plan) {
         *L.plan = {QUANT_KERNEL_FP8_FEW, MT, split, p.stages, static_cast<int>(tiles * split), smem};
         return GEMM_OK;

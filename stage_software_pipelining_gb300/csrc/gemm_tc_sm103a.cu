@@ -1322,7 +1322,7 @@ int plan(const TcLaunch& L, TcParams& p, Geometry& geo) {
     // One CTA per SM: a 256-wide tile uses all 512 TMEM columns, and a
     // stream-K finisher must never wait on a unit that is itself waiting for
     // TMEM held by another CTA of the same SM.
-    if (smem < 120 * 1024) smem = 120 * 1024;
+    if (smem < kTmemAloneSmem) smem = kTmemAloneSmem;
     geo.smem = smem;
     int max_units = sms;
     if (pair) {

@@ -98,7 +98,9 @@ struct Ctl {
     uint32_t tmem_base;
     int abort;
 };
-constexpr int kSmem = 1024 + kStages * SLOT + static_cast<int>(sizeof(Ctl));
+constexpr int kUsed = 1024 + kStages * SLOT + static_cast<int>(sizeof(Ctl));
+constexpr int kSmem = kUsed > kTmemPairedSmem ? kUsed : kTmemPairedSmem;
+static_assert(2 * (kSmem + kCtaSmem) <= kSmSmem && 2 * kTmemCols <= 512, "two CTAs an SM");
 static_assert(NC * R * 4 <= kStages * SLOT, "the partials lie over the ring");
 
 template <bool BF16, int GROUP, bool ZEROS>

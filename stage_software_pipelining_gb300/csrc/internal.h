@@ -55,6 +55,21 @@ struct SimtLaunch {
     int split_parts;
 };
 
+// Dynamic shared memory that a CTA with tensor memory asks for at least, by how
+// many of its kind an SM takes.  A CTA's allocation of tensor memory waits until
+// its neighbours on the SM leave enough columns, and CTAs wait for one another
+// (a cluster's barriers, a stream-K finisher for its contributors), so kernels
+// on two streams could close a circle of such waits.  One that may take all 512
+// columns therefore shares its SM with none, and two that share one take 256 at
+// most: 120 and 110 KB (with 1 KB of the system's each) do not fit the SM's 228
+// KB together, 110 and 110 do.
+constexpr int kSmSmem = 228 * 1024;
+constexpr int kCtaSmem = 1024;  // the system's, of each CTA
+constexpr int kTmemAloneSmem = 120 * 1024;
+constexpr int kTmemPairedSmem = 110 * 1024;
+static_assert(2 * (kTmemPairedSmem + kCtaSmem) <= kSmSmem, "two CTAs an SM");
+static_assert(kTmemAloneSmem + kTmemPairedSmem + 2 * kCtaSmem > kSmSmem, "not beside one that is alone");
+
 // gemm_debug_set's values, for the tensor-core kernels of other files.
 struct DebugHooks {
     int64_t wait_limit_ns;

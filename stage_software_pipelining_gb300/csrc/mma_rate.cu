@@ -35,7 +35,7 @@ constexpr int kRateBBytes = kRateN * kRateAtomRowBytes;      // 32 KB
 // The operands need 1 KB + 48 KB; asking for 120 KB keeps one CTA per SM, so
 // that each CTA has its SM's tensor pipe to itself and the two CTAs of a
 // pair sit on two SMs, as cta_group::2 requires.
-constexpr int kRateSmem = 120 * 1024;
+constexpr int kRateSmem = kTmemAloneSmem;
 static_assert(kRateSmem >= 1024 + kRateABytes + kRateBBytes, "operands must fit");
 constexpr unsigned long long kRateWaitNs = 2000000000ull;
 

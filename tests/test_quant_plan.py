@@ -60,3 +60,38 @@ def test_plans_on_the_gpu(gpu, lib, dtype):
     for M, kernel, rows in ((1, "w4_warp", 8), (8, "w4_warp", 8), (9, "w4_warp", 16), (20, "w4_tc", 32)):
         p = Q.gemv_w4_plan(M, 8192, 8192, 64, True, dtype)
         assert p["kernel"] == kernel and p["tile_rows"] == rows and p["grid"] % p["split"] == 0
+
+
+# Shared memory of an SM and, of that, the system's part of each CTA.
+SM_SMEM, CTA_SMEM = 228 * 1024, 1024
+
+
+def few_row_plans():
+    """Every few-row tile of gemm_fp8 and its cuts, and gemv_w4's tcgen05 kernel."""
+    for M in (1, 5, 16, 20, 32, 40, 64, 100, 200, 256, 300, 600, 700):
+        for N, K in ((64, 128), (520, 768), (600, 2048), (4096, 4096), (28672, 4096), (8192, 300), (40000, 256)):
+            yield f"gemm_fp8 {M} x {N} x {K}", Q.gemm_fp8_plan(M, N, K)
+    for M, N, K, group in ((17, 13001, 128, 32), (32, 8192, 28672, 128), (24, 8192, 8192, 64)):
+        for zeros in (False, True):
+            yield f"gemv_w4 {M} x {N} x {K}", Q.gemv_w4_plan(M, N, K, group, zeros)
+
+
+@pytest.mark.gpu
+def test_no_tensor_memory_neighbour_of_the_gemm(gpu, lib):
+    """A CTA of the GEMM may take all of an SM's tensor memory: no CTA of a
+    kernel with tensor memory fits beside it, on whichever stream it runs."""
+    least = min(G.plan(1024, 1024, 1024, G.GEMM_BF16_F32, stages, tile=tile)["smem_bytes"]
+                for tile in G.TILE_MAX_STAGES for stages in (1, 2))
+    for name, p in few_row_plans():
+        if p["kernel"] != "w4_warp":  # no tensor memory
+            assert least + p["smem_bytes"] + 2 * CTA_SMEM > SM_SMEM, f"{name}: {p}"
+
+
+@pytest.mark.gpu
+def test_two_small_ctas_still_share_an_sm(gpu, lib):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for name, p in few_row_plans():
+        if p["grid"] > 2 * sms or p["tile_rows"] > 64 or p["kernel"] == "fp8_pair":
+            continue
+        if p["kernel"] == "w4_tc" or (p["grid"] > sms and p["kernel"] == "fp8_few" and p["stages"] < 6):
+            assert 2 * (p["smem_bytes"] + CTA_SMEM) <= SM_SMEM, f"{name}: {p}"
