@@ -81,7 +81,7 @@ typedef struct {
  *   eps           >= 0
  * No alignment is asked for beyond the element's own; rows on 16-byte
  * boundaries (8-byte for q) are the fast case.  A NaN or an infinity in a row
- * of h makes that row's q and scale NaN, and y what the formula gives.  h^2 is
+ * of h or of y makes that row's q and scale NaN, and y what the formula gives.  h^2 is
  * an fp32 value: a row with |h| above 1.8e19 gives y = 0.  cols = 0 writes
  * scale alone.
  */
@@ -93,7 +93,8 @@ int add_rmsnorm(int64_t rows, int64_t cols, const void* x, int64_t ldx, const vo
 /*
  * quantize_fp8 -- scale = max(max|x| / 448, 2^-126) and q = e4m3(x / scale)
  * for each row: activations without a norm, or a weight matrix stored N x K
- * (a scale an output column).  Types, NaN and alignment as add_rmsnorm.
+ * (a scale an output column).  A NaN or an infinity in a row of x makes that
+ * row's q and scale NaN.  Types and alignment as add_rmsnorm.
  */
 int quantize_fp8(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dtype, void* q,
                  int64_t ldq, float* scale, void* stream);

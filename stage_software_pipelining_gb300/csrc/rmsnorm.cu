@@ -18,6 +18,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <mutex>
 #include <type_traits>
 
@@ -157,15 +158,18 @@ __device__ __forceinline__ Stats block_join(Stats s, Stats* buf) {
     return s;
 }
 
-// rstd, scale and 1/scale of a row from its Stats.  (The reciprocals are within
-// an ulp, and a scale lies in [2^-126, 2^120].)
+// rstd, scale and 1/scale of a row from its Stats.  A row whose largest y is not
+// finite has neither a scale nor 8-bit values: both are NaN, also where the
+// formula would give an infinite scale and zeros.  (The reciprocals are within an
+// ulp, and a scale that is a number lies in [2^-126, 2^120].)
 struct Factors {
     float rstd, scale, inv;
 };
 __device__ __forceinline__ Factors row_factors(const NormLaunch& p, Stats s) {
     Factors f;
     f.rstd = p.weight ? rsqrtf(fmaf(s.ss, p.inv_cols, p.eps)) : 1.0f;
-    f.scale = max_nan(f.rstd * s.am * (1.0f / kE4m3Max), kScaleMin);
+    const float most = f.rstd * s.am;
+    f.scale = most <= FLT_MAX ? fmaxf(most * (1.0f / kE4m3Max), kScaleMin) : __int_as_float(0x7fffffff);
     asm("rcp.approx.f32 %0, %1;" : "=f"(f.inv) : "f"(f.scale));
     return f;
 }
