@@ -81,9 +81,10 @@ typedef struct {
  *   eps           >= 0
  * No alignment is asked for beyond the element's own; rows on 16-byte
  * boundaries (8-byte for q) are the fast case.  A NaN or an infinity in a row
- * of h or of y makes that row's q and scale NaN, and y what the formula gives.  h^2 is
- * an fp32 value: a row with |h| above 1.8e19 gives y = 0.  cols = 0 writes
- * scale alone.
+ * of h or of y makes that row's q and scale NaN, and y what the formula gives
+ * (a row of zeros with eps = 0: NaN).  A row whose squares, or their sum, leave
+ * fp32's range is scaled by a power of two first: every finite h has its y.
+ * cols = 0 writes scale alone.
  */
 int add_rmsnorm(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual,
                 int64_t ldr, const void* weight, float eps, int dtype, void* residual_out,

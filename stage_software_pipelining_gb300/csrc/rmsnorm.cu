@@ -165,13 +165,33 @@ __device__ __forceinline__ Stats block_join(Stats s, Stats* buf) {
 struct Factors {
     float rstd, scale, inv;
 };
-__device__ __forceinline__ Factors row_factors(const NormLaunch& p, Stats s) {
+__device__ __forceinline__ Factors row_factors(const NormLaunch& p, Stats s, float eps) {
     Factors f;
-    f.rstd = p.weight ? rsqrtf(fmaf(s.ss, p.inv_cols, p.eps)) : 1.0f;
+    f.rstd = p.weight ? rsqrtf(fmaf(s.ss, p.inv_cols, eps)) : 1.0f;
     const float most = f.rstd * s.am;
     f.scale = most <= FLT_MAX ? fmaxf(most * (1.0f / kE4m3Max), kScaleMin) : __int_as_float(0x7fffffff);
     asm("rcp.approx.f32 %0, %1;" : "=f"(f.inv) : "f"(f.scale));
     return f;
+}
+
+// Whether a row's Stats have left fp32's range although its y need not: the
+// squares of |h| above 1.8e19 / sqrt(cols) sum to infinity, those below 2^-63 lose
+// their last bits (eps not covering them), and h w may do either before rstd
+// brings it back.  Such a row's Stats are taken again from h f with f = 2^-n near
+// 1 / max(max|h|, sqrt(eps)): y = h f / sqrt(mean((h f)^2) + eps f^2) * w, every
+// product by f exact.  (Rows of zeros keep their Stats; without a weight only
+// max|h| counts, which is exact.)
+__device__ __forceinline__ bool out_of_range(const NormLaunch& p, Stats s) {
+    if (!p.weight) return false;
+    const float v = fmaf(s.ss, p.inv_cols, p.eps);
+    if (!(v >= 0x1p-100f && v <= FLT_MAX)) return true;
+    return p.scale && (!(s.am <= FLT_MAX) || (s.am < 0x1p-100f && s.ss > 0.0f));
+}
+// f, 1 for what is not finite; m = max|h|.
+__device__ __forceinline__ float range_factor(float m, float eps) {
+    const float t = max_nan(m, sqrtf(eps));
+    const int e = min(max(__float_as_int(t) >> 23, 1), 253);
+    return t <= FLT_MAX ? __int_as_float((254 - e) << 23) : 1.0f;
 }
 
 // A row in registers: thread t of the row's `threads` holds packs t, t +
@@ -238,9 +258,45 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH))
         }
     }
     s = WARP ? warp_join(s) : block_join(s, buf);
-    const Factors f = row_factors(p, s);
-    if (p.scale && t == 0) p.scale[row] = f.scale;
     T* ro = static_cast<T*>(p.residual_out) + row * p.ldro;
+    float eps = p.eps;
+    bool summed = p.residual_out == nullptr;  // nothing of h itself is left to write
+    if (out_of_range(p, s)) {
+        Stats m = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+            if (t + c * threads < packs) {
+                P o;
+                if (!summed) {
+                    o.set(h[c]);
+                    o.store(ro + (t + c * threads) * VEC);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) m.am = max_nan(m.am, fabsf(h[c][e]));
+            }
+        summed = true;
+        if (!WARP) __syncthreads();  // buf has been read
+        m = WARP ? warp_join(m) : block_join(m, buf);
+        const float f = range_factor(m.am, eps);
+        eps = eps * f * f;
+        s = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+            if (t + c * threads < packs) {
+                float g[VEC];
+                wv[c].get(g);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    h[c][e] *= f;
+                    s.ss = fmaf(h[c][e], h[c][e], s.ss);
+                    s.am = max_nan(s.am, fabsf(h[c][e] * g[e]));
+                }
+            }
+        if (!WARP) __syncthreads();
+        s = WARP ? warp_join(s) : block_join(s, buf);
+    }
+    const Factors f = row_factors(p, s, eps);
+    if (p.scale && t == 0) p.scale[row] = f.scale;
     T* yo = static_cast<T*>(p.y) + row * p.ldy;
     uint8_t* q = static_cast<uint8_t*>(p.q) + row * p.ldq;
 #pragma unroll
@@ -248,7 +304,7 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH))
         const int i = (t + c * threads) * VEC;
         if (t + c * threads < packs) {
             P o;
-            if (p.residual_out) {
+            if (!summed) {
                 o.set(h[c]);
                 o.store(ro + i);
             }
@@ -369,7 +425,25 @@ __global__ void __launch_bounds__(512) staged_kernel(const NormLaunch p, const S
 #pragma unroll
             for (int e = 0; e < VEC; ++e) am = max_nan(am, fabsf(h[e] * g[e]));
         }
-    const Factors f = row_factors(p, block_join({ss, am}, buf));
+    Stats s = block_join({ss, am}, buf);
+    float eps = p.eps;
+    if (out_of_range(p, s)) {
+        float m = 0.0f;
+        for (int i = t; i < n; i += nt) m = max_nan(m, fabsf(hb[at(i)]));
+        __syncthreads();  // buf has been read
+        const float f = range_factor(block_join({0.0f, m}, buf).am, eps);
+        eps = eps * f * f;
+        s = {0.0f, 0.0f};
+        for (int i = t; i < n; i += nt) {
+            const float h = hb[at(i)] * f;
+            hb[at(i)] = h;
+            s.ss = fmaf(h, h, s.ss);
+            s.am = max_nan(s.am, fabsf(h * to_f32(w[i])));
+        }
+        __syncthreads();
+        s = block_join(s, buf);
+    }
+    const Factors f = row_factors(p, s, eps);
     if (p.scale && t == 0) p.scale[row] = f.scale;
     if (!yo && !q) return;
     const bool y_turned = yo && st.y_same && !st.y_vec;  // y leaves by way of shared memory
@@ -443,11 +517,28 @@ __global__ void __launch_bounds__(1024) wide_kernel(const NormLaunch p) {
         s.am = max_nan(s.am, fabsf(w ? h * to_f32(w[i]) : h));
     }
     s = block_join(s, buf);
-    const Factors f = row_factors(p, s);
+    float eps = p.eps, by = 1.0f;
+    if (out_of_range(p, s)) {
+        float m = 0.0f;
+        for (int i = threadIdx.x; i < n; i += blockDim.x)
+            m = max_nan(m, fabsf(to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f)));
+        __syncthreads();  // buf has been read
+        by = range_factor(block_join({0.0f, m}, buf).am, eps);
+        eps = eps * by * by;
+        s = {0.0f, 0.0f};
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            const float h = (to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f)) * by;
+            s.ss = fmaf(h, h, s.ss);
+            s.am = max_nan(s.am, fabsf(h * to_f32(w[i])));
+        }
+        __syncthreads();
+        s = block_join(s, buf);
+    }
+    const Factors f = row_factors(p, s, eps);
     if (p.scale && threadIdx.x == 0) p.scale[row] = f.scale;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const float h = to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f);
-        const float y = w ? h * f.rstd * to_f32(w[i]) : h;
+        const float y = w ? h * by * f.rstd * to_f32(w[i]) : h;
         if (p.residual_out) static_cast<T*>(p.residual_out)[row * p.ldro + i] = from_f32<T>(h);
         if (p.y) static_cast<T*>(p.y)[row * p.ldy + i] = from_f32<T>(y);
         const float qv[1] = {y * f.inv};

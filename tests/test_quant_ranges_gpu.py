@@ -72,3 +72,90 @@ def test_quantize_fp8_infinities_in_many_rows_of_odd_width(rows, cols, dtype):
     assert torch.isnan(q.float()).all(dim=1).cpu()[bad].all()
     R.check_q(q.float().cpu()[~bad], scale.cpu()[~bad], R.f64(x[~bad]), "q", rel=1e-6)
     assert np.isfinite(R.f64(scale)[~bad.numpy()]).all()
+
+
+def check_norm(x, r, w, eps, what, rows=None):
+    """All outputs of a call, of all or some of its rows, against the 64-bit form."""
+    n, cols = x.shape
+    ro, y = (torch.empty(n, cols, dtype=x.dtype, device="cuda") for _ in range(2))
+    q, scale = outputs(n, cols)
+    Q.add_rmsnorm(x.cuda(), w.cuda(), r.cuda() if r is not None else None, eps=eps, residual_out=ro, y=y, q=q,
+                  scale=scale)
+    eps = float(np.float32(eps))
+    rows = list(range(n)) if rows is None else rows
+    h, ref = R.norm(x[rows], w, r[rows] if r is not None else None, eps)
+    R.check_rounded(ro[rows], h, 2.0 ** -24, 0.0, f"{what}: residual_out")
+    R.check_rounded(y[rows], ref, R.NORM_REL, 0.0, f"{what}: y")
+    R.check_q(q[rows].float(), scale[rows], ref, f"{what}: q")
+    alone = torch.empty_like(y)  # without the 8-bit outputs
+    Q.add_rmsnorm(x.cuda(), w.cuda(), r.cuda() if r is not None else None, eps=eps, y=alone)
+    R.check_rounded(alone[rows], ref, R.NORM_REL, 0.0, f"{what}: y alone")
+    return ro, y, q, scale
+
+
+# The squares of 3e17 sum to infinity only in long rows; 2^-70 and less lose bits or vanish.
+SIZES = [3e17, 2e19, 1e30, 4e37, 2.0 ** -50, 2.0 ** -65, 2.0 ** -73, 1e-25, 1e-38, 2.0 ** -130]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("with_residual", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-6])
+def test_norm_rows_whose_squares_leave_the_range(eps, with_residual, cols, dtype):
+    """Large and small rows side by side with ordinary ones."""
+    size = torch.tensor([1.0] + SIZES + [0.5])[:, None]
+    # 7-bit values, which fp32 holds down to 2^-142 and bf16 down to 2^-126
+    x = (torch.randint(64, 128, (len(size), cols), generator=torch.Generator().manual_seed(5)) / 64.0 * size).to(dtype)
+    x[:, ::3] *= -1
+    r = (x.float() * 0.25).flip(1).to(dtype) if with_residual else None
+    w = (1 + 0.1 * rand(6, cols)).to(dtype)
+    check_norm(x, r, w, eps, f"{cols} columns")
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_norm_products_with_the_weight_that_leave_the_range(cols):
+    """h w overflows or vanishes where y = h w / rms is an ordinary number."""
+    x = rand(7, 3, cols) * torch.tensor([1e15, 1.0, 3e-9])[:, None]
+    check_norm(x, None, 1e25 * (1 + rand(8, cols).abs()), 0.0, "large weights")
+    check_norm(x, None, 1e-33 * (1 + rand(9, cols).abs()), 0.0, "small weights")
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_norm_rows_of_zeros(cols):
+    x = rand(10, 3, cols)
+    x[1] = 0
+    w = torch.ones(cols)
+    for eps in (1e-36, 1e-6):
+        _, y, q, scale = check_norm(x, None, w, eps, f"eps {eps}")
+        assert not y[1].any() and not q[1].float().any() and scale[1].item() == R.SCALE_MIN
+    _, y, q, scale = check_norm(x, None, w, 0.0, "eps 0", rows=[0, 2])
+    assert torch.isnan(y[1]).all() and torch.isnan(q[1].float()).all() and torch.isnan(scale[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,cols", [(2000, 1503), (2000, 2999)])
+def test_norm_ranges_in_many_rows_of_odd_width(rows, cols, dtype):
+    size = torch.tensor(SIZES)[torch.arange(rows) % len(SIZES)][:, None]
+    x = (torch.randint(64, 128, (rows, cols), generator=torch.Generator().manual_seed(11)) / 64.0 * size).to(dtype)
+    check_norm(x, None, (1 + 0.1 * rand(12, cols)).to(dtype), 0.0, "many rows")
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_norm_ranges_in_place(cols):
+    """residual_out over the residual and y over x, also where h is read twice."""
+    x = rand(13, 2, cols) * torch.tensor([1e25, 1e-25])[:, None]
+    r = rand(14, 2, cols) * torch.tensor([1e25, 1e-25])[:, None]
+    w = 1 + 0.1 * rand(15, cols)
+    dx, dr = x.cuda(), r.cuda()
+    Q.add_rmsnorm(dx, w.cuda(), dr, eps=0.0, residual_out=dr, y=dx)
+    h, y = R.norm(x, w, r, 0.0)
+    # h is one rounded addition, whose error a cancellation leaves whole: off by 2^-24 of |x| + |r| at most
+    R.check_rounded(dr, h, 2.0 ** -24, 0.0, "residual_out")
+    R.check_rounded(dx, y, R.NORM_REL, 0.0, "y")
+
+
+def test_quantize_fp8_of_large_and_small_values_is_as_it_was():
+    x = rand(16, 3, 4096) * torch.tensor([1e37, 1.0, 1e-30])[:, None]
+    q, scale = outputs(3, 4096)
+    Q.quantize_fp8(x.cuda(), q, scale)
+    R.check_q(q.float(), scale, R.f64(x), "q", rel=1e-6)
