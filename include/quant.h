@@ -84,7 +84,7 @@ typedef struct {
  * of h or of y makes that row's q and scale NaN, and y what the formula gives
  * (a row of zeros with eps = 0: NaN).  A row whose squares, or their sum, leave
  * fp32's range is scaled by a power of two first: every finite h has its y.
- * cols = 0 writes scale alone.
+ * cols = 0 writes scale alone, 2^-126 a row.
  */
 int add_rmsnorm(int64_t rows, int64_t cols, const void* x, int64_t ldx, const void* residual,
                 int64_t ldr, const void* weight, float eps, int dtype, void* residual_out,

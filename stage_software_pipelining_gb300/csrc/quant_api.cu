@@ -64,9 +64,8 @@ int add_rmsnorm(int64_t rows, int64_t cols, const void* x, int64_t ldx, const vo
                 int64_t ldro, void* y, int64_t ldy, void* q, int64_t ldq, float* scale,
                 void* stream) {
     if (weight == nullptr && rows > 0 && cols > 0) return GEMM_ERR_ARG;
-    // rows without elements: any pointer says "with the norm"
-    const void* w = weight ? weight : reinterpret_cast<const void*>(static_cast<uintptr_t>(256));
-    return norm_checked({rows, cols, x, ldx, residual, ldr, w, eps, dtype, residual_out, ldro, y,
+    // Rows without elements have no mean to divide by, only the least scale.
+    return norm_checked({rows, cols, x, ldx, residual, ldr, cols > 0 ? weight : nullptr, eps, dtype, residual_out, ldro, y,
                          ldy, q, ldq, scale},
                         stream);
 }

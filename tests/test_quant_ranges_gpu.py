@@ -159,3 +159,13 @@ def test_quantize_fp8_of_large_and_small_values_is_as_it_was():
     q, scale = outputs(3, 4096)
     Q.quantize_fp8(x.cuda(), q, scale)
     R.check_q(q.float(), scale, R.f64(x), "q", rel=1e-6)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-6])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_norm_rows_without_elements_have_the_least_scale(dtype, eps):
+    x = torch.empty(5, 0, dtype=dtype, device="cuda")
+    q, scale = outputs(5, 0)
+    scale.fill_(7.0)
+    Q.add_rmsnorm(x, torch.empty(0, dtype=dtype, device="cuda"), eps=eps, q=q, scale=scale)
+    assert (scale.cpu() == R.SCALE_MIN).all()
