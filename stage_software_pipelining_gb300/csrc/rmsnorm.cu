@@ -510,9 +510,11 @@ __global__ void __launch_bounds__(1024) wide_kernel(const NormLaunch p) {
     const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
     const T* w = static_cast<const T*>(p.weight);
     const int n = static_cast<int>(p.cols);
+    // Without a residual x itself, the sign of a zero included.
+    auto h_at = [&](int i) { return r ? to_f32(x[i]) + to_f32(r[i]) : to_f32(x[i]); };
     Stats s = {0.0f, 0.0f};
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const float h = to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f);
+        const float h = h_at(i);
         s.ss = fmaf(h, h, s.ss);
         s.am = max_nan(s.am, fabsf(w ? h * to_f32(w[i]) : h));
     }
@@ -521,13 +523,13 @@ __global__ void __launch_bounds__(1024) wide_kernel(const NormLaunch p) {
     if (out_of_range(p, s)) {
         float m = 0.0f;
         for (int i = threadIdx.x; i < n; i += blockDim.x)
-            m = max_nan(m, fabsf(to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f)));
+            m = max_nan(m, fabsf(h_at(i)));
         __syncthreads();  // buf has been read
         by = range_factor(block_join({0.0f, m}, buf).am, eps);
         eps = eps * by * by;
         s = {0.0f, 0.0f};
         for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const float h = (to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f)) * by;
+            const float h = h_at(i) * by;
             s.ss = fmaf(h, h, s.ss);
             s.am = max_nan(s.am, fabsf(h * to_f32(w[i])));
         }
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(1024) wide_kernel(const NormLaunch p) {
     const Factors f = row_factors(p, s, eps);
     if (p.scale && threadIdx.x == 0) p.scale[row] = f.scale;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const float h = to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f);
+        const float h = h_at(i);
         const float y = w ? h * by * f.rstd * to_f32(w[i]) : h;
         if (p.residual_out) static_cast<T*>(p.residual_out)[row * p.ldro + i] = from_f32<T>(h);
         if (p.y) static_cast<T*>(p.y)[row * p.ldy + i] = from_f32<T>(y);

@@ -169,3 +169,18 @@ def test_norm_rows_without_elements_have_the_least_scale(dtype, eps):
     scale.fill_(7.0)
     Q.add_rmsnorm(x, torch.empty(0, dtype=dtype, device="cuda"), eps=eps, q=q, scale=scale)
     assert (scale.cpu() == R.SCALE_MIN).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("cols", COLS)
+def test_norm_keeps_the_sign_of_zeros(cols, dtype):
+    """Without a residual h is x: a -0 stays one in every output."""
+    x = rand(17, 2, cols).to(dtype)
+    x[:, ::2] = -0.0
+    ro, y = (torch.empty(2, cols, dtype=dtype, device="cuda") for _ in range(2))
+    q, scale = outputs(2, cols)
+    Q.add_rmsnorm(x.cuda(), torch.ones(cols, dtype=dtype, device="cuda"), residual_out=ro, y=y, q=q, scale=scale)
+    Q.quantize_fp8(x.cuda(), (q2 := torch.empty_like(q)), scale)
+    assert torch.equal(ro.cpu(), x)
+    for out in (ro, y, q.float(), q2.float()):
+        assert torch.equal(torch.signbit(out).cpu(), torch.signbit(x))
