@@ -182,7 +182,9 @@ __device__ __forceinline__ Factors row_factors(const NormLaunch& p, Stats s, flo
 // product by f exact.  (Rows of zeros keep their Stats; without a weight only
 // max|h| counts, which is exact.)
 __device__ __forceinline__ bool out_of_range(const NormLaunch& p, Stats s) {
-    if (!p.weight) return false;
+    // Two comparisons settle ordinary rows (2^-100 to FLT_MAX, as integers).
+    auto ordinary = [](float v) { return __float_as_uint(v) - 0x0d800000u <= 0x7f7fffffu - 0x0d800000u; };
+    if (!p.weight || (ordinary(fmaf(s.ss, p.inv_cols, p.eps)) && ordinary(s.am))) return false;
     const float v = fmaf(s.ss, p.inv_cols, p.eps);
     if (!(v >= 0x1p-100f && v <= FLT_MAX)) return true;
     return p.scale && (!(s.am <= FLT_MAX) || (s.am < 0x1p-100f && s.ss > 0.0f));
@@ -192,6 +194,64 @@ __device__ __forceinline__ float range_factor(float m, float eps) {
     const float t = max_nan(m, sqrtf(eps));
     const int e = min(max(__float_as_int(t) >> 23, 1), 253);
     return t <= FLT_MAX ? __int_as_float((254 - e) << 23) : 1.0f;
+}
+
+// h of element i of a row; without a residual x itself, the sign of a zero included.
+template <typename T>
+struct RowIn {
+    const T *x, *r, *w;
+    __device__ __forceinline__ RowIn(const NormLaunch& p, long long row)
+        : x(static_cast<const T*>(p.x) + row * p.ldx),
+          r(p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr),
+          w(static_cast<const T*>(p.weight)) {}
+    __device__ __forceinline__ float h(int i) const { return r ? to_f32(x[i]) + to_f32(r[i]) : to_f32(x[i]); }
+};
+
+// The Stats of a row out of range, read again by its threads, of which this is
+// the t-th: f, with s and eps as row_factors wants them for h f.
+template <typename T, bool WARP>
+__device__ __forceinline__ float scaled_stats(const NormLaunch& p, long long row, int t, int threads, Stats* buf,
+                                              Stats& s, float& eps) {
+    const RowIn<T> in(p, row);
+    const int n = static_cast<int>(p.cols);
+    auto join = [&](Stats v) {
+        if (WARP) return warp_join(v);
+        __syncthreads();  // buf has been read
+        return block_join(v, buf);
+    };
+    float m = 0.0f;
+#pragma unroll 1
+    for (int i = t; i < n; i += threads) m = max_nan(m, fabsf(in.h(i)));
+    const float f = range_factor(join({0.0f, m}).am, eps);
+    eps = eps * f * f;
+    s = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int i = t; i < n; i += threads) {
+        const float h = in.h(i) * f;
+        s.ss = fmaf(h, h, s.ss);
+        s.am = max_nan(s.am, fabsf(h * to_f32(in.w[i])));
+    }
+    s = join(s);
+    return f;
+}
+
+// A row's outputs, read again; `by` scales h as the Factors expect.  Every element
+// is read and written by the same thread, so outputs may lie over inputs.
+template <typename T>
+__device__ __forceinline__ void write_row(const NormLaunch& p, long long row, int t, int threads, const Factors& f,
+                                          float by) {
+    const RowIn<T> in(p, row);
+    const int n = static_cast<int>(p.cols);
+    if (p.scale && t == 0) p.scale[row] = f.scale;
+#pragma unroll 1
+    for (int i = t; i < n; i += threads) {
+        const float h = in.h(i);
+        const float y = in.w ? h * by * f.rstd * to_f32(in.w[i]) : h;
+        if (p.residual_out) static_cast<T*>(p.residual_out)[row * p.ldro + i] = from_f32<T>(h);
+        if (p.y) static_cast<T*>(p.y)[row * p.ldy + i] = from_f32<T>(y);
+        const float qv[1] = {y * f.inv};
+        if (p.q) store_q<1>(static_cast<uint8_t*>(p.q) + row * p.ldq + i, qv);
+    }
 }
 
 // A row in registers: thread t of the row's `threads` holds packs t, t +
@@ -259,43 +319,15 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH))
     }
     s = WARP ? warp_join(s) : block_join(s, buf);
     T* ro = static_cast<T*>(p.residual_out) + row * p.ldro;
-    float eps = p.eps;
-    bool summed = p.residual_out == nullptr;  // nothing of h itself is left to write
+    // Nothing is written yet: such a row is read again, which leaves the others'
+    // registers as they are (h kept through the branch cost 5 to 13 % on short rows).
     if (out_of_range(p, s)) {
-        Stats m = {0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-            if (t + c * threads < packs) {
-                P o;
-                if (!summed) {
-                    o.set(h[c]);
-                    o.store(ro + (t + c * threads) * VEC);
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) m.am = max_nan(m.am, fabsf(h[c][e]));
-            }
-        summed = true;
-        if (!WARP) __syncthreads();  // buf has been read
-        m = WARP ? warp_join(m) : block_join(m, buf);
-        const float f = range_factor(m.am, eps);
-        eps = eps * f * f;
-        s = {0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-            if (t + c * threads < packs) {
-                float g[VEC];
-                wv[c].get(g);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    h[c][e] *= f;
-                    s.ss = fmaf(h[c][e], h[c][e], s.ss);
-                    s.am = max_nan(s.am, fabsf(h[c][e] * g[e]));
-                }
-            }
-        if (!WARP) __syncthreads();
-        s = WARP ? warp_join(s) : block_join(s, buf);
+        float eps = p.eps;
+        const float by = scaled_stats<T, WARP>(p, row, t, threads, buf, s, eps);
+        write_row<T>(p, row, t, threads, row_factors(p, s, eps), by);
+        return;
     }
-    const Factors f = row_factors(p, s, eps);
+    const Factors f = row_factors(p, s, p.eps);
     if (p.scale && t == 0) p.scale[row] = f.scale;
     T* yo = static_cast<T*>(p.y) + row * p.ldy;
     uint8_t* q = static_cast<uint8_t*>(p.q) + row * p.ldq;
@@ -304,7 +336,7 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH))
         const int i = (t + c * threads) * VEC;
         if (t + c * threads < packs) {
             P o;
-            if (!summed) {
+            if (p.residual_out) {
                 o.set(h[c]);
                 o.store(ro + i);
             }
@@ -429,11 +461,13 @@ __global__ void __launch_bounds__(512) staged_kernel(const NormLaunch p, const S
     float eps = p.eps;
     if (out_of_range(p, s)) {
         float m = 0.0f;
+#pragma unroll 1
         for (int i = t; i < n; i += nt) m = max_nan(m, fabsf(hb[at(i)]));
         __syncthreads();  // buf has been read
         const float f = range_factor(block_join({0.0f, m}, buf).am, eps);
         eps = eps * f * f;
         s = {0.0f, 0.0f};
+#pragma unroll 1
         for (int i = t; i < n; i += nt) {
             const float h = hb[at(i)] * f;
             hb[at(i)] = h;
@@ -498,54 +532,25 @@ __global__ void __launch_bounds__(512) staged_kernel(const NormLaunch p, const S
 }
 
 // A row too long for shared memory as well: one pass for its Stats, one that
-// reads it again and writes.  Every element is read and written by the same
-// thread, so outputs may lie over inputs.
+// reads it again and writes.
 template <typename T>
 __global__ void __launch_bounds__(1024) wide_kernel(const NormLaunch p) {
     __shared__ Stats buf[32];
     griddep_launch_dependents();
     griddep_wait();
     const long long row = blockIdx.x;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
-    const T* w = static_cast<const T*>(p.weight);
-    const int n = static_cast<int>(p.cols);
-    // Without a residual x itself, the sign of a zero included.
-    auto h_at = [&](int i) { return r ? to_f32(x[i]) + to_f32(r[i]) : to_f32(x[i]); };
+    const int t = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x), n = static_cast<int>(p.cols);
+    const RowIn<T> in(p, row);
     Stats s = {0.0f, 0.0f};
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const float h = h_at(i);
+    for (int i = t; i < n; i += threads) {
+        const float h = in.h(i);
         s.ss = fmaf(h, h, s.ss);
-        s.am = max_nan(s.am, fabsf(w ? h * to_f32(w[i]) : h));
+        s.am = max_nan(s.am, fabsf(in.w ? h * to_f32(in.w[i]) : h));
     }
     s = block_join(s, buf);
     float eps = p.eps, by = 1.0f;
-    if (out_of_range(p, s)) {
-        float m = 0.0f;
-        for (int i = threadIdx.x; i < n; i += blockDim.x)
-            m = max_nan(m, fabsf(h_at(i)));
-        __syncthreads();  // buf has been read
-        by = range_factor(block_join({0.0f, m}, buf).am, eps);
-        eps = eps * by * by;
-        s = {0.0f, 0.0f};
-        for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const float h = h_at(i) * by;
-            s.ss = fmaf(h, h, s.ss);
-            s.am = max_nan(s.am, fabsf(h * to_f32(w[i])));
-        }
-        __syncthreads();
-        s = block_join(s, buf);
-    }
-    const Factors f = row_factors(p, s, eps);
-    if (p.scale && threadIdx.x == 0) p.scale[row] = f.scale;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const float h = h_at(i);
-        const float y = w ? h * by * f.rstd * to_f32(w[i]) : h;
-        if (p.residual_out) static_cast<T*>(p.residual_out)[row * p.ldro + i] = from_f32<T>(h);
-        if (p.y) static_cast<T*>(p.y)[row * p.ldy + i] = from_f32<T>(y);
-        const float qv[1] = {y * f.inv};
-        if (p.q) store_q<1>(static_cast<uint8_t*>(p.q) + row * p.ldq + i, qv);
-    }
+    if (out_of_range(p, s)) by = scaled_stats<T, false>(p, row, t, threads, buf, s, eps);
+    write_row<T>(p, row, t, threads, row_factors(p, s, eps), by);
 }
 
 using Kernel = void (*)(const NormLaunch);
@@ -568,7 +573,7 @@ int launch(void (*k)(Args...), int64_t grid, int threads, size_t smem, cudaStrea
 
 // Rows whose packs (VEC elements) are whole and aligned.  Few threads with
 // several packs each hold more loads in flight for their registers than many
-// with one, and their reductions cost less: 8191 x 8192 bf16 with q takes 68 us
+// with one, and their reductions cost less: 8191 x 8192 bf16 with q takes 69 us
 // with 256 threads of 4 packs (the bytes at 6.87 TB/s), 77 with 512 of 2 and 85
 // with 1024 of 1.  Where rows are fewer than two an SM, one row's time counts:
 // one pack a thread, as many threads as that takes.  False: not for these rows.
