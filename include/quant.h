@@ -70,7 +70,8 @@ typedef struct {
  *     q = e4m3(y / scale)                     (nearest even)
  *
  * in fp32, each output rounded once from the fp32 value: residual_out is h,
- * and the norm goes on from the unrounded h.
+ * and the norm goes on from the unrounded h.  The scale is correctly rounded, and a
+ * quotient half-way between two e4m3 values goes to the even one.
  *   dtype         a quant_type_t: the type of x, residual, weight,
  *                 residual_out and y
  *   residual      may be NULL; residual_out, y, and q with scale may be NULL

@@ -112,20 +112,6 @@ struct Pack<T, 1> {
     __device__ __forceinline__ void set(const float (&f)[1]) { u = from_f32<T>(f[0]); }
 };
 
-template <int VEC>
-__device__ __forceinline__ void store_q(uint8_t* q, const float (&y)[VEC]) {
-    if constexpr (VEC == 1) {
-        *q = __nv_cvt_float_to_fp8(y[0], __NV_SATFINITE, __NV_E4M3);
-    } else {
-        alignas(VEC) uint16_t v[VEC / 2];
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e)
-            v[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e], y[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
-        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(v);
-        else *reinterpret_cast<uint32_t*>(q) = *reinterpret_cast<const uint32_t*>(v);
-    }
-}
-
 struct Stats {
     float ss;  // sum of h^2
     float am;  // max |h w|, or max |h| without a norm
@@ -160,18 +146,88 @@ __device__ __forceinline__ Stats block_join(Stats s, Stats* buf) {
 
 // rstd, scale and 1/scale of a row from its Stats.  A row whose largest y is not
 // finite has neither a scale nor 8-bit values: both are NaN, also where the
-// formula would give an infinite scale and zeros.  (The reciprocals are within an
-// ulp, and a scale that is a number lies in [2^-126, 2^120].)
+// formula would give an infinite scale and zeros.  (A scale that is a number lies
+// in [2^-126, 2^120], so 1/scale is one too.)
+//
+// Quotients often lie half-way between two e4m3 values where the scale has few
+// bits (largest 21 of small integers: 57/64 over 3/64 is 19) and must not be off
+// by an ulp there.  So the scale, max / 448, is correctly rounded (what the product
+// with the rounded reciprocal leaves of the dividend is exact, and its share closes
+// the gap: Markstein's division), and 1/scale is held in two parts, 2^-46 off at
+// most: y inv + y rest is then rounded once, and exact where the quotient is.  The
+// second part is positive, so that both products of a -0 are one.
 struct Factors {
-    float rstd, scale, inv;
+    float rstd, scale, inv, rest;
 };
 __device__ __forceinline__ Factors row_factors(const NormLaunch& p, Stats s, float eps) {
     Factors f;
     f.rstd = p.weight ? rsqrtf(fmaf(s.ss, p.inv_cols, eps)) : 1.0f;
     const float most = f.rstd * s.am;
-    f.scale = most <= FLT_MAX ? fmaxf(most * (1.0f / kE4m3Max), kScaleMin) : __int_as_float(0x7fffffff);
-    asm("rcp.approx.f32 %0, %1;" : "=f"(f.inv) : "f"(f.scale));
+    constexpr float kInv = 1.0f / kE4m3Max;
+    const float v = most * kInv;
+    f.scale = most <= FLT_MAX ? fmaxf(fmaf(fmaf(-v, kE4m3Max, most), kInv, v), kScaleMin) : __int_as_float(0x7fffffff);
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(f.scale));  // within an ulp
+    f.inv = __int_as_float(__float_as_int(r) - 1);            // and below 1/scale
+    f.rest = fmaf(-f.scale, f.inv, 1.0f) * f.inv;
     return f;
+}
+
+// Two products or multiply-adds in one instruction, rounded as two.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// y = h rstd g.
+template <int VEC>
+__device__ __forceinline__ void normed(const float (&h)[VEC], const float (&g)[VEC], const Factors& f, float (&y)[VEC]) {
+    if constexpr (VEC == 1) {
+        y[0] = h[0] * f.rstd * g[0];
+    } else {
+        const uint64_t rstd = two(f.rstd, f.rstd);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const uint64_t v = mul2(mul2(two(h[e], h[e + 1]), rstd), two(g[e], g[e + 1]));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(y[e]), "=f"(y[e + 1]) : "l"(v));
+        }
+    }
+}
+
+// e4m3(y / scale).
+template <int VEC>
+__device__ __forceinline__ void store_q(uint8_t* q, const float (&y)[VEC], const Factors& f) {
+    if constexpr (VEC == 1) {
+        *q = __nv_cvt_float_to_fp8(fmaf(y[0], f.inv, y[0] * f.rest), __NV_SATFINITE, __NV_E4M3);
+    } else {
+        const uint64_t inv = two(f.inv, f.inv), rest = two(f.rest, f.rest);
+        alignas(VEC) uint16_t v[VEC / 2];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const uint64_t yy = two(y[e], y[e + 1]), r = fma2(yy, inv, mul2(yy, rest));
+            float2 o;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+            v[e / 2] = __nv_cvt_float2_to_fp8x2(o, __NV_SATFINITE, __NV_E4M3);
+        }
+        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(v);
+        else *reinterpret_cast<uint32_t*>(q) = *reinterpret_cast<const uint32_t*>(v);
+    }
 }
 
 // Whether a row's Stats have left fp32's range although its y need not: the
@@ -249,8 +305,8 @@ __device__ __forceinline__ void write_row(const NormLaunch& p, long long row, in
         const float y = in.w ? h * by * f.rstd * to_f32(in.w[i]) : h;
         if (p.residual_out) static_cast<T*>(p.residual_out)[row * p.ldro + i] = from_f32<T>(h);
         if (p.y) static_cast<T*>(p.y)[row * p.ldy + i] = from_f32<T>(y);
-        const float qv[1] = {y * f.inv};
-        if (p.q) store_q<1>(static_cast<uint8_t*>(p.q) + row * p.ldq + i, qv);
+        const float one[1] = {y};
+        if (p.q) store_q<1>(static_cast<uint8_t*>(p.q) + row * p.ldq + i, one, f);
     }
 }
 
@@ -309,11 +365,23 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH))
             rv[c].get(b);
             wv[c].get(g);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float v = a[e] + b[e];
-                h[c][e] = v;
-                s.ss = fmaf(v, v, s.ss);
-                s.am = max_nan(s.am, fabsf(v * g[e]));
+            for (int e = 0; e < VEC; e += 2) {
+                if constexpr (VEC == 1) {
+                    const float v = a[e] + b[e];
+                    h[c][e] = v;
+                    s.ss = fmaf(v, v, s.ss);
+                    s.am = max_nan(s.am, fabsf(v * g[e]));
+                } else {
+                    const uint64_t v = add2(two(a[e], a[e + 1]), two(b[e], b[e + 1]));
+                    const uint64_t u = mul2(v, two(g[e], g[e + 1]));
+                    float2 o;
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(h[c][e]), "=f"(h[c][e + 1]) : "l"(v));
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(u));
+                    s.ss = fmaf(h[c][e], h[c][e], s.ss);
+                    s.ss = fmaf(h[c][e + 1], h[c][e + 1], s.ss);
+                    s.am = max_nan(s.am, fabsf(o.x));
+                    s.am = max_nan(s.am, fabsf(o.y));
+                }
             }
         }
     }
@@ -342,17 +410,12 @@ __global__ void __launch_bounds__(WARP ? 128 : max_threads(sizeof(T), VEC, NCH))
             }
             float g[VEC], y[VEC];
             wv[c].get(g);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = h[c][e] * f.rstd * g[e];
+            normed(h[c], g, f, y);
             if (p.y) {
                 o.set(y);
                 o.store(yo + i);
             }
-            if (p.q) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) y[e] *= f.inv;
-                store_q<VEC>(q + i, y);
-            }
+            if (p.q) store_q<VEC>(q + i, y, f);
         }
     }
 }
@@ -485,8 +548,7 @@ __global__ void __launch_bounds__(512) staged_kernel(const NormLaunch p, const S
         float h[VEC], g[VEC];
         both(i, h, g);
         const bool whole = i + VEC <= n;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) h[e] = h[e] * f.rstd * g[e];
+        normed(h, g, f, h);
         if (yo) {
             if (y_turned) {
 #pragma unroll
@@ -503,21 +565,20 @@ __global__ void __launch_bounds__(512) staged_kernel(const NormLaunch p, const S
             }
         }
         if (q) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) h[e] *= f.inv;
             if (whole && st.q_vec) {
-                store_q<VEC>(q + i, h);
+                store_q<VEC>(q + i, h, f);
             } else {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float one[1] = {h[e]};
-                    if (i + e < n) store_q<1>(q + i + e, one);
+                    if (i + e < n) store_q<1>(q + i + e, one, f);
                 }
             }
         }
     }
     if (!y_turned) return;
     __syncthreads();
+#pragma unroll 1  // unrolled, fp16's takes 53 registers for 40: 8000 x 2541 with q 41.6 us for 38.5
     for (int j = t; j < packs; j += nt) {
         const int i = head + j * VEC;
         float y[VEC];

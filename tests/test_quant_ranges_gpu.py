@@ -184,3 +184,43 @@ def test_norm_keeps_the_sign_of_zeros(cols, dtype):
     assert torch.equal(ro.cpu(), x)
     for out in (ro, y, q.float(), q2.float()):
         assert torch.equal(torch.signbit(out).cpu(), torch.signbit(x))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("cols", [510, 4096, 20000, 46000])
+def test_quantize_fp8_half_way_between_two_values(cols, dtype):
+    """Rows of small multiples of 1/64 whose largest is an integer: many of
+    their quotients by the scale lie half-way between two e4m3 values and go to
+    the even one.  The scale is the nearest fp32 value to max / 448, the
+    quotient the nearest one to x / scale."""
+    top = torch.arange(7, 128)
+    x = torch.randint(0, 256, (len(top), cols), generator=torch.Generator().manual_seed(18)).float()
+    x = torch.minimum(x / 64 * 2.0 ** torch.randint(0, 6, x.shape, generator=torch.Generator().manual_seed(19)),
+                      top[:, None])
+    x[:, 1::2] *= -1
+    x[:, 0] = top
+    x = x.to(dtype)
+    q, scale = outputs(len(top), cols)
+    Q.quantize_fp8(x.cuda(), q, scale)
+    s = top.numpy().astype(np.float32) / np.float32(448)
+    assert np.array_equal(scale.cpu().numpy(), s)
+    quotient = x.float().numpy() / s[:, None]
+    assert quotient.dtype == np.float32 and np.isin(np.abs(quotient), ties()).sum() > 100
+    assert np.array_equal(R.f64(q.float()), R.e4m3(quotient.astype(np.float64)))
+
+
+def ties():
+    v = torch.arange(0, 127, dtype=torch.uint8).view(E4M3).double().numpy()
+    return (v[1:] + v[:-1]) / 2
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_norm_quantises_the_values_that_it_writes(cols):
+    """q is e4m3 of the fp32 quotient of y and scale, as both are written."""
+    x, r, w = rand(20, 5, cols), rand(21, 5, cols), 1 + 0.2 * rand(22, cols)
+    y = torch.empty(5, cols, device="cuda")
+    q, scale = outputs(5, cols)
+    Q.add_rmsnorm(x.cuda(), w.cuda(), r.cuda(), y=y, q=q, scale=scale)
+    quotient = y.cpu().numpy() / scale.cpu().numpy()[:, None]
+    assert quotient.dtype == np.float32
+    assert np.array_equal(R.f64(q.float()), R.e4m3(quotient.astype(np.float64)))
