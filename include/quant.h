@@ -169,9 +169,10 @@ int gemv_w4_plan(int64_t M, int64_t N, int64_t K, int group, int zeros, int dtyp
  * quantize_w4 -- a weight matrix (N x K, row-major, any quant_type_t) in the
  * form gemv_w4 reads, with scales of `scale_dtype` (QUANT_F16 or QUANT_BF16).
  * A group's scale is max|w|/7 with zero point 8 (zeros = NULL), or
- * (max(w,0) - min(w,0))/15 with zero point round(-min(w,0)/scale); it is
- * rounded to scale_dtype first, and w is then round(w/scale) + zero point,
- * limited to 0..15.  Weights are finite.  Arguments otherwise as gemv_w4; no
+ * (max(w,0) - min(w,0))/15 with zero point round(-min(w,0)/scale), limited to
+ * 15; it is rounded to scale_dtype first (to its largest finite value at most),
+ * and w is then round(w/scale) + zero point, limited to 0..15, round to nearest
+ * even and round(w/0) = 0.  Weights are finite.  Arguments otherwise as gemv_w4; no
  * alignment beyond the elements' own, and ldw need only be >= K/2.
  */
 int quantize_w4(int64_t N, int64_t K, const void* w, int64_t ld, int dtype, int group, void* W,

@@ -10,6 +10,7 @@
 // once they are complete, so that no weight is rounded.  K is also cut over the
 // CTAs of a cluster, whose partials are added in order through distributed
 // shared memory.
+#include <cfloat>
 #include <type_traits>
 
 #include "gemv_w4.cuh"
@@ -414,15 +415,18 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const W4QuantLaunch p)
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    S s16 = of_f32<S>(p.zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f);
-    if (f32_of(s16) < 1.17549435e-38f) s16 = of_f32<S>(0.0f);  // below 2^-126, 1/scale overflows
+    // Weights too large for a scale of 16 bits take the largest one and are limited.
+    constexpr float kMostScale = std::is_same<S, __half>::value ? 65504.0f : 3.38953139e38f;
+    const float range = hi - lo <= FLT_MAX ? (hi - lo) / 15.0f : hi / 15.0f - lo / 15.0f;
+    const S s16 = of_f32<S>(fminf(p.zeros ? range : fmaxf(hi, -lo) / 7.0f, kMostScale));
     const float s = f32_of(s16);
-    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-    const float z = p.zeros ? fminf(rintf(-lo * inv), 15.0f) : 8.0f;
+    // Divisions, not products with 1/s: w / s is often half-way between two integers.
+    auto steps = [&](float w) { return s > 0.0f ? rintf(w / s) : 0.0f; };
+    const float z = p.zeros ? fminf(steps(-lo), 15.0f) : 8.0f;
     uint32_t word = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float q = fminf(fmaxf(rintf(v[e] * inv) + z, 0.0f), 15.0f);
+        const float q = fminf(fmaxf(steps(v[e]) + z, 0.0f), 15.0f);
         word |= static_cast<uint32_t>(q) << (4 * e);
     }
     if (!in) return;
