@@ -92,3 +92,26 @@ def test_weights_at_the_ends_of_the_range(size, zeros, stype):
     w = (torch.rand(9, 256, generator=torch.Generator().manual_seed(2)) * 2 - 1) * size
     q, scale = check(w, 64, zeros, stype)
     assert torch.isfinite(scale).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+@pytest.mark.parametrize("pitch", [0, 1, 8])
+def test_rows_on_any_address(pitch, offset, dtype):
+    """Rows of weights and of packed values that do not start on 16- and 4-byte
+    boundaries, and nothing written beside them."""
+    N, K, group = 7, 192, 64
+    w = torch.randn(N, K, generator=torch.Generator().manual_seed(3)).to(dtype)
+    buf = torch.full((N * (K + pitch) + offset,), float("nan"), dtype=dtype, device="cuda")
+    dw = buf[offset:].view(N, K + pitch)[:, :K]
+    dw.copy_(w)
+    packed = torch.full((N * (K // 2 + pitch) + offset + 3,), 0xA5, dtype=torch.uint8, device="cuda")
+    W = packed[offset:offset + N * (K // 2 + pitch)].view(N, K // 2 + pitch)[:, :K // 2]
+    s = torch.empty(N, K // group, dtype=BF16, device="cuda")
+    Q.quantize_w4(dw, W, s)
+    q, scale, _ = formula(w, group, False, BF16)
+    b = W.cpu().numpy()
+    assert np.array_equal(np.stack((b & 15, b >> 4), axis=2).reshape(N, K), q) and torch.equal(s.cpu(), scale)
+    outside = torch.ones_like(packed, dtype=torch.bool)
+    outside[offset:offset + N * (K // 2 + pitch)].view(N, K // 2 + pitch)[:, :K // 2] = False
+    assert (packed[outside] == 0xA5).all()
