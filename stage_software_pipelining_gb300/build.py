@@ -4,8 +4,9 @@ extension ``_quant.so`` that marshals torch tensors into its quantised operators
 Each ``csrc/*.cu`` file is compiled by its own ``nvcc -c`` and ``binding.cpp``
 by g++ (in parallel), then linked into
 ``stage_software_pipelining_gb300/libgemm.so`` against the shared CUDA runtime
-and ``_quant.so`` against libgemm.so and torch.  No cmake, one ``-gencode``: a cold build takes well under a
-minute, on the x86 dev host (cross-compiling) and on the Arm GPU host alike.
+and ``_quant.so`` against libgemm.so and torch.  No cmake, one ``-gencode``: a
+cold build takes well under a minute, on the x86 dev host (cross-compiling) and
+on the Arm GPU host alike.
 """
 from __future__ import annotations
 
@@ -82,7 +83,10 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 
 def _torch_dir() -> str:
     import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        raise RuntimeError("torch is not installed")
+    return os.path.dirname(spec.origin)
 
 
 def _compile_binding() -> str:
@@ -114,7 +118,8 @@ def _link_binding(obj: str) -> None:
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile and link libgemm.so and _quant.so if any source changed; return
-    libgemm.so's path."""
+    libgemm.so's path.  Where only the extension cannot be built, libgemm.so is
+    linked all the same before the error is raised."""
     if not force and not verbose_ptxas and not is_stale():
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -122,7 +127,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     libdir = cuda_lib_dir()
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared",
@@ -131,7 +135,11 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    # The library serves C callers where torch's or Python's headers are missing.
+    try:
+        _link_binding(binding.result())
+    except Exception as e:
+        raise RuntimeError(f"{LIB} is built, but not the Python extension {BINDING}: {e}") from e
     return LIB
 
 
