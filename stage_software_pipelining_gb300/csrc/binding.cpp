@@ -126,6 +126,15 @@ void* stream_of(PyObject* o, const Tensor& like) {
     return s;
 }
 
+bool truth_of(PyObject* o, const char* name) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) {
+        PyErr_Clear();
+        refuse(std::string(name) + " must be true or false");
+    }
+    return t != 0;
+}
+
 int group_of(int64_t K, int64_t groups) {
     const int64_t g = groups > 0 ? K / groups : 32;
     if (groups * g != K || (g != 32 && g != 64 && g != 128))
@@ -190,7 +199,7 @@ int gemm_fp8_(PyObject* const* a) {
     const float* sa = static_cast<const float*>(vector_of(*tensor(a[3], "a_scale"), "a_scale", at::kFloat, M, A));
     const float* sb = static_cast<const float*>(vector_of(*tensor(a[4], "b_scale"), "b_scale", at::kFloat, N, A));
     void* stream = stream_of(a[5], A);
-    const int checked = PyObject_IsTrue(a[6]);
+    const bool checked = truth_of(a[6], "checked");
     const c10::cuda::CUDAGuard guard(A.device());
     if (checked) {
         int st;
@@ -217,7 +226,7 @@ int gemv_w4_(PyObject* const* a) {
     const Rows C = rows_of(*tensor(a[3], "C"), "C", dt, M, N, x);
     const Rows Z = rows_or_none(a[4], "zeros", at::kByte, N, groups, x);
     void* stream = stream_of(a[5], x);
-    const int checked = PyObject_IsTrue(a[6]);
+    const bool checked = truth_of(a[6], "checked");
     const c10::cuda::CUDAGuard guard(x.device());
     if (checked) {
         int st;
