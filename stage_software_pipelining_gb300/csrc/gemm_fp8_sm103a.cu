@@ -25,7 +25,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
@@ -33,6 +32,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant.h"
+#include "tensor_copy.cuh"
 
 namespace ssp {
 
@@ -64,13 +64,6 @@ struct Fp8Params {
     unsigned long long wait_limit_ns;
     int withhold;
 };
-
-// Shared-memory matrix descriptor of a K-major operand: 128-byte rows, 8-row
-// groups 1024 bytes apart, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) |
-           (1ull << 46) | (2ull << 61);
-}
 
 __device__ __forceinline__ void record_timeout(int role, int iter) {
     if (atomicCAS(&g_fp8_status.code, 0, GEMM_ERR_TIMEOUT) == 0) {
@@ -104,14 +97,6 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
             }
         }
     }
-}
-
-// After an abort: no flag check, still bounded.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity,
-                                           unsigned long long limit_ns) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
 // Two accumulators times a row's scale and their columns' scales, in 16 bits.
@@ -284,8 +269,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (leader) {
-            const uint64_t a_desc0 = smem_desc(smem_addr(a_ring));
-            const uint64_t b_desc0 = smem_desc(smem_addr(b_ring));
+            const uint64_t a_desc0 = k_major_desc(smem_addr(a_ring));
+            const uint64_t b_desc0 = k_major_desc(smem_addr(b_ring));
             int s = 0, it = 0, lt = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -540,7 +525,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
         }
         __syncwarp();
     } else if (warp == 1) {
-        const uint64_t w_desc0 = smem_desc(smem_addr(w_ring)), x_desc0 = smem_desc(smem_addr(x_ring));
+        const uint64_t w_desc0 = k_major_desc(smem_addr(w_ring)), x_desc0 = k_major_desc(smem_addr(x_ring));
         int s = 0;
         uint32_t ph = 0;
         for (int kb = k0; kb < k1; ++kb) {
@@ -680,36 +665,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
 }
 
 // ---------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
-// Tensor map over a row-major matrix of `rows` x `cols` elements with row
-// pitch ld_bytes: boxes of box_cols x box_rows, swizzled, zero fill.
-bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base,
-                 uint64_t rows, uint64_t cols, uint64_t ld_bytes, uint32_t box_cols, uint32_t box_rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {ld_bytes};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool encode_e4m3(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+bool encode_e4m3(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
     return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, base, rows, cols, ld, BK,
                        box_rows);
 }

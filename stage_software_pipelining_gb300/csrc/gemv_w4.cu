@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(256, 8) w4_quantize_kernel(const W4QuantLaunch
 // x as K/32 slices of M rows by 32 elements (64 bytes): a box lands slice by
 // slice, so that a warp's 16-byte reads of eight rows touch every bank once.
 bool encode_x(CUtensorMap* map, const W4Launch& L, int x_rows) {
-    auto fn = encode_fn();
+    auto fn = tensor_map_encoder();
     if (!fn) return false;
     cuuint64_t dims[3] = {32, static_cast<cuuint64_t>(L.M), static_cast<cuuint64_t>(L.K / 32)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(L.ldx * 2), 64};

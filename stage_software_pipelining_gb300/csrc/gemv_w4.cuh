@@ -1,11 +1,10 @@
 // gemv_w4.cuh -- what the two kernels of the 4-bit product share: the unpacking
-// of nibbles, bounded waits, tensor maps and the choice of the K split.
+// of nibbles, bounded waits and the choice of the K split.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
@@ -13,6 +12,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant.h"
+#include "tensor_copy.cuh"
 
 namespace ssp {
 namespace w4 {
@@ -97,13 +97,6 @@ struct Wait {
     }
 };
 
-// Bounded wait without a look at the abort flag.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > limit_ns) return;
-}
-
 // (a & mask) | magic in one instruction.
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
     uint32_t r;
@@ -177,35 +170,6 @@ __device__ __forceinline__ void store4(const Params& p, int m, int n, float4 v) 
 }
 
 // ---------------------------------------------------------------- host side
-inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
-// A row-major matrix in boxes of box_cols of a row by box_rows rows, swizzled;
-// zeros outside it.
-inline bool encode_rows(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int64_t rows, int64_t cols,
-                 int64_t ld_bytes, int box_cols, int box_rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld_bytes)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // CTAs of a kernel that the current device holds at once, by cluster size
 // 1..8; asked for once a device, with the kernel's shared-memory limit.
 struct Residency {

@@ -40,13 +40,6 @@ constexpr int kStages = 6;
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kDCols = 128;    // TMEM columns of the accumulators, after the A operand's 128
 
-// Shared-memory descriptor of a K-major operand: 128-byte rows, 8-row groups
-// 1024 bytes apart, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-
 // Eight 4-bit weights less their zero point as four pairs (k, k + 1), exact in
 // 16 bits, the order in which x lies in memory.  A byte goes into both halves
 // and a nibble of it is kept in each, under an exponent as in unpack(): fp16
@@ -189,7 +182,7 @@ __global__ void __launch_bounds__(Geo<GROUP>::kThreads, 2)
         bool ok = true;
         for (int kb = k0; ok && kb < k1; ++kb) {
             const Wait full(full_bar(s), ph);  // x is there
-            const uint64_t x_desc = smem_desc(smem_addr(x_ring + s * X_BYTES));
+            const uint64_t x_desc = k_major_desc(smem_addr(x_ring + s * X_BYTES));
             for (int ch = 0; ch < CPS; ++ch, ++i) {
                 const int b = i % NB;
                 const uint32_t bp = static_cast<uint32_t>(i / NB) & 1u;
