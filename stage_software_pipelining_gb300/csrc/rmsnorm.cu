@@ -11,8 +11,9 @@
 //
 // Bound by memory: per element two reads and, for the 8-bit form, a write of
 // the sum and of one byte.  Rows of up to 1024 elements (16-bit) take a warp
-// each, longer ones a block; a row that does not fit a block's registers is
-// read twice (wide_kernel).
+// each, longer ones a block (row_kernel); a row off 16-byte boundaries, or too long
+// for a block's registers, goes by way of shared memory (staged_kernel), and one
+// that does not fit there either is read twice (wide_kernel).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

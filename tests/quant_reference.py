@@ -5,10 +5,10 @@ Unit roundoffs (half a unit in the last place over the value): bf16 2^-8, fp16
 2^-14).
 
 * add_rmsnorm: h is one fp32 addition (2^-24).  The mean of squares is a sum
-  of positive fp32 terms; whatever the order, at most n/32 of them are added
-  in a row by one thread and then at most 40 partial sums, so its relative
-  error is below (n/32 + 42) 2^-24, of which the square root halves; the other
-  factors of y add five roundings.  n <= 40000 gives 4e-5, halved 2e-5 + 3e-7:
+  of positive fp32 terms, at most 100 of which one thread adds in a row (a row
+  of 1024 by a warp, 45000 by 512 threads, 100000 by 1024), and then at most 40
+  partial sums, so its relative error is below 142 * 2^-24 = 9e-6, of which the
+  square root halves; the other factors of y add five roundings, 3e-7.
   NORM_REL = 2.5e-5.  The output's own rounding comes on top.  q is compared
   with the roundings of the exact quotient moved down and up by 2 NORM_REL
   (y's error and the scale's), between which a monotone rounding must fall.
@@ -16,9 +16,12 @@ Unit roundoffs (half a unit in the last place over the value): bf16 2^-8, fp16
   them to the running sum and may truncate: at most 2^-22 of the sum of
   magnitudes a step, K/32 <= 64 steps for K <= 2048: SUM_REL = 2e-5 of
   (|A||B|)_ij, the scales' two roundings and the output's one on top.
-* gemv_w4: the same with K/16 <= 512 steps a warp for K <= 8192, the sums of a
-  group scaled in fp32 and the groups' sums added: 512 * 2^-23 < 7e-5 and the
-  group sums' 256 * 2^-24 < 2e-5: W4_REL = 1e-4 of (|x||w|)_ij.
+* gemv_w4: a group's sum is at most 8 steps of 16 products, each off by 2^-22
+  of its magnitudes: 8 * 2^-22 < 2e-6.  The groups' sums are scaled and added in
+  fp32, one 2^-24 each, at most K/group of them in a row by one thread (fewer
+  where K is cut over warps and CTAs), and the cut's 32 partials at most:
+  (K/32 + 32) 2^-24 < 2e-5 for K <= 8192; 24576 uncut 5e-5; 81920, which is cut
+  in eight, 2.5e-5.  W4_REL = 1e-4 of (|x||w|)_ij holds all of them.
 """
 import numpy as np
 import torch
