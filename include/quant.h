@@ -109,7 +109,8 @@ int quantize_fp8(int64_t rows, int64_t cols, const void* x, int64_t ldx, int dty
  *            fp32 result rounded to nearest even; fp16 overflows to infinity).
  *            QUANT_F32 is GEMM_ERR_UNSUPPORTED.
  *   a_scale, b_scale   M and N fp32 values
- * Products are summed in fp32 on the tensor cores.  K = 0 gives C = 0.
+ * Products are summed in fp32 on the tensor cores; the sum is multiplied in fp32
+ * by a_scale[i], then by b_scale[j].  K = 0 gives C = 0.
  * Alignment (GEMM_ERR_ALIGN otherwise): A, B and C start on 16-byte
  * boundaries and lda, ldb and ldc*2 are multiples of 16; a_scale and b_scale
  * are 4-byte aligned.

@@ -12,6 +12,11 @@ arithmetic runs in the CUDA kernels of libgemm.so.  The caller owns every
 buffer, outputs included; ``empty_rows`` makes one whose rows start on 16-byte
 boundaries.  A tensor that an operator cannot take raises ValueError, a status
 other than GEMM_OK raises GemmError.  There is no CPU fallback.
+
+A call runs on the current stream of its tensors' device, or on ``stream``; with
+another stream than the one a tensor was made on, the caller orders the two and
+keeps the tensor until the call has run (torch's ``wait_stream`` and
+``record_stream``).
 """
 from __future__ import annotations
 
