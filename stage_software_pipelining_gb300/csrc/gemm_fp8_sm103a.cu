@@ -825,8 +825,8 @@ int launch_few(const Fp8Launch& L, int slot, int split, bool two, cudaStream_t s
 // Which kernel, tile and cut of K: the one with the least time by a model whose
 // constants (microseconds) were fitted to every choice measured on 40 shapes of
 // 1 to 5536 rows, 153 to 28672 columns and 82 to 8192 of K.  On 60 other shapes,
-// drawn, its choices are 0.5 % slower than the best one of each on average, 16 %
-// at most (541 x 1332 x 966: 6.9 us for 5.9).
+// drawn, its choices are 2 % slower than the best one of each on average, 22 %
+// at most (541 x 1332 x 966: 7.0 us for 5.7).
 //   * few rows: a round of resident CTAs takes each one's K blocks and an
 //     epilogue that grows with MT, twice where two share an SM; a cut K adds the
 //     partials' way through distributed shared memory, and rounds of clusters
