@@ -1,0 +1,205 @@
+// act_grad.cu -- dz = dy act'(z) and the bias gradient, the sum of dz's rows.
+//
+// One pass over dy and z, bound by memory.  A cluster of CTAs owns a strip of
+// columns and shares its rows: every thread adds its rows' unrounded values in
+// fp32, a CTA its threads', and the first CTA of the cluster the others' through
+// distributed shared memory, all in a fixed order and without a workspace.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "activation.cuh"
+#include "internal.h"
+#include "linear.h"
+#include "product.cuh"
+#include "ptx.cuh"
+
+namespace ssp {
+namespace {
+
+constexpr int THREADS = 256;
+
+struct Params {
+    int M, N;
+    int rows;  // of a CTA
+    int act;
+    const uint16_t* dy;
+    long long lddy;
+    const uint16_t* pre;
+    long long ldp;
+    uint16_t* dz;
+    long long lddz;
+    float* dbias;
+    const float* addend;
+};
+
+template <int VEC>
+struct Values {
+    uint32_t u[VEC / 2];
+};
+template <>
+struct Values<1> {
+    uint32_t u[1];
+};
+
+// VEC adjacent values, of which `left` are in the row.
+template <int VEC>
+__device__ __forceinline__ Values<VEC> load(const uint16_t* p, int left) {
+    Values<VEC> v;
+    if constexpr (VEC == 1) {
+        v.u[0] = *p;
+    } else if (left >= VEC) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        v.u[0] = q.x;
+        v.u[1] = q.y;
+        v.u[2] = q.z;
+        v.u[3] = q.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i)
+            v.u[i] = (2 * i < left ? p[2 * i] : 0u) | (2 * i + 1 < left ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
+    }
+    return v;
+}
+
+// Strips of VEC * GROUPS columns; ROWS rows at a time.  VEC = 8 wants rows on
+// 16-byte boundaries.
+template <bool BF16, int VEC, int ACT>
+__device__ __forceinline__ void pass(const Params& p, int r0, int r1, int c, float (&sum)[VEC]) {
+    constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS;
+    constexpr int AHEAD = 4;  // rows of a thread whose loads are under way together
+    const int left = p.N - c;
+    if (left <= 0) return;
+    for (int r = r0 + static_cast<int>(threadIdx.x) / GROUPS; r < r1; r += AHEAD * ROWS) {
+        Values<VEC> dy[AHEAD], z[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const long long row = r + a * ROWS;
+            if (row < r1) {
+                dy[a] = load<VEC>(p.dy + row * p.lddy + c, left);
+                if (ACT != LINEAR_ACT_NONE) z[a] = load<VEC>(p.pre + row * p.ldp + c, left);
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const long long row = r + a * ROWS;
+            if (row >= r1) break;
+            uint32_t out[VEC == 8 ? 4 : 1];
+#pragma unroll
+            for (int i = 0; i < (VEC + 1) / 2; ++i) {
+                float2 g = unpack16<BF16>(dy[a].u[i]);
+                if constexpr (ACT != LINEAR_ACT_NONE) {
+                    const float2 f = unpack16<BF16>(z[a].u[i]);
+                    g.x *= derivative<ACT>(f.x);
+                    if (VEC > 1) g.y *= derivative<ACT>(f.y);
+                }
+                sum[2 * i] += g.x;
+                if (VEC > 1) sum[(2 * i + 1) % VEC] += g.y;
+                out[i] = pack16<BF16>(g.x, g.y);
+            }
+            if (p.dz) {
+                uint16_t* d = p.dz + row * p.lddz + c;
+                if constexpr (VEC == 1) {
+                    *d = static_cast<uint16_t>(out[0]);
+                } else if (left >= VEC) {
+                    *reinterpret_cast<uint4*>(d) = make_uint4(out[0], out[1], out[2], out[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (i < left) d[i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
+                }
+            }
+        }
+    }
+}
+
+template <bool BF16, int VEC>
+__global__ void __launch_bounds__(THREADS) act_grad_kernel(const Params p) {
+    constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS, COLS = GROUPS * VEC;
+    __shared__ float sums[ROWS][COLS + 4];
+    __shared__ float total[COLS];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int rank = static_cast<int>(blockIdx.y), parts = static_cast<int>(gridDim.y);  // a cluster is a column of the grid
+    const int col0 = static_cast<int>(blockIdx.x) * COLS;
+    const int c = col0 + static_cast<int>(threadIdx.x % GROUPS) * VEC;
+    const int r0 = min(p.M, rank * p.rows), r1 = min(p.M, r0 + p.rows);
+    float sum[VEC] = {};
+    if (p.act == LINEAR_ACT_NONE)
+        pass<BF16, VEC, LINEAR_ACT_NONE>(p, r0, r1, c, sum);
+    else
+        with_activation(p.act, [&](auto a) { pass<BF16, VEC, decltype(a)::value>(p, r0, r1, c, sum); });
+    if (!p.dbias) return;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sums[threadIdx.x / GROUPS][(threadIdx.x % GROUPS) * VEC + i] = sum[i];
+    __syncthreads();
+    if (threadIdx.x < COLS) {
+        float s = 0.0f;
+        for (int r = 0; r < ROWS; ++r) s += sums[r][threadIdx.x];
+        total[threadIdx.x] = s;
+    }
+    if (parts > 1) cluster_sync_all();
+    else __syncthreads();
+    if (rank == 0 && threadIdx.x < COLS && col0 + static_cast<int>(threadIdx.x) < p.N) {
+        const int j = col0 + static_cast<int>(threadIdx.x);
+        float s = total[threadIdx.x];
+        for (int r = 1; r < parts; ++r)
+            s += ld_cluster_f32(mapa_shared(smem_addr(&total[threadIdx.x]), static_cast<uint32_t>(r)));
+        p.dbias[j] = p.addend ? p.addend[j] + s : s;
+    }
+    if (parts > 1) cluster_sync_all();  // the others' sums have been read
+}
+
+template <bool BF16, int VEC>
+int launch(const ActGradLaunch& L, cudaStream_t stream) {
+    constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS, COLS = GROUPS * VEC;
+    Params p = {};
+    p.M = static_cast<int>(L.M);
+    p.N = static_cast<int>(L.N);
+    p.act = L.act;
+    p.dy = static_cast<const uint16_t*>(L.dy);
+    p.lddy = L.lddy;
+    p.pre = static_cast<const uint16_t*>(L.pre);
+    p.ldp = L.ldp;
+    p.dz = static_cast<uint16_t*>(L.dz);
+    p.lddz = L.lddz;
+    p.dbias = L.dbias;
+    p.addend = L.addend;
+    // Rows are shared among as many CTAs as have a few each; a sum's are a
+    // cluster of eight at most.
+    const int64_t strips = (L.N + COLS - 1) / COLS;
+    int64_t parts = (L.M + 4 * ROWS - 1) / (4 * ROWS);
+    const int64_t most = L.dbias ? 8 : 65535;
+    if (parts < 1) parts = 1;
+    if (parts > most) parts = most;
+    p.rows = static_cast<int>((L.M + parts - 1) / parts);
+    if (p.rows < 1) p.rows = 1;
+    if (!L.dbias) parts = (L.M + p.rows - 1) / p.rows;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = static_cast<unsigned>(parts);
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.dbias && parts > 1 ? 2 : 1;
+    return product_finish(cudaLaunchKernelEx(&cfg, act_grad_kernel<BF16, VEC>, p));
+}
+
+}  // namespace
+
+int act_grad_launch(const ActGradLaunch& L, cudaStream_t stream) {
+    auto fits = [&](const void* p, int64_t ld) {
+        return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld % 8 == 0 || L.M <= 1));
+    };
+    const bool vec = fits(L.dy, L.lddy) && fits(L.pre, L.ldp) && fits(L.dz, L.lddz);
+    if (L.bf16) return vec ? launch<true, 8>(L, stream) : launch<true, 1>(L, stream);
+    return vec ? launch<false, 8>(L, stream) : launch<false, 1>(L, stream);
+}
+
+}  // namespace ssp

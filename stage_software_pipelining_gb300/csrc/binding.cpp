@@ -1,11 +1,11 @@
 // binding.cpp -- Python's way into libgemm.so's quantised operators
-// (include/quant.h): the checks of tensor arguments and their marshalling into
+// (include/quant.h) and training operators (include/linear.h): the checks of tensor arguments and their marshalling into
 // (pointer, leading dimension) pairs, in C++ because at a token a call they
 // are most of a call's time (measured on a Grace host: 14 us of a 20 us
 // gemm_fp8 call when written in Python over ctypes).
 //
-// Every function takes its arguments by position (quant.py holds the
-// signatures), raises ValueError for a tensor it cannot take, and returns the
+// Every function takes its arguments by position (quant.py and linear.py hold
+// the signatures), raises ValueError for a tensor it cannot take, and returns the
 // entry point's gemm_status_t.
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -15,6 +15,7 @@
 #include <stdexcept>
 #include <string>
 
+#include "../../include/linear.h"
 #include "../../include/quant.h"
 
 namespace {
@@ -255,6 +256,183 @@ int quantize_w4_(PyObject* const* a) {
     return quantize_w4(N, K, IN.p, IN.ld, code, group, RW.p, RW.ld, S.p, S.ld, scode, Z.p, Z.ld, stream);
 }
 
+// ---------------------------------------------------------------- include/linear.h
+int act_of(PyObject* o) {
+    const long a = PyLong_AsLong(o);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("act must be an activation's number");
+    }
+    return static_cast<int>(a);
+}
+
+void* vector_or_none(PyObject* o, const char* name, at::ScalarType type, int64_t n, const Tensor& like) {
+    const Tensor* t = tensor(o, name, true);
+    return t ? vector_of(*t, name, type, n, like) : nullptr;
+}
+
+float number_of(PyObject* o, const char* name) {
+    const double v = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(std::string(name) + " must be a number");
+    }
+    return static_cast<float>(v);
+}
+
+// One of a product's two entry points; the second waits for the stream.
+template <class F, class G>
+int call(bool checked, F plain, G waiting) {
+    if (!checked) return plain();
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = waiting();
+    Py_END_ALLOW_THREADS
+    return st;
+}
+
+// x, W, y, bias, residual, act, pre, stream, checked
+int linear_(PyObject* const* a) {
+    const Tensor& x = matrix(a[0], "x");
+    const Tensor& W = matrix(a[1], "W");
+    const int code = type16_of(x, "x");
+    const at::ScalarType dt = x.scalar_type();
+    const int64_t M = x.size(0), K = x.size(1), N = W.size(0);
+    const Rows X = rows_of(x, "x", dt, M, K, x);
+    const Rows RW = rows_of(W, "W", dt, N, K, x);
+    const Rows Y = rows_of(*tensor(a[2], "y"), "y", dt, M, N, x);
+    const void* bias = vector_or_none(a[3], "bias", dt, N, x);
+    const Rows R = rows_or_none(a[4], "residual", dt, M, N, x);
+    const int act = act_of(a[5]);
+    const Rows P = rows_or_none(a[6], "pre", dt, M, N, x);
+    void* s = stream_of(a[7], x);
+    const bool checked = truth_of(a[8], "checked");
+    const c10::cuda::CUDAGuard guard(x.device());
+    auto with = [&](auto f) {
+        return f(M, N, K, X.p, X.ld, RW.p, RW.ld, bias, R.p, R.ld, act, P.p, P.ld, Y.p, Y.ld, code, s);
+    };
+    return call(checked, [&] { return with(linear); }, [&] { return with(linear_checked); });
+}
+
+// dy, dz, pre, act, dbias, addend, stream
+int act_grad_(PyObject* const* a) {
+    const Tensor& dy = matrix(a[0], "dy");
+    const int code = type16_of(dy, "dy");
+    const at::ScalarType dt = dy.scalar_type();
+    const int64_t M = dy.size(0), N = dy.size(1);
+    const Rows DY = rows_of(dy, "dy", dt, M, N, dy);
+    const Rows DZ = rows_or_none(a[1], "dz", dt, M, N, dy);
+    const Rows P = rows_or_none(a[2], "pre", dt, M, N, dy);
+    const int act = act_of(a[3]);
+    if (act != LINEAR_ACT_NONE && a[2] == Py_None) refuse("pre is needed for an activation's derivative");
+    float* db = static_cast<float*>(vector_or_none(a[4], "dbias", at::kFloat, N, dy));
+    const float* c = static_cast<const float*>(vector_or_none(a[5], "addend", at::kFloat, N, dy));
+    if (a[1] == Py_None && a[4] == Py_None) refuse("act_grad needs an output: dz or dbias");
+    if (a[4] == Py_None && a[5] != Py_None) refuse("addend is added to dbias, which is not given");
+    void* s = stream_of(a[6], dy);
+    const c10::cuda::CUDAGuard guard(dy.device());
+    return act_grad(M, N, DY.p, DY.ld, P.p, P.ld, act, DZ.p, DZ.ld, db, c, code, s);
+}
+
+// dz, W, dx, residual, act, pre, stream, checked
+int linear_dx_(PyObject* const* a) {
+    const Tensor& dz = matrix(a[0], "dz");
+    const Tensor& W = matrix(a[1], "W");
+    const int code = type16_of(dz, "dz");
+    const at::ScalarType dt = dz.scalar_type();
+    const int64_t M = dz.size(0), N = dz.size(1), K = W.size(1);
+    const Rows DZ = rows_of(dz, "dz", dt, M, N, dz);
+    const Rows RW = rows_of(W, "W", dt, N, K, dz);
+    const Rows DX = rows_of(*tensor(a[2], "dx"), "dx", dt, M, K, dz);
+    const Rows R = rows_or_none(a[3], "residual", dt, M, K, dz);
+    const int act = act_of(a[4]);
+    const Rows P = rows_or_none(a[5], "pre", dt, M, K, dz);
+    if ((act == LINEAR_ACT_NONE) != (a[5] == Py_None)) refuse("pre and an activation go together");
+    void* s = stream_of(a[6], dz);
+    const bool checked = truth_of(a[7], "checked");
+    const c10::cuda::CUDAGuard guard(dz.device());
+    auto with = [&](auto f) {
+        return f(M, N, K, DZ.p, DZ.ld, RW.p, RW.ld, R.p, R.ld, act, P.p, P.ld, DX.p, DX.ld, code, s);
+    };
+    return call(checked, [&] { return with(linear_dx); }, [&] { return with(linear_dx_checked); });
+}
+
+// dz, x, dw, addend, stream, checked
+int linear_dw_(PyObject* const* a) {
+    const Tensor& dz = matrix(a[0], "dz");
+    const Tensor& x = matrix(a[1], "x");
+    const Tensor& dw = matrix(a[2], "dw");
+    const int code = type16_of(dz, "dz"), out = type_of(dw, "dw");
+    const at::ScalarType dt = dz.scalar_type(), to = dw.scalar_type();
+    if (out != QUANT_F32 && to != dt) refuse("dw must be fp32 or of dz's type");
+    const int64_t M = dz.size(0), N = dz.size(1), K = x.size(1);
+    const Rows DZ = rows_of(dz, "dz", dt, M, N, dz);
+    const Rows X = rows_of(x, "x", dt, M, K, dz);
+    const Rows DW = rows_of(dw, "dw", to, N, K, dz);
+    const Rows C = rows_or_none(a[3], "addend", to, N, K, dz);
+    void* s = stream_of(a[4], dz);
+    const bool checked = truth_of(a[5], "checked");
+    const c10::cuda::CUDAGuard guard(dz.device());
+    auto with = [&](auto f) {
+        return f(M, N, K, DZ.p, DZ.ld, X.p, X.ld, C.p, C.ld, DW.p, DW.ld, code, out, s);
+    };
+    return call(checked, [&] { return with(linear_dw); }, [&] { return with(linear_dw_checked); });
+}
+
+// A matrix, or a batch of matrices in a 3-D tensor, whose rows are contiguous.
+struct Batch {
+    void* p = nullptr;
+    int64_t batch = 1, rows = 0, cols = 0, ld = 0, stride = 0;
+};
+Batch batch_of(const Tensor& t, const char* name) {
+    if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+    const int d = static_cast<int>(t.dim());
+    if (d != 2 && d != 3) refuse(std::string(name) + " must be 2-D or 3-D");
+    Batch b;
+    b.batch = d == 3 ? t.size(0) : 1;
+    b.rows = t.size(d - 2);
+    b.cols = t.size(d - 1);
+    b.ld = t.stride(d - 2);
+    b.stride = d == 3 ? t.stride(0) : 0;
+    if (b.cols > 1 && t.numel() > 0 && t.stride(d - 1) != 1) refuse(std::string(name) + " must be row-major (unit column stride)");
+    if (b.rows > 1 && b.ld < b.cols) refuse(std::string(name) + "'s rows overlap");
+    const int64_t span = b.rows > 0 ? (b.rows - 1) * (b.rows > 1 ? b.ld : 0) + b.cols : 0;
+    if (b.batch > 1 && b.stride < span) refuse(std::string(name) + "'s matrices overlap");
+    b.p = t.data_ptr();
+    return b;
+}
+
+// g, out, workspace, steps, a, b, c, eps, scale, stream, checked
+int orthogonalize_(PyObject* const* a) {
+    const Tensor& g = *tensor(a[0], "g");
+    const Tensor& out = *tensor(a[1], "out");
+    const Tensor& ws = *tensor(a[2], "workspace");
+    const Batch G = batch_of(g, "g"), O = batch_of(out, "out");
+    const int code = type_of(g, "g"), to = type16_of(out, "out");
+    if (out.device() != g.device()) refuse("out must be on " + g.device().str());
+    if (out.sizes() != g.sizes()) refuse("out must be " + text(g.sizes()) + ", not " + text(out.sizes()));
+    const long steps = PyLong_AsLong(a[3]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("steps must be a whole number");
+    }
+    if (steps < 0 || steps > 100) refuse("steps must be 0 to 100");
+    const float abc[3] = {number_of(a[4], "a coefficient"), number_of(a[5], "a coefficient"),
+                          number_of(a[6], "a coefficient")};
+    const float eps = number_of(a[7], "eps"), scale = number_of(a[8], "scale");
+    if (ws.device() != g.device()) refuse("workspace must be on " + g.device().str());
+    if (!ws.is_contiguous()) refuse("workspace must be contiguous");
+    void* s = stream_of(a[9], g);
+    const bool checked = truth_of(a[10], "checked");
+    const c10::cuda::CUDAGuard guard(g.device());
+    const size_t bytes = static_cast<size_t>(ws.numel()) * ws.element_size();
+    auto with = [&](auto f) {
+        return f(G.batch, G.rows, G.cols, G.p, G.ld, G.stride, code, O.p, O.ld, O.stride, to, static_cast<int>(steps),
+                 abc, eps, scale, ws.data_ptr(), bytes, s);
+    };
+    return call(checked, [&] { return with(orthogonalize); }, [&] { return with(orthogonalize_checked); });
+}
+
 template <int (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != N) {
@@ -274,7 +452,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define ENTRY(name, args) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<name##_, args>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(add_rmsnorm, 9), ENTRY(quantize_fp8, 4), ENTRY(gemm_fp8, 7), ENTRY(gemv_w4, 7),
-                         ENTRY(quantize_w4, 5), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(quantize_w4, 5), ENTRY(linear, 9), ENTRY(act_grad, 7), ENTRY(linear_dx, 8),
+                         ENTRY(linear_dw, 6), ENTRY(orthogonalize, 11), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_quant", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

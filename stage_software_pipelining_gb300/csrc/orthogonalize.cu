@@ -1,0 +1,310 @@
+// orthogonalize.cu -- Newton-Schulz steps X <- a X + (b A + c A^2) X, A = X X^T,
+// on the tensor cores, and the two passes before them: the sum of squares, and
+// the first X.
+//
+// A step is three products (product_*_sm103a.cu).  The first two are symmetric,
+// so where a matrix has many tiles only those on and below the diagonal are
+// computed and mirrored.  The polynomial's coefficients are epilogue factors:
+// nothing but X, A and b A + c A^2 is ever written.  A tall matrix is not
+// transposed: A = X^T X takes both operands MN-major.
+//
+// Between the products everything is fp16 at power-of-two scales, which cost
+// nothing (they go into the same factors) and put the elements where fp16 has
+// all its 11 bits: X of spectral norm one has elements about 1 / sqrt(longer
+// side), A about 1 / shorter side off its diagonal.  bf16 would lose three of
+// those bits for a range that is not needed.  The first X is G times a power of
+// two, exact for 16-bit gradients whose elements lie within fp16's range of one
+// another; what is left of the norm, t, is applied to the first step's factors,
+// on the device.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "internal.h"
+#include "linear.h"
+#include "product.cuh"
+#include "ptx.cuh"
+
+namespace ssp {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int kMostParts = 256;  // CTAs that share a matrix's sum
+
+struct Params {
+    int rows, cols;
+    int vecs;  // groups of eight elements a row
+    const void* g;
+    long long ldg, stride_g;
+    double* parts;  // [batch][gridDim.x]: sums of squares
+    int n_parts;
+    float eps;
+    // What the second pass writes: the first X, or (no steps) the output.
+    void* out;
+    long long ldo, stride_o;
+    int out_bf16, last;
+    float scale;
+    float* factor;
+};
+
+// Eight elements of a row from column c on, zeros past its end.
+template <int TYPE>
+__device__ __forceinline__ void load8(const Params& p, int b, int row, int c, float (&v)[8]) {
+    const long long at = static_cast<long long>(b) * p.stride_g + static_cast<long long>(row) * p.ldg + c;
+    const int left = p.cols - c;
+    if constexpr (TYPE == QUANT_F32) {
+        const float* s = static_cast<const float*>(p.g) + at;
+        if (left >= 8) {
+            const float4 x = reinterpret_cast<const float4*>(s)[0], y = reinterpret_cast<const float4*>(s)[1];
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? s[i] : 0.0f;
+        }
+    } else {
+        constexpr bool BF16 = TYPE == QUANT_BF16;
+        const uint16_t* s = static_cast<const uint16_t*>(p.g) + at;
+        if (left >= 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(s);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack16<BF16>(w[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? load16<BF16>(s, i) : 0.0f;
+        }
+    }
+}
+
+// The sum of v over the CTA's threads, in a fixed order, for every thread.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double warps[THREADS / 32];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) s += warps[w];
+    return s;
+}
+
+// Sums of squares.  Sums of squares of elements beyond 2^45 or below 2^-45 may
+// leave fp32's range: a group of eight whose largest is such is scaled by 2^-80
+// or 2^100 and summed apart.  (Beside a larger element of its group, a square
+// that underflows is too small to count.)
+template <int TYPE>
+__global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int b = static_cast<int>(blockIdx.y);
+    const long long n = static_cast<long long>(p.rows) * p.vecs;
+    float sum = 0.0f, large = 0.0f, small = 0.0f;
+    for (long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * THREADS) {
+        const int row = static_cast<int>(i / p.vecs);
+        float v[8];
+        load8<TYPE>(p, b, row, static_cast<int>(i - static_cast<long long>(row) * p.vecs) * 8, v);
+        float most = 0.0f, s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            most = fmaxf(most, fabsf(v[e]));
+            s = fmaf(v[e], v[e], s);
+        }
+        if (most <= 0x1p45f && (most >= 0x1p-45f || most == 0.0f)) {
+            sum += s;  // a NaN among the eight is in s
+        } else {
+            const float by = most > 1.0f ? 0x1p-80f : 0x1p100f;
+            s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(v[e] * by, v[e] * by, s);
+            if (most > 1.0f) large += s;
+            else small += s;
+        }
+    }
+    const double s = block_sum(static_cast<double>(sum) + static_cast<double>(large) * 0x1p160 +
+                               static_cast<double>(small) * 0x1p-200);
+    if (threadIdx.x == 0) p.parts[static_cast<long long>(b) * gridDim.x + blockIdx.x] = s;
+}
+
+// X = G 2^e with a root mean square of about one, and t = 2^-e / (|G| + eps).
+// The largest element is at most 2^15 then.
+template <int TYPE>
+__global__ void __launch_bounds__(THREADS) ortho_first_kernel(const Params p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int b = static_cast<int>(blockIdx.y);
+    double v = 0.0;
+    if (static_cast<int>(threadIdx.x) < p.n_parts) v = p.parts[static_cast<long long>(b) * p.n_parts + threadIdx.x];
+    const double norm = sqrt(block_sum(v));
+    int e = 0;
+    if (norm > 0.0 && norm < 1e300) {
+        double target = sqrt(static_cast<double>(p.rows) * p.cols);
+        if (target > 16384.0) target = 16384.0;
+        e = ilogb(target) - ilogb(norm);
+    }
+    // Not finite: NaN everywhere.  No elements but zeros: zeros, or 0 / 0.
+    float t = nanf("");
+    if (norm < 1e300)
+        t = norm == 0.0 && p.eps > 0.0f ? 1.0f : static_cast<float>(ldexp(1.0, -e) / (norm + static_cast<double>(p.eps)));
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.factor[b] = t;
+    // 2^e may lie beyond fp32's exponents: two factors.
+    const float by0 = ldexpf(1.0f, e / 2), by1 = ldexpf(1.0f, e - e / 2);
+    const float after = p.last ? t * p.scale : 1.0f;
+    const long long n = static_cast<long long>(p.rows) * p.vecs;
+    for (long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * THREADS) {
+        const int row = static_cast<int>(i / p.vecs);
+        const int c = static_cast<int>(i - static_cast<long long>(row) * p.vecs) * 8;
+        float x[8];
+        load8<TYPE>(p, b, row, c, x);
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            u[k] = pack16(p.out_bf16 != 0, x[2 * k] * by0 * by1 * after, x[2 * k + 1] * by0 * by1 * after);
+        uint16_t* d = static_cast<uint16_t*>(p.out) + static_cast<long long>(b) * p.stride_o +
+                      static_cast<long long>(row) * p.ldo + c;
+        if (p.cols - c >= 8 || !p.last) {  // the first X's rows are padded to whole groups
+            *reinterpret_cast<uint4*>(d) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+            for (int k = 0; k < p.cols - c; ++k) d[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
+        }
+    }
+}
+
+template <int TYPE>
+int launch_first(const Params& p, int64_t batch, cudaStream_t stream) {
+    ProductConfig c(1, 1, THREADS, 0, stream);
+    c.cfg.gridDim = dim3(static_cast<unsigned>(p.n_parts), static_cast<unsigned>(batch));
+    const int st = product_finish(cudaLaunchKernelEx(&c.cfg, ortho_sum_kernel<TYPE>, p));
+    return st != GEMM_OK ? st : product_finish(cudaLaunchKernelEx(&c.cfg, ortho_first_kernel<TYPE>, p));
+}
+
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Where the workspace's parts begin.
+struct Layout {
+    size_t factor, parts, x[2], a, b, bytes;
+};
+Layout layout(int64_t batch, int64_t rows, int64_t cols) {
+    const int64_t n = rows < cols ? rows : cols;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t r = at;
+        at += (bytes + 255) / 256 * 256;
+        return r;
+    };
+    Layout l;
+    const size_t k = static_cast<size_t>(batch);
+    l.factor = take(k * sizeof(float));
+    l.parts = take(k * kMostParts * sizeof(double));
+    for (size_t& x : l.x) x = take(k * rows * round8(cols) * 2);
+    l.a = take(k * n * round8(n) * 2);
+    l.b = take(k * n * round8(n) * 2);
+    l.bytes = at;
+    return l;
+}
+
+}  // namespace
+
+size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols) { return layout(batch, rows, cols).bytes; }
+
+int ortho_launch(const OrthoLaunch& L, cudaStream_t stream) {
+    const Layout at = layout(L.batch, L.rows, L.cols);
+    uint8_t* ws = static_cast<uint8_t*>(L.workspace);
+    const bool tall = L.rows > L.cols;
+    const int64_t n = tall ? L.cols : L.rows, m = tall ? L.rows : L.cols;
+    Params p = {};
+    p.rows = static_cast<int>(L.rows);
+    p.cols = static_cast<int>(L.cols);
+    p.vecs = static_cast<int>((L.cols + 7) / 8);
+    p.g = L.g;
+    p.ldg = L.ldg;
+    p.stride_g = L.stride_g;
+    p.parts = reinterpret_cast<double*>(ws + at.parts);
+    const int64_t groups = (static_cast<int64_t>(p.rows) * p.vecs + THREADS - 1) / THREADS;
+    const int64_t share = (groups + 3) / 4;  // four groups a thread before all CTAs take part
+    p.n_parts = static_cast<int>(share < kMostParts ? share : kMostParts);
+    p.eps = L.eps;
+    p.scale = L.scale;
+    p.factor = reinterpret_cast<float*>(ws + at.factor);
+    p.last = L.steps == 0;
+    const int64_t ldx = round8(L.cols), ldn = round8(n);
+    if (p.last) {
+        p.out = L.out;
+        p.ldo = L.ldo;
+        p.stride_o = L.stride_o;
+        p.out_bf16 = L.out_bf16;
+    } else {
+        p.out = ws + at.x[0];
+        p.ldo = ldx;
+        p.stride_o = L.rows * ldx;
+    }
+    int st = L.dtype == QUANT_F32    ? launch_first<QUANT_F32>(p, L.batch, stream)
+             : L.dtype == QUANT_BF16 ? launch_first<QUANT_BF16>(p, L.batch, stream)
+                                     : launch_first<QUANT_F16>(p, L.batch, stream);
+    // Scales of A (and b A + c A^2) and of X, powers of two.
+    int la = std::ilogb(static_cast<double>(n));
+    if (la > 14) la = 14;
+    const double sa = std::ldexp(1.0, la);
+    const double sx = std::ldexp(1.0, std::ilogb(std::sqrt(static_cast<double>(m))));
+    for (int s = 0; st == GEMM_OK && s < L.steps; ++s) {
+        const bool first = s == 0, last = s + 1 == L.steps;
+        const ProductMatrix X = {ws + at.x[s & 1], ldx, L.rows * ldx};
+        const ProductMatrix A = {ws + at.a, ldn, n * ldn}, B = {ws + at.b, ldn, n * ldn};
+        ProductLaunch q;
+        q.batch = L.batch;
+        q.epi = EPI_STEP;
+        q.padded = 1;
+        q.factor = p.factor;
+        // A = X X^T, or X^T X
+        q.M = q.N = n;
+        q.K = m;
+        q.A = q.B = X;
+        q.a_mn = q.b_mn = tall;
+        q.symmetric = 1;
+        q.D = A;
+        q.alpha = static_cast<float>(first ? sa : sa / (sx * sx));
+        q.alpha_pow = first ? 2 : 0;
+        if ((st = product_launch(q, stream)) != GEMM_OK) break;
+        // B = b A + c A^2
+        q.K = n;
+        q.A = q.B = q.R = A;
+        q.a_mn = q.b_mn = 0;
+        q.D = B;
+        q.alpha = static_cast<float>(L.c / sa);
+        q.alpha_pow = 0;
+        q.beta = L.b;
+        if ((st = product_launch(q, stream)) != GEMM_OK) break;
+        // X = a X + B X, or a X + X B
+        const double sn = last ? static_cast<double>(L.scale) : sx;  // what the new X is multiplied by
+        q.M = L.rows;
+        q.N = L.cols;
+        q.A = tall ? X : B;
+        q.B = tall ? B : X;
+        q.b_mn = !tall;
+        q.symmetric = 0;
+        q.R = X;
+        q.alpha = static_cast<float>(first ? sn / sa : sn / (sa * sx));
+        q.beta = static_cast<float>(first ? L.a * sn : L.a * sn / sx);
+        q.alpha_pow = q.beta_pow = first;
+        if (last) {
+            q.padded = 0;
+            q.D = {L.out, L.ldo, L.stride_o};
+            q.out_bf16 = L.out_bf16;
+        } else {
+            q.D = {ws + at.x[(s + 1) & 1], ldx, L.rows * ldx};
+        }
+        st = product_launch(q, stream);
+    }
+    return st;
+}
+
+}  // namespace ssp

@@ -1,0 +1,573 @@
+// product_few_sm103a.cu -- the products of a 16-bit linear layer for few rows, or
+// few tiles: D = epilogue(A B) on single CTAs and clusters (tcgen05).
+//
+// The roles of the operands are exchanged: 128 columns of the result (rows of
+// the weights) are the MMA's M side and MT = 16 to 256 rows its N side, so one
+// row costs a 16-wide MMA instead of a 128-row tile that is empty but for one
+// row.  K is cut over the CTAs of a cluster, whose fp32 partials meet in
+// distributed shared memory and are added in rank order, so that a narrow product
+// or a long sum still keeps every SM loading.  Bound by reading the operands.
+//
+// Every wait is bounded as in product_pair_sm103a.cu.
+#include <mutex>
+
+#include "activation.cuh"
+#include "product.cuh"
+
+namespace ssp {
+
+__device__ GemmDeviceStatus g_product_few_status;
+
+namespace {
+
+constexpr int THREADS = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr int kMaxStages = 12;
+constexpr int kTwo = 64;   // widest MT of which two CTAs fit an SM
+constexpr int kPush = 32;  // widest MT with room of its own for the cluster's partials
+
+struct FewParams {
+    int M, N;
+    int tiles_m, tiles_n, k_blocks;
+    int split;       // CTAs of a cluster, each with a part of K
+    int stages;
+    int acc_blocks;  // K blocks that one accumulator sums
+    uint32_t tmem_cols;
+    int f_mn, t_mn;  // the weights' side (columns of the result) and the rows'
+    uint32_t idesc;
+    int epi, act;
+    int bf16;        // type of the 16-bit tensors, of the output for EPI_STEP
+    float alpha, beta;
+    const float* factor;
+    int alpha_pow, beta_pow;
+    const void* bias;
+    ProductMatrix D, R, P;
+    unsigned long long wait_limit_ns;
+    int withhold;
+};
+
+struct FewCtl {
+    unsigned long long bar[2 * kMaxStages + 1];  // full, empty, done
+    uint32_t tmem_base;
+    int abort;
+    alignas(16) float bias[128];
+};
+static_assert(sizeof(FewCtl) % 16 == 0, "pushed partials follow");
+
+// Four adjacent elements of a row, of which `left` lie in it.
+__device__ __forceinline__ float4 load_quad16(bool bf16, const void* p, long long i, int left) {
+    if (left >= 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+        const float2 a = unpack16(bf16, u.x), b = unpack16(bf16, u.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(load16(bf16, p, i), left > 1 ? load16(bf16, p, i + 1) : 0.0f,
+                       left > 2 ? load16(bf16, p, i + 2) : 0.0f, 0.0f);
+}
+
+__device__ __forceinline__ void store_quad16(bool bf16, const void* p, long long i, int left, float4 v) {
+    uint16_t* d = static_cast<uint16_t*>(const_cast<void*>(p)) + i;
+    const uint32_t lo = pack16(bf16, v.x, v.y), hi = pack16(bf16, v.z, v.w);
+    if (left >= 4) {
+        *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+    } else {
+        d[0] = static_cast<uint16_t>(lo);
+        if (left > 1) d[1] = static_cast<uint16_t>(lo >> 16);
+        if (left > 2) d[2] = static_cast<uint16_t>(hi);
+    }
+}
+
+// The epilogue of four adjacent sums v of row `row` from column n on.
+__device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, int n, float4 v, float4 bias,
+                                            float alpha, float beta) {
+    const int left = p.N - n;
+    if (left <= 0) return;
+    const bool bf16 = p.bf16 != 0;
+    auto at = [&](const ProductMatrix& m) {
+        return static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld + n;
+    };
+    if (p.epi == EPI_F32) {
+        const float* r = static_cast<const float*>(p.R.p);
+        float* d = static_cast<float*>(const_cast<void*>(p.D.p)) + at(p.D);
+        if (r) {
+            r += at(p.R);
+            if (left >= 4) {
+                const float4 u = *reinterpret_cast<const float4*>(r);
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            } else {
+                v.x += r[0];
+                if (left > 1) v.y += r[1];
+                if (left > 2) v.z += r[2];
+            }
+        }
+        if (left >= 4) {
+            *reinterpret_cast<float4*>(d) = v;
+        } else {
+            d[0] = v.x;
+            if (left > 1) d[1] = v.y;
+            if (left > 2) d[2] = v.z;
+        }
+        return;
+    }
+    if (p.epi == EPI_LINEAR) {
+        v = make_float4(v.x + bias.x, v.y + bias.y, v.z + bias.z, v.w + bias.w);
+        if (p.P.p) store_quad16(bf16, p.P.p, at(p.P), left, v);
+        with_activation(p.act, [&](auto a) {
+            constexpr int ACT = decltype(a)::value;
+            v = make_float4(activation<ACT>(v.x), activation<ACT>(v.y), activation<ACT>(v.z), activation<ACT>(v.w));
+        });
+    }
+    if (p.epi == EPI_STEP) v = make_float4(alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w);
+    if (p.R.p) {
+        const float4 u = load_quad16(bf16 && p.epi != EPI_STEP, p.R.p, at(p.R), left);
+        v = make_float4(fmaf(beta, u.x, v.x), fmaf(beta, u.y, v.y), fmaf(beta, u.z, v.z), fmaf(beta, u.w, v.w));
+    }
+    if (p.epi == EPI_GRAD) {
+        const float4 u = load_quad16(bf16, p.P.p, at(p.P), left);
+        with_activation(p.act, [&](auto a) {
+            constexpr int ACT = decltype(a)::value;
+            v = make_float4(v.x * derivative<ACT>(u.x), v.y * derivative<ACT>(u.y), v.z * derivative<ACT>(u.z),
+                            v.w * derivative<ACT>(u.w));
+        });
+    }
+    store_quad16(bf16, p.D.p, at(p.D), left, v);
+}
+
+// One 128 (columns) x MT (rows) tile, a part of its K blocks.
+template <int MT>
+__global__ void __launch_bounds__(THREADS)
+    product_few_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmT,
+                       const FewParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    constexpr int T_BYTES = MT * PK * 2;
+    const int S = p.stages;
+    uint8_t* f_ring = smem;
+    uint8_t* t_ring = smem + S * P_TILE_BYTES;
+    FewCtl* ctl = reinterpret_cast<FewCtl*>(t_ring + S * T_BYTES);
+    // Partials of a cut K.  PUSH: every CTA writes its share of each output to
+    // the CTA that owns the output, in room of its own; a row's 32 quads (four
+    // outputs) are dealt to the CTAs in runs.  Else they lie over the ring once
+    // it is read and are fetched, with a second barrier until they have been.
+    constexpr bool PUSH = MT <= kPush;
+    float* part = reinterpret_cast<float*>(smem);  // [MT][128]
+    const uint32_t recv = smem_addr(ctl + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = p.split;
+    const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    int cl = static_cast<int>(blockIdx.x) / split;
+    const int b = cl / (p.tiles_m * p.tiles_n);
+    cl -= b * (p.tiles_m * p.tiles_n);
+    const int m0 = (cl % p.tiles_m) * MT, n0 = (cl / p.tiles_m) * 128;
+    const int k0 = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / split);
+    const int k1 = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / split);
+    const uint32_t bar0 = smem_addr(&ctl->bar[0]);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * S);
+    volatile int* abort_flag = &ctl->abort;
+
+    if (threadIdx.x == 0) {
+        if (p.k_blocks) {
+            tma_prefetch_desc(&tmF);
+            tma_prefetch_desc(&tmT);
+        }
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        ctl->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&ctl->tmem_base), p.tmem_cols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (PUSH && split > 1) cluster_arrive_relaxed();  // this CTA has started: its shared memory may be written to
+    tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    int it = 0;  // thread 0: stages issued
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                if (!product_wait<false>(empty_bar(s), ph ^ 1u, abort_flag, p.wait_limit_ns, &g_product_few_status,
+                                         P_PRODUCER, it))
+                    break;
+                if (!(it == p.withhold && blockIdx.x == 0)) {
+                    const uint32_t f = smem_addr(f_ring + s * P_TILE_BYTES), t = smem_addr(t_ring + s * T_BYTES);
+                    mbar_arrive_expect_tx(full_bar(s), P_TILE_BYTES + T_BYTES);
+                    if (p.f_mn) {
+                        tma_load_3d(f, &tmF, full_bar(s), n0, kb * PK, b);
+                        tma_load_3d(f + P_CHUNK_BYTES, &tmF, full_bar(s), n0 + 64, kb * PK, b);
+                    } else {
+                        tma_load_3d(f, &tmF, full_bar(s), kb * PK, n0, b);
+                    }
+                    if (MT >= 64 && p.t_mn) {
+#pragma unroll
+                        for (int c = 0; c < MT / 64; ++c)
+                            tma_load_3d(t + c * P_CHUNK_BYTES, &tmT, full_bar(s), m0 + 64 * c, kb * PK, b);
+                    } else {
+                        tma_load_3d(t, &tmT, full_bar(s), kb * PK, m0, b);
+                    }
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint64_t f_desc0 = operand_desc(smem_addr(f_ring), p.f_mn);
+        const uint64_t t_desc0 = operand_desc(smem_addr(t_ring), p.t_mn);
+        const uint32_t f_step = operand_step(p.f_mn), t_step = operand_step(p.t_mn);
+        int s = 0;
+        uint32_t ph = 0;
+        uint32_t d_tmem = tmem_base;
+        int in_acc = 0;  // blocks in the present accumulator
+        for (int kb = k0; kb < k1; ++kb) {
+            const bool r = product_wait<false>(full_bar(s), ph, abort_flag, p.wait_limit_ns, &g_product_few_status,
+                                               P_MMA, kb - k0);
+            if (!__all_sync(0xffffffffu, r)) break;
+            tc_fence_after();
+            if (in_acc == p.acc_blocks) {
+                in_acc = 0;
+                d_tmem += MT;
+            }
+            const uint32_t f_off = static_cast<uint32_t>(s * P_TILE_BYTES) / 16u;
+            const uint32_t t_off = static_cast<uint32_t>(s * T_BYTES) / 16u;
+            if (elect_one_sync()) {
+#pragma unroll
+                for (int kk = 0; kk < PK / PUMMA_K; ++kk)
+                    umma_f16(d_tmem, f_desc0 + (f_off + f_step * kk), t_desc0 + (t_off + t_step * kk), p.idesc,
+                             in_acc != 0 || kk != 0);
+                umma_commit(empty_bar(s));
+            }
+            __syncwarp();
+            ++in_acc;
+            if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        // Also after an abort: every MMA this warp issued finishes here.
+        if (elect_one_sync()) umma_commit(done_bar);
+        __syncwarp();
+        drain_wait(done_bar, 0u, p.wait_limit_ns);
+        tc_fence_after();
+        tc_fence_before();
+    } else {
+        const int et = static_cast<int>(threadIdx.x) - 64;  // 0..127
+        ctl->bias[et] = p.bias && n0 + et < p.N ? load16(p.bf16 != 0, p.bias, n0 + et) : 0.0f;
+    }
+    __syncthreads();  // the accumulators are complete and the ring is read
+    tc_fence_after();
+    if (*abort_flag) {
+        // Copies that no MMA waited for land before the ring is reused.
+        if (threadIdx.x == 0)
+            for (int j = it - S > 0 ? it - S : 0; j < it; ++j) {
+                if (j == p.withhold && blockIdx.x == 0) continue;
+                drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1), p.wait_limit_ns);
+            }
+        __syncthreads();
+    }
+    float alpha = 1.0f, beta = 1.0f;
+    if (p.epi == EPI_STEP) {
+        alpha = p.alpha;
+        beta = p.beta;
+        if (p.factor) {
+            alpha *= power_of(p.factor, b, p.alpha_pow);
+            beta *= power_of(p.factor, b, p.beta_pow);
+        }
+    }
+    const int accs = (k1 - k0 + p.acc_blocks - 1) / p.acc_blocks;
+    const int rows = min(MT, p.M - m0);
+    const int most = (32 + split - 1) / split;  // quads of an owner
+    auto first = [&](int r) { return (32 * r + split - 1) / split; };
+    if (PUSH && split > 1) cluster_wait();  // every CTA has started
+    if (warp >= 2) {
+        const int q = warp & 3;
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+        const int n = 32 * q + lane;
+        const int quad = 8 * q + (lane & 7);  // split = 1: this thread's four columns
+        const float4 bias = *reinterpret_cast<const float4*>(ctl->bias + 4 * quad);
+        const int owner = (n >> 2) * split >> 5;
+        const uint32_t push = PUSH && split > 1 ? mapa_shared(recv, static_cast<uint32_t>(owner)) +
+                                                      16u * static_cast<uint32_t>(rank * rows * most + (n >> 2) - first(owner)) +
+                                                      4u * (n & 3)
+                                                : 0u;
+#pragma unroll 1
+        for (int c = 0; c < MT; c += 16) {
+            if (c >= rows) break;
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
+            tmem_ld_wait();
+            if (accs == 0) {  // K = 0
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = 0u;
+            }
+            for (int a = 1; a < accs; ++a) {  // fp32 sums of long K, rounded to nearest
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(a * MT + c), o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(o[i]));
+            }
+            if (PUSH && split > 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < rows)
+                        st_cluster_f32(push + 16u * static_cast<uint32_t>((c + i) * most), __uint_as_float(r[i]));
+            } else if (split > 1) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + n] = __uint_as_float(r[i]);
+            } else {
+                // By way of shared memory, a warp its own, from a column a thread
+                // to four adjacent outputs of four rows a thread.
+                const uint32_t turn = smem_addr(part) + static_cast<uint32_t>(q * 4096 + (c & 16) * 128);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st_shared_u32(turn + static_cast<uint32_t>(i * 128 + lane * 4), r[i]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = c + 4 * i + (lane >> 3);
+                    const uint4 v = ld_shared_v4(turn + static_cast<uint32_t>(i * 512 + (lane >> 3) * 128 + (lane & 7) * 16));
+                    if (m < rows)
+                        finish_quad(p, b, m0 + m, n0 + 4 * quad,
+                                    make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                                __uint_as_float(v.w)),
+                                    bias, alpha, beta);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync_all();
+        // CTA `rank` adds the partials of its outputs in rank order, four
+        // adjacent ones a thread.
+        const int d0 = PUSH ? first(rank) : 0, count = PUSH ? first(rank + 1) - d0 : 32;
+        const int i0 = PUSH ? 0 : rows * 32 * rank / split, i1 = PUSH ? rows * count : rows * 32 * (rank + 1) / split;
+        const uint32_t part_addr = smem_addr(part);
+        for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += THREADS) {
+            const int m = i / count, d = d0 + i % count;
+            float4 u[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < split)
+                    u[c] = ld_cluster_f4(PUSH ? mapa_shared(recv + 16u * static_cast<uint32_t>((c * rows + m) * most + d - d0),
+                                                            static_cast<uint32_t>(rank))
+                                              : mapa_shared(part_addr + 16u * i, static_cast<uint32_t>(c)));
+            float4 v = u[0];
+#pragma unroll
+            for (int c = 1; c < 8; ++c)
+                if (c < split) {
+                    v.x += u[c].x;
+                    v.y += u[c].y;
+                    v.z += u[c].z;
+                    v.w += u[c].w;
+                }
+            finish_quad(p, b, m0 + m, n0 + 4 * d, v, *reinterpret_cast<const float4*>(ctl->bias + 4 * d), alpha, beta);
+        }
+    }
+    if (!PUSH && split > 1) cluster_sync_all();  // the peers have read this CTA's partials
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, p.tmem_cols);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// The kernels' dynamic shared-memory limit is set once a device.
+bool allow_smem(const void* kernel, int slot) {
+    static std::mutex mu;
+    static bool done[64][8] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> g(mu);
+    if (!done[dev][slot])
+        done[dev][slot] =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem) == cudaSuccess;
+    return done[dev][slot];
+}
+
+template <int MT>
+int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t stream) {
+    if (MT < 64 && L.a_mn) return GEMM_ERR_UNSUPPORTED;  // an MN-major operand comes in chunks of 64
+    FewParams p = {};
+    constexpr int STAGE = P_TILE_BYTES + MT * PK * 2;
+    p.M = static_cast<int>(L.M);
+    p.N = static_cast<int>(L.N);
+    p.k_blocks = static_cast<int>((L.K + PK - 1) / PK);
+    p.tiles_m = static_cast<int>((L.M + MT - 1) / MT);
+    p.tiles_n = static_cast<int>((L.N + 127) / 128);
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * L.batch;
+    p.split = split;
+    if (tiles * split > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
+    // Accumulators: as many of MT columns as the longest sum of an fp32 output
+    // asks for.
+    const int blocks = (p.k_blocks + split - 1) / split;
+    p.acc_blocks = L.epi == EPI_F32 ? kProductChunk : p.k_blocks > 0 ? p.k_blocks : 1;
+    const int accs = (blocks + p.acc_blocks - 1) / p.acc_blocks;
+    if (accs * MT > 512) return GEMM_ERR_UNSUPPORTED;
+    p.tmem_cols = 32;
+    while (static_cast<int>(p.tmem_cols) < (accs > 0 ? accs : 1) * MT) p.tmem_cols *= 2;
+    if (p.tmem_cols > 256) two = false;
+    // Two CTAs an SM with half of shared memory each, or a ring as deep as one
+    // CTA's room.
+    const int budget = (two ? 112 : 226) * 1024;
+    // Room for pushed partials: ceil(32/c) quads of a row from each of c CTAs.
+    const int recv = MT <= kPush && split > 1 ? static_cast<int>(L.M < MT ? L.M : MT) * (32 + split) * 16 : 0;
+    const int stages = (budget - 1024 - static_cast<int>(sizeof(FewCtl)) - recv) / STAGE;
+    static_assert(4 * STAGE >= MT * 512, "other partials lie over the ring");
+    p.stages = stages < kMaxStages ? stages : kMaxStages;
+    p.f_mn = L.b_mn;
+    p.t_mn = L.a_mn;
+    p.idesc = product_instruction(128, MT, L.bf16, L.b_mn, L.a_mn);
+    p.epi = L.epi;
+    p.act = L.act;
+    p.bf16 = L.out_bf16;
+    p.alpha = L.alpha;
+    p.beta = L.beta;
+    p.factor = L.factor;
+    p.alpha_pow = L.alpha_pow;
+    p.beta_pow = L.beta_pow;
+    p.bias = L.bias;
+    p.D = L.D;
+    p.R = L.R;
+    p.P = L.P;
+    const DebugHooks d = debug_hooks();
+    p.wait_limit_ns = static_cast<unsigned long long>(d.wait_limit_ns);
+    p.withhold = d.withhold_arrive;
+    int smem = 1024 + p.stages * STAGE + static_cast<int>(sizeof(FewCtl)) + recv;
+    const int least = p.tmem_cols > 256 ? kTmemAloneSmem : kTmemPairedSmem;
+    if (smem < least) smem = least;
+    if (L.plan) {
+        *L.plan = {LINEAR_KERNEL_FEW, MT, split, p.stages, static_cast<int>(tiles * split), smem};
+        return GEMM_OK;
+    }
+    CUtensorMap tmF = {}, tmT = {};
+    if (L.K > 0 && (!encode_operand(&tmF, L.B, L.b_mn, L.bf16, L.N, L.K, L.batch, 128) ||
+                    !encode_operand(&tmT, L.A, L.a_mn, L.bf16, L.M, L.K, L.batch, MT)))
+        return GEMM_ERR_LAUNCH;
+    auto kernel = product_few_kernel<MT>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
+    ProductConfig c(tiles * split, split, THREADS, smem, stream);
+    return product_finish(cudaLaunchKernelEx(&c.cfg, kernel, tmF, tmT, p));
+}
+
+// Which kernel, tile and cut of K: the one with the least time by a model in
+// microseconds.
+//   * few rows: a round of resident CTAs takes each one's K blocks and an
+//     epilogue that grows with MT, twice where two share an SM; a cut K adds the
+//     partials' way through distributed shared memory.
+//   * pairs: a round takes its K blocks at the tensor pipe's rate.
+struct Choice {
+    int mt = 0;  // 0: the pair kernel
+    int split = 1;
+    bool two = false;  // two CTAs an SM
+};
+
+bool choose(const ProductLaunch& L, Choice* best) {
+    int resident[9];
+    if (!product_resident_ctas(resident)) return false;
+    const int64_t kb = (L.K + PK - 1) / PK;
+    if (kb == 0) {  // no operands to read: the epilogue alone
+        *best = {128, 1, false};
+        return true;
+    }
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t tm = up(L.M, 256), tn = up(L.N, 256);
+    const int64_t pairs = (L.symmetric ? tm * (tm + 1) / 2 : tm * tn) * L.batch;
+    double least = 3.4 + static_cast<double>(up(pairs, resident[2] > 1 ? resident[2] / 2 : 1)) * (0.3 * kb + 1.98);
+    const int mt0 = L.a_mn ? 64 : 16;
+    for (int mt = mt0; mt <= 256 && (mt == mt0 || mt < 2 * L.M); mt *= 2) {
+        const int64_t tiles = up(L.M, mt) * up(L.N, 128) * L.batch;
+        for (int c = 1; c <= 8 && c <= kb; ++c) {
+            if (resident[c] <= 0) continue;
+            const int64_t accs = L.epi == EPI_F32 ? up(up(kb, c), kProductChunk) : 1;
+            if (accs * mt > 512) continue;
+            const int64_t ctas = tiles * c;
+            if (ctas > 0x7fffffff) continue;
+            for (int t = 0; t <= (mt <= kTwo && accs * mt <= 256 ? 1 : 0); ++t) {
+                const double rounds = static_cast<double>(up(ctas, resident[c] * (1 + t)));
+                const bool alone = ctas <= resident[c];  // one CTA an SM at most
+                const double block = (t && alone ? 0.29 : 0.163) + 0.0009 * mt;
+                const double us = (t ? 0.74 : 1.93) +
+                                  rounds * (t && !alone ? 2.0 : 1.0) * (up(kb, c) * block + 0.69 + 0.012 * mt) +
+                                  (c > 1 ? 1.17 + 0.0023 * mt + 0.08 * (rounds - 1.0) * c : 0.0);
+                if (us < least) {
+                    least = us;
+                    *best = {mt, c, t == 1};
+                }
+            }
+        }
+    }
+    return true;
+}
+
+}  // namespace
+
+bool product_resident_ctas(int (&out)[9]) {
+    static std::mutex mu;
+    static bool known[64] = {};
+    static int n[64][9] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const void* kernel = reinterpret_cast<const void*>(product_few_kernel<128>);
+    if (!allow_smem(kernel, 3)) return false;
+    std::lock_guard<std::mutex> g(mu);
+    if (!known[dev]) {
+        for (int c = 1; c <= 8; ++c) {
+            ProductConfig cfg(c, c, THREADS, 200 * 1024, nullptr);
+            cfg.cfg.attrs = &cfg.attr[1];  // the cluster alone
+            cfg.cfg.numAttrs = 1;
+            int k = 0;
+            if (cudaOccupancyMaxActiveClusters(&k, kernel, &cfg.cfg) != cudaSuccess) {
+                cudaGetLastError();
+                k = 0;
+            }
+            n[dev][c] = k * c;
+        }
+        if (n[dev][1] <= 0) return false;
+        known[dev] = true;
+    }
+    for (int c = 0; c <= 8; ++c) out[c] = n[dev][c];
+    return true;
+}
+
+int product_few_launch(const ProductLaunch& L, int mt, int split, bool two, cudaStream_t stream) {
+    switch (mt) {
+        case 16: return launch<16>(L, 0, split, two, stream);
+        case 32: return launch<32>(L, 1, split, two, stream);
+        case 64: return launch<64>(L, 2, split, two, stream);
+        case 128: return launch<128>(L, 3, split, two, stream);
+        default: return launch<256>(L, 4, split, two, stream);
+    }
+}
+
+int product_launch(const ProductLaunch& L, cudaStream_t stream) {
+    Choice c;
+    if (!choose(L, &c)) return GEMM_ERR_CUDA;
+    return c.mt ? product_few_launch(L, c.mt, c.split, c.two, stream) : product_pair_launch(L, stream);
+}
+
+int product_few_status(GemmDeviceStatus* out) {
+    const GemmDeviceStatus zero = {0, 0, 0, 0};
+    if (cudaMemcpyFromSymbol(out, g_product_few_status, sizeof(GemmDeviceStatus)) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (cudaMemcpyToSymbol(g_product_few_status, &zero, sizeof(GemmDeviceStatus)) != cudaSuccess) return GEMM_ERR_CUDA;
+    return GEMM_OK;
+}
+
+}  // namespace ssp
