@@ -59,7 +59,9 @@ int product_read_and_clear_status(GemmDeviceStatus* out);
 
 // product_few_sm103a.cu and product_pair_sm103a.cu
 int product_few_launch(const ProductLaunch& L, int mt, int split, bool two, cudaStream_t stream);
-int product_pair_launch(const ProductLaunch& L, cudaStream_t stream);
+int product_pair_launch(const ProductLaunch& L, int bn, cudaStream_t stream);
+// CTA pairs that the current device holds at once.
+int product_resident_pairs();
 // CTAs (one an SM) that the current device holds at once, by cluster size 1..8.
 bool product_resident_ctas(int (&out)[9]);
 int product_few_status(GemmDeviceStatus* out);

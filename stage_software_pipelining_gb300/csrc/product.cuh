@@ -7,7 +7,12 @@
 //   * K-major (adjacent k): rows of 64 k, one 128-byte swizzle row each;
 //   * MN-major (adjacent rows or columns of the result, as dz and x lie for
 //     dz^T x): chunks of 64 of them, a 128-byte swizzle row a k, 8 KB a chunk.
-// Either way 128 rows or columns of a stage are 16 KB.
+// Either way 128 rows or columns of a stage are 16 KB.  All chunks of an MN-major
+// stage come by one copy, through a map that has the chunk as a dimension of its
+// own, 64 elements from one to the next; a copy a chunk cost 7 % of the pair
+// kernel's time for each such operand (4096^3: 82 us, with chunks by themselves 89
+// for one and 98 for two).  Where a tile's chunks reach past the matrix they come
+// one by one, from a map that ends where the matrix does.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -145,12 +150,34 @@ inline CUtensorMapDataType type16(int bf16) {
     return bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// An operand with `len` rows or columns of the result and sums of K: boxes of 64
-// k by `tile`, or (MN-major) of 64 rows or columns by 64 k.
-inline bool encode_operand(CUtensorMap* map, const ProductMatrix& m, int mn, int bf16, int64_t len, int64_t K,
-                           int64_t batch, int tile) {
-    return mn ? encode_matrices(map, type16(bf16), 2, CU_TENSOR_MAP_SWIZZLE_128B, m, K, len, batch, 64, PK)
-              : encode_matrices(map, type16(bf16), 2, CU_TENSOR_MAP_SWIZZLE_128B, m, len, K, batch, PK, tile);
+// An operand with `len` rows or columns of the result and sums of K, `tile` of them
+// a stage.  `map`: boxes of 64 k by `tile`, or (MN-major) all chunks of a stage at
+// once, for tiles that lie within the matrix; `edge`: (MN-major) boxes of 64 rows or
+// columns by 64 k.
+inline bool encode_operand(CUtensorMap* map, CUtensorMap* edge, const ProductMatrix& m, int mn, int bf16, int64_t len,
+                           int64_t K, int64_t batch, int tile) {
+    if (!mn) {
+        *edge = {};
+        return encode_matrices(map, type16(bf16), 2, CU_TENSOR_MAP_SWIZZLE_128B, m, len, K, batch, PK, tile);
+    }
+    if (!encode_matrices(edge, type16(bf16), 2, CU_TENSOR_MAP_SWIZZLE_128B, m, K, len, batch, 64, PK)) return false;
+    const int chunks = (tile + 63) / 64;
+    if (len < 64 * chunks) {  // no tile lies within the matrix
+        *map = *edge;
+        return true;
+    }
+    auto fn = tensor_map_encoder();
+    const int64_t ld = K > 1 ? m.ld : (len + 7) / 8 * 8;
+    const int64_t stride = batch > 1 ? m.stride : ld;
+    // Elements of a chunk start where the last one's still end within the row.
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(len - 64 * (chunks - 1)), static_cast<cuuint64_t>(K),
+                          static_cast<cuuint64_t>(chunks), static_cast<cuuint64_t>(batch)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld * 2), 128, static_cast<cuuint64_t>(stride * 2)};
+    cuuint32_t box[4] = {64, PK, static_cast<cuuint32_t>(chunks), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, type16(bf16), 4, const_cast<void*>(m.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct ProductConfig {

@@ -25,6 +25,10 @@ constexpr int kMaxStages = 12;
 constexpr int kTwo = 64;   // widest MT of which two CTAs fit an SM
 constexpr int kPush = 32;  // widest MT with room of its own for the cluster's partials
 
+struct FewMaps {
+    CUtensorMap F, F_edge, T, T_edge;
+};
+
 struct FewParams {
     int M, N;
     int tiles_m, tiles_n, k_blocks;
@@ -33,6 +37,7 @@ struct FewParams {
     int acc_blocks;  // K blocks that one accumulator sums
     uint32_t tmem_cols;
     int f_mn, t_mn;  // the weights' side (columns of the result) and the rows'
+    int f_whole, t_whole;  // columns and rows below which a stage's chunks come by one copy
     uint32_t idesc;
     int epi, act;
     int bf16;        // type of the 16-bit tensors, of the output for EPI_STEP
@@ -53,15 +58,47 @@ struct FewCtl {
 };
 static_assert(sizeof(FewCtl) % 16 == 0, "pushed partials follow");
 
-// Four adjacent elements of a row, of which `left` lie in it.
-__device__ __forceinline__ float4 load_quad16(bool bf16, const void* p, long long i, int left) {
-    if (left >= 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-        const float2 a = unpack16(bf16, u.x), b = unpack16(bf16, u.y);
-        return make_float4(a.x, a.y, b.x, b.y);
+// What the epilogue of four adjacent outputs reads: asked for ahead of their sums.
+struct QuadInputs {
+    uint4 r;  // fp32, or 16 bits in x and y
+    uint2 p;
+};
+
+__device__ __forceinline__ long long place(const ProductMatrix& m, int b, int row, int n) {
+    return static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld + n;
+}
+
+__device__ __forceinline__ uint2 load_quad16(const void* p, long long i, int left) {
+    const uint16_t* s = static_cast<const uint16_t*>(p) + i;
+    if (left >= 4) return *reinterpret_cast<const uint2*>(s);
+    const uint32_t x = s[0], y = left > 1 ? s[1] : 0, z = left > 2 ? s[2] : 0;
+    return make_uint2(x | (y << 16), z);
+}
+
+// Columns n.. of row `row`, of which the row has at least one.
+__device__ __forceinline__ QuadInputs fetch_quad(const FewParams& p, int b, int row, int n) {
+    QuadInputs in = {};
+    const int left = p.N - n;
+    if (left <= 0) return in;
+    if (p.R.p) {
+        const long long i = place(p.R, b, row, n);
+        if (p.epi != EPI_F32) {
+            const uint2 u = load_quad16(p.R.p, i, left);
+            in.r.x = u.x;
+            in.r.y = u.y;
+        } else {
+            const uint32_t* s = static_cast<const uint32_t*>(p.R.p) + i;
+            if (left >= 4) in.r = *reinterpret_cast<const uint4*>(s);
+            else in.r = make_uint4(s[0], left > 1 ? s[1] : 0, left > 2 ? s[2] : 0, 0);
+        }
     }
-    return make_float4(load16(bf16, p, i), left > 1 ? load16(bf16, p, i + 1) : 0.0f,
-                       left > 2 ? load16(bf16, p, i + 2) : 0.0f, 0.0f);
+    if (p.epi == EPI_GRAD) in.p = load_quad16(p.P.p, place(p.P, b, row, n), left);
+    return in;
+}
+
+__device__ __forceinline__ float4 quad16(bool bf16, uint32_t lo, uint32_t hi) {
+    const float2 a = unpack16(bf16, lo), b = unpack16(bf16, hi);
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 __device__ __forceinline__ void store_quad16(bool bf16, const void* p, long long i, int left, float4 v) {
@@ -77,28 +114,16 @@ __device__ __forceinline__ void store_quad16(bool bf16, const void* p, long long
 }
 
 // The epilogue of four adjacent sums v of row `row` from column n on.
-__device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, int n, float4 v, float4 bias,
-                                            float alpha, float beta) {
+__device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, int n, float4 v,
+                                            const QuadInputs& in, float4 bias, float alpha, float beta) {
     const int left = p.N - n;
     if (left <= 0) return;
     const bool bf16 = p.bf16 != 0;
-    auto at = [&](const ProductMatrix& m) {
-        return static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld + n;
-    };
     if (p.epi == EPI_F32) {
-        const float* r = static_cast<const float*>(p.R.p);
-        float* d = static_cast<float*>(const_cast<void*>(p.D.p)) + at(p.D);
-        if (r) {
-            r += at(p.R);
-            if (left >= 4) {
-                const float4 u = *reinterpret_cast<const float4*>(r);
-                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-            } else {
-                v.x += r[0];
-                if (left > 1) v.y += r[1];
-                if (left > 2) v.z += r[2];
-            }
-        }
+        if (p.R.p)
+            v = make_float4(v.x + __uint_as_float(in.r.x), v.y + __uint_as_float(in.r.y), v.z + __uint_as_float(in.r.z),
+                            v.w + __uint_as_float(in.r.w));
+        float* d = static_cast<float*>(const_cast<void*>(p.D.p)) + place(p.D, b, row, n);
         if (left >= 4) {
             *reinterpret_cast<float4*>(d) = v;
         } else {
@@ -110,7 +135,7 @@ __device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, 
     }
     if (p.epi == EPI_LINEAR) {
         v = make_float4(v.x + bias.x, v.y + bias.y, v.z + bias.z, v.w + bias.w);
-        if (p.P.p) store_quad16(bf16, p.P.p, at(p.P), left, v);
+        if (p.P.p) store_quad16(bf16, p.P.p, place(p.P, b, row, n), left, v);
         with_activation(p.act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
             v = make_float4(activation<ACT>(v.x), activation<ACT>(v.y), activation<ACT>(v.z), activation<ACT>(v.w));
@@ -118,25 +143,24 @@ __device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, 
     }
     if (p.epi == EPI_STEP) v = make_float4(alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w);
     if (p.R.p) {
-        const float4 u = load_quad16(bf16 && p.epi != EPI_STEP, p.R.p, at(p.R), left);
+        const float4 u = quad16(bf16 && p.epi != EPI_STEP, in.r.x, in.r.y);
         v = make_float4(fmaf(beta, u.x, v.x), fmaf(beta, u.y, v.y), fmaf(beta, u.z, v.z), fmaf(beta, u.w, v.w));
     }
     if (p.epi == EPI_GRAD) {
-        const float4 u = load_quad16(bf16, p.P.p, at(p.P), left);
+        const float4 u = quad16(bf16, in.p.x, in.p.y);
         with_activation(p.act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
             v = make_float4(v.x * derivative<ACT>(u.x), v.y * derivative<ACT>(u.y), v.z * derivative<ACT>(u.z),
                             v.w * derivative<ACT>(u.w));
         });
     }
-    store_quad16(bf16, p.D.p, at(p.D), left, v);
+    store_quad16(bf16, p.D.p, place(p.D, b, row, n), left, v);
 }
 
 // One 128 (columns) x MT (rows) tile, a part of its K blocks.
 template <int MT>
 __global__ void __launch_bounds__(THREADS)
-    product_few_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmT,
-                       const FewParams p) {
+    product_few_kernel(const __grid_constant__ FewMaps maps, const FewParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -170,8 +194,8 @@ __global__ void __launch_bounds__(THREADS)
 
     if (threadIdx.x == 0) {
         if (p.k_blocks) {
-            tma_prefetch_desc(&tmF);
-            tma_prefetch_desc(&tmT);
+            tma_prefetch_desc(&maps.F);
+            tma_prefetch_desc(&maps.T);
         }
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
@@ -205,18 +229,22 @@ __global__ void __launch_bounds__(THREADS)
                 if (!(it == p.withhold && blockIdx.x == 0)) {
                     const uint32_t f = smem_addr(f_ring + s * P_TILE_BYTES), t = smem_addr(t_ring + s * T_BYTES);
                     mbar_arrive_expect_tx(full_bar(s), P_TILE_BYTES + T_BYTES);
-                    if (p.f_mn) {
-                        tma_load_3d(f, &tmF, full_bar(s), n0, kb * PK, b);
-                        tma_load_3d(f + P_CHUNK_BYTES, &tmF, full_bar(s), n0 + 64, kb * PK, b);
+                    if (!p.f_mn) {
+                        tma_load_3d(f, &maps.F, full_bar(s), kb * PK, n0, b);
+                    } else if (n0 < p.f_whole) {
+                        tma_load_4d(f, &maps.F, full_bar(s), n0, kb * PK, 0, b);
                     } else {
-                        tma_load_3d(f, &tmF, full_bar(s), kb * PK, n0, b);
+                        tma_load_3d(f, &maps.F_edge, full_bar(s), n0, kb * PK, b);
+                        tma_load_3d(f + P_CHUNK_BYTES, &maps.F_edge, full_bar(s), n0 + 64, kb * PK, b);
                     }
-                    if (MT >= 64 && p.t_mn) {
+                    if (MT < 64 || !p.t_mn) {
+                        tma_load_3d(t, &maps.T, full_bar(s), kb * PK, m0, b);
+                    } else if (m0 < p.t_whole) {
+                        tma_load_4d(t, &maps.T, full_bar(s), m0, kb * PK, 0, b);
+                    } else {
 #pragma unroll
                         for (int c = 0; c < MT / 64; ++c)
-                            tma_load_3d(t + c * P_CHUNK_BYTES, &tmT, full_bar(s), m0 + 64 * c, kb * PK, b);
-                    } else {
-                        tma_load_3d(t, &tmT, full_bar(s), kb * PK, m0, b);
+                            tma_load_3d(t + c * P_CHUNK_BYTES, &maps.T_edge, full_bar(s), m0 + 64 * c, kb * PK, b);
                     }
                 }
                 if (++s == S) {
@@ -305,7 +333,18 @@ __global__ void __launch_bounds__(THREADS)
                                                       16u * static_cast<uint32_t>(rank * rows * most + (n >> 2) - first(owner)) +
                                                       4u * (n & 3)
                                                 : 0u;
-#pragma unroll 1
+        // Uncut: this thread's outputs of 16 rows, rows c + 4 i + lane / 8; what their
+        // epilogue reads is asked for 16 rows ahead.
+        QuadInputs in[4];
+        auto ask = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = c + 4 * i + (lane >> 3);
+                if (m < rows) in[i] = fetch_quad(p, b, m0 + m, n0 + 4 * quad);
+            }
+        };
+        if (split == 1) ask(0);
+#pragma unroll 2
         for (int c = 0; c < MT; c += 16) {
             if (c >= rows) break;
             uint32_t r[16];
@@ -337,15 +376,21 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) st_shared_u32(turn + static_cast<uint32_t>(i * 128 + lane * 4), r[i]);
                 __syncwarp();
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(turn + static_cast<uint32_t>(i * 512 + lane * 16));
+                QuadInputs had[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) had[i] = in[i];
+                ask(c + 16);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = c + 4 * i + (lane >> 3);
-                    const uint4 v = ld_shared_v4(turn + static_cast<uint32_t>(i * 512 + (lane >> 3) * 128 + (lane & 7) * 16));
                     if (m < rows)
                         finish_quad(p, b, m0 + m, n0 + 4 * quad,
-                                    make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                                                __uint_as_float(v.w)),
-                                    bias, alpha, beta);
+                                    make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y),
+                                                __uint_as_float(v[i].z), __uint_as_float(v[i].w)),
+                                    had[i], bias, alpha, beta);
                 }
             }
         }
@@ -359,25 +404,39 @@ __global__ void __launch_bounds__(THREADS)
         const int d0 = PUSH ? first(rank) : 0, count = PUSH ? first(rank + 1) - d0 : 32;
         const int i0 = PUSH ? 0 : rows * 32 * rank / split, i1 = PUSH ? rows * count : rows * 32 * (rank + 1) / split;
         const uint32_t part_addr = smem_addr(part);
-        for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += THREADS) {
-            const int m = i / count, d = d0 + i % count;
-            float4 u[8];
+        // Four quads a thread at a time, so that their loads are under way together.
+        constexpr int Q = 4;
+        for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += Q * THREADS) {
+            QuadInputs in[Q];
+            float4 v[Q];
+            uint32_t at[Q];  // of a partial in its CTA
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < split)
-                    u[c] = ld_cluster_f4(PUSH ? mapa_shared(recv + 16u * static_cast<uint32_t>((c * rows + m) * most + d - d0),
-                                                            static_cast<uint32_t>(rank))
-                                              : mapa_shared(part_addr + 16u * i, static_cast<uint32_t>(c)));
-            float4 v = u[0];
+            for (int k = 0; k < Q; ++k) {
+                const int j = min(i + k * THREADS, i1 - 1), m = j / count, d = d0 + j % count;
+                in[k] = fetch_quad(p, b, m0 + m, n0 + 4 * d);
+                at[k] = PUSH ? recv + 16u * static_cast<uint32_t>(m * most + d - d0) : part_addr + 16u * j;
+                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            const uint32_t step = PUSH ? 16u * static_cast<uint32_t>(rows * most) : 0u;
+#pragma unroll 2
+            for (int c = 0; c < split; ++c) {
+                float4 u[Q];
 #pragma unroll
-            for (int c = 1; c < 8; ++c)
-                if (c < split) {
-                    v.x += u[c].x;
-                    v.y += u[c].y;
-                    v.z += u[c].z;
-                    v.w += u[c].w;
-                }
-            finish_quad(p, b, m0 + m, n0 + 4 * d, v, *reinterpret_cast<const float4*>(ctl->bias + 4 * d), alpha, beta);
+                for (int k = 0; k < Q; ++k)
+                    u[k] = ld_cluster_f4(mapa_shared(at[k] + static_cast<uint32_t>(c) * step,
+                                                     static_cast<uint32_t>(PUSH ? rank : c)));
+#pragma unroll
+                for (int k = 0; k < Q; ++k)
+                    v[k] = c ? make_float4(v[k].x + u[k].x, v[k].y + u[k].y, v[k].z + u[k].z, v[k].w + u[k].w) : u[k];
+            }
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const int j = i + k * THREADS;
+                if (j >= i1) break;
+                const int m = j / count, d = d0 + j % count;
+                finish_quad(p, b, m0 + m, n0 + 4 * d, v[k], in[k], *reinterpret_cast<const float4*>(ctl->bias + 4 * d),
+                            alpha, beta);
+            }
         }
     }
     if (!PUSH && split > 1) cluster_sync_all();  // the peers have read this CTA's partials
@@ -434,6 +493,8 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
     p.stages = stages < kMaxStages ? stages : kMaxStages;
     p.f_mn = L.b_mn;
     p.t_mn = L.a_mn;
+    p.f_whole = p.N - 127;
+    p.t_whole = p.M - (MT - 1);
     p.idesc = product_instruction(128, MT, L.bf16, L.b_mn, L.a_mn);
     p.epi = L.epi;
     p.act = L.act;
@@ -457,14 +518,14 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
         *L.plan = {LINEAR_KERNEL_FEW, MT, split, p.stages, static_cast<int>(tiles * split), smem};
         return GEMM_OK;
     }
-    CUtensorMap tmF = {}, tmT = {};
-    if (L.K > 0 && (!encode_operand(&tmF, L.B, L.b_mn, L.bf16, L.N, L.K, L.batch, 128) ||
-                    !encode_operand(&tmT, L.A, L.a_mn, L.bf16, L.M, L.K, L.batch, MT)))
+    FewMaps maps = {};
+    if (L.K > 0 && (!encode_operand(&maps.F, &maps.F_edge, L.B, L.b_mn, L.bf16, L.N, L.K, L.batch, 128) ||
+                    !encode_operand(&maps.T, &maps.T_edge, L.A, L.a_mn, L.bf16, L.M, L.K, L.batch, MT)))
         return GEMM_ERR_LAUNCH;
     auto kernel = product_few_kernel<MT>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
     ProductConfig c(tiles * split, split, THREADS, smem, stream);
-    return product_finish(cudaLaunchKernelEx(&c.cfg, kernel, tmF, tmT, p));
+    return product_finish(cudaLaunchKernelEx(&c.cfg, kernel, maps, p));
 }
 
 // Which kernel, tile and cut of K: the one with the least time by a model in
@@ -475,6 +536,7 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
 //   * pairs: a round takes its K blocks at the tensor pipe's rate.
 struct Choice {
     int mt = 0;  // 0: the pair kernel
+    int bn = 256;  // its tiles' width
     int split = 1;
     bool two = false;  // two CTAs an SM
 };
@@ -484,13 +546,27 @@ bool choose(const ProductLaunch& L, Choice* best) {
     if (!product_resident_ctas(resident)) return false;
     const int64_t kb = (L.K + PK - 1) / PK;
     if (kb == 0) {  // no operands to read: the epilogue alone
-        *best = {128, 1, false};
+        best->mt = 128;
         return true;
     }
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    const int64_t tm = up(L.M, 256), tn = up(L.N, 256);
-    const int64_t pairs = (L.symmetric ? tm * (tm + 1) / 2 : tm * tn) * L.batch;
-    double least = 3.4 + static_cast<double>(up(pairs, resident[2] > 1 ? resident[2] / 2 : 1)) * (0.3 * kb + 1.98);
+    const int64_t tm = up(L.M, 256);
+    const int64_t units = product_resident_pairs();
+    if (units <= 0) return false;
+    double least = 1e30;
+    // Microseconds of a K block by the tile's width: 256, 224, 192.  (An MN-major B's
+    // narrower tiles do not start on whole 128-byte lines.)
+    const double kBlock[3] = {0.2925, L.b_mn ? 0.294 : 0.273, L.b_mn ? 0.27 : 0.244};
+    for (int w = 0; w < (L.symmetric ? 1 : 3); ++w) {
+        const int bn = 256 - 32 * w;
+        const int64_t tn = up(L.N, bn);
+        const int64_t pairs = (L.symmetric ? tm * (tm + 1) / 2 : tm * tn) * L.batch;
+        const double us = 5.3 + static_cast<double>(up(pairs, units)) * (kBlock[w] * kb + 0.55);
+        if (us < least) {
+            least = us;
+            best->bn = bn;
+        }
+    }
     const int mt0 = L.a_mn ? 64 : 16;
     for (int mt = mt0; mt <= 256 && (mt == mt0 || mt < 2 * L.M); mt *= 2) {
         const int64_t tiles = up(L.M, mt) * up(L.N, 128) * L.batch;
@@ -509,7 +585,9 @@ bool choose(const ProductLaunch& L, Choice* best) {
                                   (c > 1 ? 1.17 + 0.0023 * mt + 0.08 * (rounds - 1.0) * c : 0.0);
                 if (us < least) {
                     least = us;
-                    *best = {mt, c, t == 1};
+                    best->mt = mt;
+                    best->split = c;
+                    best->two = t == 1;
                 }
             }
         }
@@ -560,7 +638,7 @@ int product_few_launch(const ProductLaunch& L, int mt, int split, bool two, cuda
 int product_launch(const ProductLaunch& L, cudaStream_t stream) {
     Choice c;
     if (!choose(L, &c)) return GEMM_ERR_CUDA;
-    return c.mt ? product_few_launch(L, c.mt, c.split, c.two, stream) : product_pair_launch(L, stream);
+    return c.mt ? product_few_launch(L, c.mt, c.split, c.two, stream) : product_pair_launch(L, c.bn, stream);
 }
 
 int product_few_status(GemmDeviceStatus* out) {
