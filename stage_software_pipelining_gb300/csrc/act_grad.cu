@@ -42,7 +42,7 @@ struct Values<1> {
     uint32_t u[1];
 };
 
-// VEC adjacent values, of which `left` are in the row.
+// VEC adjacent values, of which `left` are in the row (one: and a zero beside it).
 template <int VEC>
 __device__ __forceinline__ Values<VEC> load(const uint16_t* p, int left) {
     Values<VEC> v;
@@ -65,7 +65,7 @@ __device__ __forceinline__ Values<VEC> load(const uint16_t* p, int left) {
 // Strips of VEC * GROUPS columns; ROWS rows at a time.  VEC = 8 wants rows on
 // 16-byte boundaries.
 template <bool BF16, int VEC, int ACT>
-__device__ __forceinline__ void pass(const Params& p, int r0, int r1, int c, float (&sum)[VEC]) {
+__device__ __forceinline__ void pass(const Params& p, int r0, int r1, int c, Pair (&sum)[(VEC + 1) / 2]) {
     constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS;
     constexpr int AHEAD = 4;  // rows of a thread whose loads are under way together
     const int left = p.N - c;
@@ -87,15 +87,10 @@ __device__ __forceinline__ void pass(const Params& p, int r0, int r1, int c, flo
             uint32_t out[VEC == 8 ? 4 : 1];
 #pragma unroll
             for (int i = 0; i < (VEC + 1) / 2; ++i) {
-                float2 g = unpack16<BF16>(dy[a].u[i]);
-                if constexpr (ACT != LINEAR_ACT_NONE) {
-                    const float2 f = unpack16<BF16>(z[a].u[i]);
-                    g.x *= derivative<ACT>(f.x);
-                    if (VEC > 1) g.y *= derivative<ACT>(f.y);
-                }
-                sum[2 * i] += g.x;
-                if (VEC > 1) sum[(2 * i + 1) % VEC] += g.y;
-                out[i] = pack16<BF16>(g.x, g.y);
+                Pair g = unpack16_pair<BF16>(dy[a].u[i]);
+                if constexpr (ACT != LINEAR_ACT_NONE) g = mul2(g, derivative<ACT>(unpack16_pair<BF16>(z[a].u[i])));
+                sum[i] = add2(sum[i], g);
+                out[i] = pack16<BF16>(g);
             }
             if (p.dz) {
                 uint16_t* d = p.dz + row * p.lddz + c;
@@ -124,14 +119,17 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(const Params p) {
     const int col0 = static_cast<int>(blockIdx.x) * COLS;
     const int c = col0 + static_cast<int>(threadIdx.x % GROUPS) * VEC;
     const int r0 = min(p.M, rank * p.rows), r1 = min(p.M, r0 + p.rows);
-    float sum[VEC] = {};
+    Pair sum[(VEC + 1) / 2] = {};
     if (p.act == LINEAR_ACT_NONE)
         pass<BF16, VEC, LINEAR_ACT_NONE>(p, r0, r1, c, sum);
     else
         with_activation(p.act, [&](auto a) { pass<BF16, VEC, decltype(a)::value>(p, r0, r1, c, sum); });
     if (!p.dbias) return;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sums[threadIdx.x / GROUPS][(threadIdx.x % GROUPS) * VEC + i] = sum[i];
+    for (int i = 0; i < VEC; ++i) {
+        const float2 s = both(sum[i / 2]);
+        sums[threadIdx.x / GROUPS][(threadIdx.x % GROUPS) * VEC + i] = i & 1 ? s.y : s.x;
+    }
     __syncthreads();
     if (threadIdx.x < COLS) {
         float s = 0.0f;

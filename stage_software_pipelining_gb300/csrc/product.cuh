@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "activation.cuh"
 #include "internal.h"
 #include "linear.h"
 #include "ptx.cuh"
@@ -96,6 +97,11 @@ __device__ __forceinline__ uint32_t pack16(float x, float y) {
         return *reinterpret_cast<const uint32_t*>(&o);
     }
 }
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(Pair p) {
+    const float2 v = both(p);
+    return pack16<BF16>(v.x, v.y);
+}
 __device__ __forceinline__ uint32_t pack16(bool bf16, float x, float y) {
     return bf16 ? pack16<true>(x, y) : pack16<false>(x, y);
 }
@@ -109,6 +115,11 @@ __device__ __forceinline__ float2 unpack16(uint32_t v) {
 }
 __device__ __forceinline__ float2 unpack16(bool bf16, uint32_t v) {
     return bf16 ? unpack16<true>(v) : unpack16<false>(v);
+}
+template <bool BF16>
+__device__ __forceinline__ Pair unpack16_pair(uint32_t v) {
+    const float2 f = unpack16<BF16>(v);
+    return make_pair2(f.x, f.y);
 }
 template <bool BF16>
 __device__ __forceinline__ float load16(const void* p, long long i) {

@@ -138,7 +138,8 @@ __device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, 
         if (p.P.p) store_quad16(bf16, p.P.p, place(p.P, b, row, n), left, v);
         with_activation(p.act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
-            v = make_float4(activation<ACT>(v.x), activation<ACT>(v.y), activation<ACT>(v.z), activation<ACT>(v.w));
+            const float2 lo = both(activation<ACT>(make_pair2(v.x, v.y))), hi = both(activation<ACT>(make_pair2(v.z, v.w)));
+            v = make_float4(lo.x, lo.y, hi.x, hi.y);
         });
     }
     if (p.epi == EPI_STEP) v = make_float4(alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w);
@@ -150,8 +151,8 @@ __device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, 
         const float4 u = quad16(bf16, in.p.x, in.p.y);
         with_activation(p.act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
-            v = make_float4(v.x * derivative<ACT>(u.x), v.y * derivative<ACT>(u.y), v.z * derivative<ACT>(u.z),
-                            v.w * derivative<ACT>(u.w));
+            const float2 lo = both(derivative<ACT>(make_pair2(u.x, u.y))), hi = both(derivative<ACT>(make_pair2(u.z, u.w)));
+            v = make_float4(v.x * lo.x, v.y * lo.y, v.z * hi.x, v.w * hi.y);
         });
     }
     store_quad16(bf16, p.D.p, place(p.D, b, row, n), left, v);

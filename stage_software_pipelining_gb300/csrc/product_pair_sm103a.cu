@@ -104,28 +104,27 @@ __device__ __forceinline__ void tile_coords(const PairParams& p, int t, int& b, 
     if (g & 1) tn = p.tiles_n - 1 - tn;
 }
 
-// Thirty-two 16-bit values of this thread's row of a box of 64 or 32 columns, in
-// pairs, from the half h.
-template <int W>
-__device__ __forceinline__ uint32_t piece_addr(uint32_t buf, int lane, int j) {
-    return W == 64 ? buf + lane * 128 + ((j ^ (lane & 7)) << 4) : buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+// Where 16-byte piece j of this thread's row of a box lies: rows of 128 bytes, or
+// (narrow) of 64.
+__device__ __forceinline__ uint32_t piece_addr(uint32_t buf, int lane, int j, bool narrow = false) {
+    return narrow ? buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4) : buf + lane * 128 + ((j ^ (lane & 7)) << 4);
 }
-template <int W>
-__device__ __forceinline__ void read_box(uint32_t buf, int lane, int h, uint32_t (&u)[16]) {
+// Thirty-two 16-bit values of it, in pairs, from the half h.
+__device__ __forceinline__ void read_box(uint32_t buf, int lane, int h, bool narrow, uint32_t (&u)[16]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint4 v = ld_shared_v4(piece_addr<W>(buf, lane, 4 * h + j));
+        const uint4 v = ld_shared_v4(piece_addr(buf, lane, 4 * h + j, narrow));
         u[4 * j] = v.x;
         u[4 * j + 1] = v.y;
         u[4 * j + 2] = v.z;
         u[4 * j + 3] = v.w;
     }
 }
-template <int W>
-__device__ __forceinline__ void write_box(uint32_t buf, int lane, int h, const uint32_t (&u)[16]) {
+__device__ __forceinline__ void write_box(uint32_t buf, int lane, int h, bool narrow, const uint32_t (&u)[16]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        st_shared_v4(piece_addr<W>(buf, lane, 4 * h + j), make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]));
+        st_shared_v4(piece_addr(buf, lane, 4 * h + j, narrow),
+                     make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]));
 }
 
 // The same of the first `left` columns of a row in global memory.
@@ -362,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (tma) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                const uint32_t to = piece_addr<64>(buf, lane, j);
+                                const uint32_t to = piece_addr(buf, lane, j);
                                 const uint4 u = p.has_r ? ld_shared_v4(to) : make_uint4(0u, 0u, 0u, 0u);
                                 st_shared_v4(to, make_uint4(__float_as_uint(kept[i][4 * j] + __uint_as_float(u.x)),
                                                             __float_as_uint(kept[i][4 * j + 1] + __uint_as_float(u.y)),
@@ -386,26 +385,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             } else {
-                auto do_box = [&](int box, auto w) {
-                    constexpr int W = decltype(w)::value;
+                if (half >= within) release(acc);
+#pragma unroll 1
+                for (int box = half; box < within; box += 2) {
                     const int n0 = col0 + box * 64;
-                    const bool tma = whole(box);
+                    const bool tma = whole(box), narrow = width(box) == 32;
                     const uint32_t at = count % depth, buf = buf0 + at * BOX;
-                    uint32_t r[W];
-#pragma unroll
-                    for (int h = 0; h < W / 32; ++h)
-                        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(box * 64 + 32 * h),
-                                           *reinterpret_cast<uint32_t(*)[32]>(&r[32 * h]));
                     slot_ready(at, tma);
-                    tmem_ld_wait();
-                    if (box + 2 >= within) release(acc);
-#pragma unroll
-                    for (int h = 0; h < W / 32; ++h) {
+                    // Thirty-two columns at a time, in a loop: unrolled, the four
+                    // activations' code would be read from memory once a tile.
+#pragma unroll 1
+                    for (int h = 0; h < (narrow ? 1 : 2); ++h) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(box * 64 + 32 * h), r);
+                        tmem_ld_wait();
+                        if (box + 2 >= within && (narrow || h == 1)) release(acc);
                         const int n = n0 + 32 * h, left = p.N - n;  // columns within the result, from n
                         const bool mine = row < p.M && left > 0;    // edge boxes: this thread's row is in the result
-                        float v[32];
+                        Pair v[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[32 * h + e]);
+                        for (int e = 0; e < 16; ++e)
+                            v[e] = make_pair2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                         uint32_t u[16];
                         if (EPI == EPI_LINEAR && p.bias && left > 0) {
                             if (vec_bias && left >= 32) {
@@ -422,57 +422,44 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 read_row(static_cast<const uint8_t*>(p.bias) + 2ll * n, left, u);
                             }
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float2 f = unpack16<BF16>(u[e]);
-                                v[2 * e] += f.x;
-                                v[2 * e + 1] += f.y;
-                            }
+                            for (int e = 0; e < 16; ++e) v[e] = add2(v[e], unpack16_pair<BF16>(u[e]));
                         }
                         if (EPI == EPI_LINEAR && p.has_p) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[2 * e], v[2 * e + 1]);
-                            if (tma) write_box<W>(buf + BOX, lane, h, u);
+                            for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[e]);
+                            if (tma) write_box(buf + BOX, lane, h, narrow, u);
                             else if (mine) write_row(element(p.P, n, 2), left, u);
                         }
                         if constexpr (EPI == EPI_LINEAR)
                             with_activation(p.act, [&](auto a) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = activation<decltype(a)::value>(v[e]);
+                                for (int e = 0; e < 16; ++e) v[e] = activation<decltype(a)::value>(v[e]);
                             });
                         if constexpr (EPI == EPI_STEP) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] *= alpha;
+                            for (int e = 0; e < 16; ++e) v[e] = mul2(v[e], pair_of(alpha));
                         }
                         if (p.has_r) {
-                            if (tma) read_box<W>(buf, lane, h, u);
+                            if (tma) read_box(buf, lane, h, narrow, u);
                             else if (mine) read_row(element(p.R, n, 2), left, u);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const float2 f = unpack16<(BF16 && EPI != EPI_STEP)>(u[e]);
-                                if constexpr (EPI == EPI_STEP) {
-                                    v[2 * e] = fmaf(beta, f.x, v[2 * e]);
-                                    v[2 * e + 1] = fmaf(beta, f.y, v[2 * e + 1]);
-                                } else {
-                                    v[2 * e] += f.x;
-                                    v[2 * e + 1] += f.y;
-                                }
+                                const Pair f = unpack16_pair<(BF16 && EPI != EPI_STEP)>(u[e]);
+                                v[e] = EPI == EPI_STEP ? fma2(pair_of(beta), f, v[e]) : add2(v[e], f);
                             }
                         }
                         if constexpr (EPI == EPI_GRAD) {
-                            if (tma) read_box<W>(buf + (p.has_r ? BOX : 0), lane, h, u);
+                            if (tma) read_box(buf + (p.has_r ? BOX : 0), lane, h, narrow, u);
                             else if (mine) read_row(element(p.P, n, 2), left, u);
                             with_activation(p.act, [&](auto a) {
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const float2 f = unpack16<BF16>(u[e]);
-                                    v[2 * e] *= derivative<decltype(a)::value>(f.x);
-                                    v[2 * e + 1] *= derivative<decltype(a)::value>(f.y);
-                                }
+                                for (int e = 0; e < 16; ++e)
+                                    v[e] = mul2(v[e], derivative<decltype(a)::value>(unpack16_pair<BF16>(u[e])));
                             });
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[2 * e], v[2 * e + 1]);
-                        if (tma) write_box<W>(buf, lane, h, u);
+                        for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[e]);
+                        if (tma) write_box(buf, lane, h, narrow, u);
                         else if (mine) write_row(element(p.D, n, 2), left, u);
                         if (EPI == EPI_STEP && mirror) {
                             // Row e of the mirrored box is column n0 + e of this one.
@@ -483,23 +470,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                                               static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1))));
                         }
                     }
-                    if (!tma) return;
+                    if (!tma) continue;
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(W == 32 ? &maps.D32 : &maps.D, buf, n0, row_base, b);
+                        tma_store_3d(narrow ? &maps.D32 : &maps.D, buf, n0, row_base, b);
                         if (EPI == EPI_LINEAR && p.has_p)
-                            tma_store_3d(W == 32 ? &maps.P32 : &maps.P, buf + BOX, n0, row_base, b);
+                            tma_store_3d(narrow ? &maps.P32 : &maps.P, buf + BOX, n0, row_base, b);
                         if (EPI == EPI_STEP && mirror) tma_store_3d(&maps.mirror, buf + BOX, row_base, n0, b);
                         bulk_commit_group();
                     }
                     stored(box);
-                };
-                if (half >= within) release(acc);
-#pragma unroll 1
-                for (int box = half; box < within; box += 2) {
-                    if (width(box) == 64) do_box(box, std::integral_constant<int, 64>{});
-                    else do_box(box, std::integral_constant<int, 32>{});
                 }
             }
         }
@@ -640,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
         }
     }
-    if (warp >= FIRST && lane == 0) bulk_wait_group_all();
+    if (warp >= FIRST && lane == 0) bulk_wait_group_read<0>();  // shared memory may go; the grid's end waits for the rest
     __syncthreads();
     cluster_sync_all();  // no remote arrive or multicast is still pending
     if (warp == 1) {

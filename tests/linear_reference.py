@@ -7,7 +7,7 @@ Unit roundoffs as in quant_reference.py (bf16 2^-8, fp16 2^-11, fp32 2^-24).
   sum of magnitudes a step, K/16 steps; at most 7 partial sums of a cut K and the
   accumulators of a long one join in fp32, 2^-24 each.  sum_rel(K) of (|A||B|)_ij.
   An fp32 dw sums 4096 rows at most in one accumulator, so its steps stop at 256.
-* Activations: exp, the quotient and normcdf are good to 2^-20 of their value
+* Activations: exp, the reciprocal and the normal tail are good to 2^-20 of their value
   where the argument is moderate; an argument v of exp is itself rounded, which
   adds |v| 2^-24, below 2^-17 where the result is not tiny.  ACT_REL = 2^-16 of
   |act(z)|.  |act'| is below 1.13, so an error of z comes through at most 1.13
@@ -28,7 +28,7 @@ from quant_reference import TINY, UNIT, check_rounded, f64  # noqa: F401
 
 ACT_REL = 2.0 ** -16
 DERIVATIVE = 1e-5
-LEAST = 1e-30           # where an activation's tail has run out of fp32's range
+LEAST = 1e-16           # arguments end where the function is within 43 exp(-43) = 9e-18 of its limit
 GELU_C = math.sqrt(2 / math.pi)
 
 
