@@ -20,7 +20,8 @@ __device__ GemmDeviceStatus g_product_few_status;
 
 namespace {
 
-constexpr int THREADS = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr int FIRST = 4;  // first epilogue warp, after the weights' copies, MMA, the rows' copies and none
+constexpr int THREADS = 32 * (FIRST + 4);
 constexpr int kMaxStages = 12;
 constexpr int kTwo = 64;   // widest MT of which two CTAs fit an SM
 constexpr int kPush = 32;  // widest MT with room of its own for the cluster's partials
@@ -54,113 +55,122 @@ struct FewCtl {
     unsigned long long bar[2 * kMaxStages + 1];  // full, empty, done
     uint32_t tmem_base;
     int abort;
-    alignas(16) float bias[128];
+    alignas(16) float bias[128];  // of the tile's columns
 };
 static_assert(sizeof(FewCtl) % 16 == 0, "pushed partials follow");
-
-// What the epilogue of four adjacent outputs reads: asked for ahead of their sums.
-struct QuadInputs {
-    uint4 r;  // fp32, or 16 bits in x and y
-    uint2 p;
-};
 
 __device__ __forceinline__ long long place(const ProductMatrix& m, int b, int row, int n) {
     return static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld + n;
 }
 
-__device__ __forceinline__ uint2 load_quad16(const void* p, long long i, int left) {
+// Eight adjacent 16-bit elements of a row, of which `left` lie in it.
+__device__ __forceinline__ uint4 load_eight(const void* p, long long i, int left) {
     const uint16_t* s = static_cast<const uint16_t*>(p) + i;
-    if (left >= 4) return *reinterpret_cast<const uint2*>(s);
-    const uint32_t x = s[0], y = left > 1 ? s[1] : 0, z = left > 2 ? s[2] : 0;
-    return make_uint2(x | (y << 16), z);
-}
-
-// Columns n.. of row `row`, of which the row has at least one.
-__device__ __forceinline__ QuadInputs fetch_quad(const FewParams& p, int b, int row, int n) {
-    QuadInputs in = {};
-    const int left = p.N - n;
-    if (left <= 0) return in;
-    if (p.R.p) {
-        const long long i = place(p.R, b, row, n);
-        if (p.epi != EPI_F32) {
-            const uint2 u = load_quad16(p.R.p, i, left);
-            in.r.x = u.x;
-            in.r.y = u.y;
-        } else {
-            const uint32_t* s = static_cast<const uint32_t*>(p.R.p) + i;
-            if (left >= 4) in.r = *reinterpret_cast<const uint4*>(s);
-            else in.r = make_uint4(s[0], left > 1 ? s[1] : 0, left > 2 ? s[2] : 0, 0);
-        }
+    if (left >= 8) return *reinterpret_cast<const uint4*>(s);
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = 2 * k < left ? s[2 * k] : 0, hi = 2 * k + 1 < left ? s[2 * k + 1] : 0;
+        u[k] = lo | (hi << 16);
     }
-    if (p.epi == EPI_GRAD) in.p = load_quad16(p.P.p, place(p.P, b, row, n), left);
-    return in;
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__device__ __forceinline__ float4 quad16(bool bf16, uint32_t lo, uint32_t hi) {
-    const float2 a = unpack16(bf16, lo), b = unpack16(bf16, hi);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-__device__ __forceinline__ void store_quad16(bool bf16, const void* p, long long i, int left, float4 v) {
+__device__ __forceinline__ void store_eight(bool bf16, const void* p, long long i, int left, const Pair (&v)[4]) {
     uint16_t* d = static_cast<uint16_t*>(const_cast<void*>(p)) + i;
-    const uint32_t lo = pack16(bf16, v.x, v.y), hi = pack16(bf16, v.z, v.w);
-    if (left >= 4) {
-        *reinterpret_cast<uint2*>(d) = make_uint2(lo, hi);
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = both(v[k]);
+        u[k] = pack16(bf16, f.x, f.y);
+    }
+    if (left >= 8) {
+        *reinterpret_cast<uint4*>(d) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
-        d[0] = static_cast<uint16_t>(lo);
-        if (left > 1) d[1] = static_cast<uint16_t>(lo >> 16);
-        if (left > 2) d[2] = static_cast<uint16_t>(hi);
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+            if (k < left) d[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
     }
 }
 
-// The epilogue of four adjacent sums v of row `row` from column n on.
-__device__ __forceinline__ void finish_quad(const FewParams& p, int b, int row, int n, float4 v,
-                                            const QuadInputs& in, float4 bias, float alpha, float beta) {
+__device__ __forceinline__ void unpack_eight(bool bf16, uint4 u, Pair (&f)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 x = unpack16(bf16, w[k]);
+        f[k] = make_pair2(x.x, x.y);
+    }
+}
+
+// The epilogue of eight adjacent sums v of row `row` from column n on; `bias` is the
+// shared-memory address of the columns'.  Both its callers call it in a loop that
+// is not unrolled: its code is long, runs once a CTA, and eight copies of it took
+// 8 us to be read and run for 64 rows, one takes 2.
+__device__ __forceinline__ void finish_eight(const FewParams& p, int b, int row, int n, Pair (&v)[4], uint32_t bias,
+                                             float alpha, float beta) {
     const int left = p.N - n;
     if (left <= 0) return;
-    const bool bf16 = p.bf16 != 0;
     if (p.epi == EPI_F32) {
-        if (p.R.p)
-            v = make_float4(v.x + __uint_as_float(in.r.x), v.y + __uint_as_float(in.r.y), v.z + __uint_as_float(in.r.z),
-                            v.w + __uint_as_float(in.r.w));
         float* d = static_cast<float*>(const_cast<void*>(p.D.p)) + place(p.D, b, row, n);
-        if (left >= 4) {
-            *reinterpret_cast<float4*>(d) = v;
-        } else {
-            d[0] = v.x;
-            if (left > 1) d[1] = v.y;
-            if (left > 2) d[2] = v.z;
+        const float* r = p.R.p ? static_cast<const float*>(p.R.p) + place(p.R, b, row, n) : nullptr;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 x = both(v[2 * h]), y = both(v[2 * h + 1]);
+            float4 o = make_float4(x.x, x.y, y.x, y.y);
+            if (left >= 4 * h + 4) {
+                if (r) {
+                    const float4 u = *reinterpret_cast<const float4*>(r + 4 * h);
+                    o = make_float4(o.x + u.x, o.y + u.y, o.z + u.z, o.w + u.w);
+                }
+                *reinterpret_cast<float4*>(d + 4 * h) = o;
+            } else {
+                if (left > 4 * h) d[4 * h] = r ? o.x + r[4 * h] : o.x;
+                if (left > 4 * h + 1) d[4 * h + 1] = r ? o.y + r[4 * h + 1] : o.y;
+                if (left > 4 * h + 2) d[4 * h + 2] = r ? o.z + r[4 * h + 2] : o.z;
+            }
         }
         return;
     }
+    const bool bf16 = p.bf16 != 0;
+    // What is read beside the sums, asked for together.
+    uint4 ru = {}, pu = {};
+    if (p.R.p) ru = load_eight(p.R.p, place(p.R, b, row, n), left);
+    if (p.epi == EPI_GRAD) pu = load_eight(p.P.p, place(p.P, b, row, n), left);
+    Pair f[4];
     if (p.epi == EPI_LINEAR) {
-        v = make_float4(v.x + bias.x, v.y + bias.y, v.z + bias.z, v.w + bias.w);
-        if (p.P.p) store_quad16(bf16, p.P.p, place(p.P, b, row, n), left, v);
+        const uint4 lo = ld_shared_v4(bias), hi = ld_shared_v4(bias + 16);
+        v[0] = add2(v[0], make_pair2(__uint_as_float(lo.x), __uint_as_float(lo.y)));
+        v[1] = add2(v[1], make_pair2(__uint_as_float(lo.z), __uint_as_float(lo.w)));
+        v[2] = add2(v[2], make_pair2(__uint_as_float(hi.x), __uint_as_float(hi.y)));
+        v[3] = add2(v[3], make_pair2(__uint_as_float(hi.z), __uint_as_float(hi.w)));
+        if (p.P.p) store_eight(bf16, p.P.p, place(p.P, b, row, n), left, v);
         with_activation(p.act, [&](auto a) {
-            constexpr int ACT = decltype(a)::value;
-            const float2 lo = both(activation<ACT>(make_pair2(v.x, v.y))), hi = both(activation<ACT>(make_pair2(v.z, v.w)));
-            v = make_float4(lo.x, lo.y, hi.x, hi.y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = activation<decltype(a)::value>(v[k]);
         });
     }
-    if (p.epi == EPI_STEP) v = make_float4(alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w);
+    if (p.epi == EPI_STEP) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], pair_of(alpha));
+    }
     if (p.R.p) {
-        const float4 u = quad16(bf16 && p.epi != EPI_STEP, in.r.x, in.r.y);
-        v = make_float4(fmaf(beta, u.x, v.x), fmaf(beta, u.y, v.y), fmaf(beta, u.z, v.z), fmaf(beta, u.w, v.w));
+        unpack_eight(bf16 && p.epi != EPI_STEP, ru, f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = fma2(pair_of(beta), f[k], v[k]);
     }
     if (p.epi == EPI_GRAD) {
-        const float4 u = quad16(bf16, in.p.x, in.p.y);
+        unpack_eight(bf16, pu, f);
         with_activation(p.act, [&](auto a) {
-            constexpr int ACT = decltype(a)::value;
-            const float2 lo = both(derivative<ACT>(make_pair2(u.x, u.y))), hi = both(derivative<ACT>(make_pair2(u.z, u.w)));
-            v = make_float4(v.x * lo.x, v.y * lo.y, v.z * hi.x, v.w * hi.y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], derivative<decltype(a)::value>(f[k]));
         });
     }
-    store_quad16(bf16, p.D.p, place(p.D, b, row, n), left, v);
+    store_eight(bf16, p.D.p, place(p.D, b, row, n), left, v);
 }
 
 // One 128 (columns) x MT (rows) tile, a part of its K blocks.
 template <int MT>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
     product_few_kernel(const __grid_constant__ FewMaps maps, const FewParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -171,8 +181,8 @@ __global__ void __launch_bounds__(THREADS)
     uint8_t* t_ring = smem + S * P_TILE_BYTES;
     FewCtl* ctl = reinterpret_cast<FewCtl*>(t_ring + S * T_BYTES);
     // Partials of a cut K.  PUSH: every CTA writes its share of each output to
-    // the CTA that owns the output, in room of its own; a row's 32 quads (four
-    // outputs) are dealt to the CTAs in runs.  Else they lie over the ring once
+    // the CTA that owns the output, in room of its own; a row's 16 groups of eight
+    // outputs are dealt to the CTAs in runs.  Else they lie over the ring once
     // it is read and are fetched, with a second barrier until they have been.
     constexpr bool PUSH = MT <= kPush;
     float* part = reinterpret_cast<float*>(smem);  // [MT][128]
@@ -218,40 +228,42 @@ __global__ void __launch_bounds__(THREADS)
     griddep_launch_dependents();
     griddep_wait();
 
-    int it = 0;  // thread 0: stages issued
-    if (warp == 0) {
+    int it = 0;  // the copying threads: stages issued
+    if (warp == 0 || warp == 2) {
         if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            for (int kb = k0; kb < k1; ++kb, ++it) {
-                if (!product_wait<false>(empty_bar(s), ph ^ 1u, abort_flag, p.wait_limit_ns, &g_product_few_status,
-                                         P_PRODUCER, it))
-                    break;
-                if (!(it == p.withhold && blockIdx.x == 0)) {
-                    const uint32_t f = smem_addr(f_ring + s * P_TILE_BYTES), t = smem_addr(t_ring + s * T_BYTES);
-                    mbar_arrive_expect_tx(full_bar(s), P_TILE_BYTES + T_BYTES);
-                    if (!p.f_mn) {
-                        tma_load_3d(f, &maps.F, full_bar(s), kb * PK, n0, b);
-                    } else if (n0 < p.f_whole) {
-                        tma_load_4d(f, &maps.F, full_bar(s), n0, kb * PK, 0, b);
-                    } else {
-                        tma_load_3d(f, &maps.F_edge, full_bar(s), n0, kb * PK, b);
-                        tma_load_3d(f + P_CHUNK_BYTES, &maps.F_edge, full_bar(s), n0 + 64, kb * PK, b);
+            const bool weights = warp == 0;
+            const uint32_t ring = smem_addr(weights ? f_ring : t_ring);
+            const uint32_t bytes = weights ? P_TILE_BYTES : T_BYTES;
+            const CUtensorMap* map = weights ? &maps.F : &maps.T;
+            const int r0 = weights ? n0 : m0;
+            auto stages = [&](auto issue) {
+                int s = 0;
+                uint32_t ph = 0;
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    if (!product_wait<false>(empty_bar(s), ph ^ 1u, abort_flag, p.wait_limit_ns, &g_product_few_status,
+                                             P_PRODUCER, it))
+                        break;
+                    if (!(it == p.withhold && blockIdx.x == 0)) {
+                        // One arrive a stage: the rows' bytes may be counted before it.
+                        if (weights) mbar_arrive_expect_tx(full_bar(s), P_TILE_BYTES + T_BYTES);
+                        issue(ring + static_cast<uint32_t>(s) * bytes, full_bar(s), kb * PK);
                     }
-                    if (MT < 64 || !p.t_mn) {
-                        tma_load_3d(t, &maps.T, full_bar(s), kb * PK, m0, b);
-                    } else if (m0 < p.t_whole) {
-                        tma_load_4d(t, &maps.T, full_bar(s), m0, kb * PK, 0, b);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < MT / 64; ++c)
-                            tma_load_3d(t + c * P_CHUNK_BYTES, &maps.T_edge, full_bar(s), m0 + 64 * c, kb * PK, b);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
                     }
                 }
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1u;
-                }
+            };
+            if (!(weights ? p.f_mn : p.t_mn)) {
+                stages([&](uint32_t dst, uint32_t bar, int k) { tma_load_3d(dst, map, bar, k, r0, b); });
+            } else if (r0 < (weights ? p.f_whole : p.t_whole)) {  // the chunks lie within the matrix
+                stages([&](uint32_t dst, uint32_t bar, int k) { tma_load_4d(dst, map, bar, r0, k, 0, b); });
+            } else {
+                const CUtensorMap* edge = weights ? &maps.F_edge : &maps.T_edge;
+                const int n = weights ? 2 : MT / 64;
+                stages([&](uint32_t dst, uint32_t bar, int k) {
+                    for (int c = 0; c < n; ++c) tma_load_3d(dst + c * P_CHUNK_BYTES, edge, bar, r0 + 64 * c, k, b);
+                });
             }
         }
         __syncwarp();
@@ -294,15 +306,27 @@ __global__ void __launch_bounds__(THREADS)
         drain_wait(done_bar, 0u, p.wait_limit_ns);
         tc_fence_after();
         tc_fence_before();
-    } else {
-        const int et = static_cast<int>(threadIdx.x) - 64;  // 0..127
+    } else if (warp >= FIRST) {
+        const int et = static_cast<int>(threadIdx.x) - 32 * FIRST;  // 0..127
         ctl->bias[et] = p.bias && n0 + et < p.N ? load16(p.bf16 != 0, p.bias, n0 + et) : 0.0f;
+        // What this CTA's epilogue will read comes closer meanwhile, a line a thread.
+        if (p.R.p || p.epi == EPI_GRAD) {
+            const int rows = min(MT, p.M - m0);
+            const int own0 = PUSH ? 0 : rows * rank / split, own1 = PUSH ? rows : rows * (rank + 1) / split;
+            const int size = p.epi == EPI_F32 ? 4 : 2, lines = size;  // 128 columns a row
+            for (int i = et; i < (own1 - own0) * lines; i += 128) {
+                const int m = m0 + own0 + i / lines, n = min(n0 + i % lines * (128 / size), p.N - 1);
+                if (p.R.p) prefetch_l1(static_cast<const uint8_t*>(p.R.p) + place(p.R, b, m, n) * size);
+                if (p.epi == EPI_GRAD) prefetch_l1(static_cast<const uint8_t*>(p.P.p) + place(p.P, b, m, n) * size);
+            }
+        }
     }
     __syncthreads();  // the accumulators are complete and the ring is read
     tc_fence_after();
     if (*abort_flag) {
-        // Copies that no MMA waited for land before the ring is reused.
-        if (threadIdx.x == 0)
+        // Copies that no MMA waited for land before the ring is reused.  (A stage
+        // that only one of the two warps issued is waited for until the limit.)
+        if (lane == 0 && (warp == 0 || warp == 2))
             for (int j = it - S > 0 ? it - S : 0; j < it; ++j) {
                 if (j == p.withhold && blockIdx.x == 0) continue;
                 drain_wait(full_bar(j % S), static_cast<uint32_t>((j / S) & 1), p.wait_limit_ns);
@@ -320,34 +344,21 @@ __global__ void __launch_bounds__(THREADS)
     }
     const int accs = (k1 - k0 + p.acc_blocks - 1) / p.acc_blocks;
     const int rows = min(MT, p.M - m0);
-    const int most = (32 + split - 1) / split;  // quads of an owner
-    auto first = [&](int r) { return (32 * r + split - 1) / split; };
+    const int most = (16 + split - 1) / split;  // groups of eight outputs of an owner
+    auto first = [&](int r) { return (16 * r + split - 1) / split; };
+    const uint32_t bias0 = smem_addr(ctl->bias);
     if (PUSH && split > 1) cluster_wait();  // every CTA has started
-    if (warp >= 2) {
+    if (warp >= FIRST) {
         const int q = warp & 3;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         const int n = 32 * q + lane;
-        const int quad = 8 * q + (lane & 7);  // split = 1: this thread's four columns
-        const float4 bias = *reinterpret_cast<const float4*>(ctl->bias + 4 * quad);
-        const int owner = (n >> 2) * split >> 5;
+        const int owner = (n >> 3) * split >> 4;
         const uint32_t push = PUSH && split > 1 ? mapa_shared(recv, static_cast<uint32_t>(owner)) +
-                                                      16u * static_cast<uint32_t>(rank * rows * most + (n >> 2) - first(owner)) +
-                                                      4u * (n & 3)
+                                                      32u * static_cast<uint32_t>(rank * rows * most + (n >> 3) - first(owner)) +
+                                                      4u * (n & 7)
                                                 : 0u;
-        // Uncut: this thread's outputs of 16 rows, rows c + 4 i + lane / 8; what their
-        // epilogue reads is asked for 16 rows ahead.
-        QuadInputs in[4];
-        auto ask = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int m = c + 4 * i + (lane >> 3);
-                if (m < rows) in[i] = fetch_quad(p, b, m0 + m, n0 + 4 * quad);
-            }
-        };
-        if (split == 1) ask(0);
-#pragma unroll 2
-        for (int c = 0; c < MT; c += 16) {
-            if (c >= rows) break;
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 16) {
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
             tmem_ld_wait();
@@ -366,33 +377,29 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (c + i < rows)
-                        st_cluster_f32(push + 16u * static_cast<uint32_t>((c + i) * most), __uint_as_float(r[i]));
+                        st_cluster_f32(push + 32u * static_cast<uint32_t>((c + i) * most), __uint_as_float(r[i]));
             } else if (split > 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) part[(c + i) * 128 + n] = __uint_as_float(r[i]);
             } else {
                 // By way of shared memory, a warp its own, from a column a thread
-                // to four adjacent outputs of four rows a thread.
+                // to eight adjacent outputs of two rows a thread.
                 const uint32_t turn = smem_addr(part) + static_cast<uint32_t>(q * 4096 + (c & 16) * 128);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) st_shared_u32(turn + static_cast<uint32_t>(i * 128 + lane * 4), r[i]);
                 __syncwarp();
-                uint4 v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(turn + static_cast<uint32_t>(i * 512 + lane * 16));
-                QuadInputs had[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) had[i] = in[i];
-                ask(c + 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = c + 4 * i + (lane >> 3);
-                    if (m < rows)
-                        finish_quad(p, b, m0 + m, n0 + 4 * quad,
-                                    make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y),
-                                                __uint_as_float(v[i].z), __uint_as_float(v[i].w)),
-                                    had[i], bias, alpha, beta);
+#pragma unroll 1
+                for (int i = lane >> 2; i < min(16, rows - c); i += 8) {
+                    const uint32_t at = turn + static_cast<uint32_t>(i * 128 + (lane & 3) * 32);
+                    const uint4 lo = ld_shared_v4(at), hi = ld_shared_v4(at + 16);
+                    Pair v[4] = {make_pair2(__uint_as_float(lo.x), __uint_as_float(lo.y)),
+                                 make_pair2(__uint_as_float(lo.z), __uint_as_float(lo.w)),
+                                 make_pair2(__uint_as_float(hi.x), __uint_as_float(hi.y)),
+                                 make_pair2(__uint_as_float(hi.z), __uint_as_float(hi.w))};
+                    const int d = 32 * q + 8 * (lane & 3);
+                    finish_eight(p, b, m0 + c + i, n0 + d, v, bias0 + 4u * d, alpha, beta);
                 }
+                __syncwarp();
             }
         }
         tc_fence_before();
@@ -400,44 +407,27 @@ __global__ void __launch_bounds__(THREADS)
     if (split > 1) {
         __syncwarp();
         cluster_sync_all();
-        // CTA `rank` adds the partials of its outputs in rank order, four
+        // CTA `rank` adds the partials of its outputs in rank order, eight
         // adjacent ones a thread.
-        const int d0 = PUSH ? first(rank) : 0, count = PUSH ? first(rank + 1) - d0 : 32;
-        const int i0 = PUSH ? 0 : rows * 32 * rank / split, i1 = PUSH ? rows * count : rows * 32 * (rank + 1) / split;
+        const int d0 = PUSH ? first(rank) : 0, count = PUSH ? first(rank + 1) - d0 : 16;
+        const int i0 = PUSH ? 0 : rows * rank / split * 16, i1 = PUSH ? rows * count : rows * (rank + 1) / split * 16;
         const uint32_t part_addr = smem_addr(part);
-        // Four quads a thread at a time, so that their loads are under way together.
-        constexpr int Q = 4;
-        for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += Q * THREADS) {
-            QuadInputs in[Q];
-            float4 v[Q];
-            uint32_t at[Q];  // of a partial in its CTA
-#pragma unroll
-            for (int k = 0; k < Q; ++k) {
-                const int j = min(i + k * THREADS, i1 - 1), m = j / count, d = d0 + j % count;
-                in[k] = fetch_quad(p, b, m0 + m, n0 + 4 * d);
-                at[k] = PUSH ? recv + 16u * static_cast<uint32_t>(m * most + d - d0) : part_addr + 16u * j;
-                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-            const uint32_t step = PUSH ? 16u * static_cast<uint32_t>(rows * most) : 0u;
-#pragma unroll 2
+        const uint32_t step = PUSH ? 32u * static_cast<uint32_t>(rows * most) : 0u;
+#pragma unroll 1
+        for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += THREADS) {
+            const int m = i / count, d = d0 + i % count;
+            const uint32_t at = PUSH ? recv + 32u * static_cast<uint32_t>(m * most + d - d0) : part_addr + 32u * i;
+            Pair v[4] = {};
+#pragma unroll 4
             for (int c = 0; c < split; ++c) {
-                float4 u[Q];
-#pragma unroll
-                for (int k = 0; k < Q; ++k)
-                    u[k] = ld_cluster_f4(mapa_shared(at[k] + static_cast<uint32_t>(c) * step,
-                                                     static_cast<uint32_t>(PUSH ? rank : c)));
-#pragma unroll
-                for (int k = 0; k < Q; ++k)
-                    v[k] = c ? make_float4(v[k].x + u[k].x, v[k].y + u[k].y, v[k].z + u[k].z, v[k].w + u[k].w) : u[k];
+                const uint32_t from = mapa_shared(at + static_cast<uint32_t>(c) * step, static_cast<uint32_t>(PUSH ? rank : c));
+                const float4 lo = ld_cluster_f4(from), hi = ld_cluster_f4(from + 16);
+                v[0] = add2(v[0], make_pair2(lo.x, lo.y));
+                v[1] = add2(v[1], make_pair2(lo.z, lo.w));
+                v[2] = add2(v[2], make_pair2(hi.x, hi.y));
+                v[3] = add2(v[3], make_pair2(hi.z, hi.w));
             }
-#pragma unroll
-            for (int k = 0; k < Q; ++k) {
-                const int j = i + k * THREADS;
-                if (j >= i1) break;
-                const int m = j / count, d = d0 + j % count;
-                finish_quad(p, b, m0 + m, n0 + 4 * d, v[k], in[k], *reinterpret_cast<const float4*>(ctl->bias + 4 * d),
-                            alpha, beta);
-            }
+            finish_eight(p, b, m0 + m, n0 + 8 * d, v, bias0 + 32u * d, alpha, beta);
         }
     }
     if (!PUSH && split > 1) cluster_sync_all();  // the peers have read this CTA's partials
@@ -487,8 +477,8 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
     // Two CTAs an SM with half of shared memory each, or a ring as deep as one
     // CTA's room.
     const int budget = (two ? 112 : 226) * 1024;
-    // Room for pushed partials: ceil(32/c) quads of a row from each of c CTAs.
-    const int recv = MT <= kPush && split > 1 ? static_cast<int>(L.M < MT ? L.M : MT) * (32 + split) * 16 : 0;
+    // Room for pushed partials: ceil(16/c) groups of eight of a row from each of c CTAs.
+    const int recv = MT <= kPush && split > 1 ? static_cast<int>(L.M < MT ? L.M : MT) * (16 + split) * 32 : 0;
     const int stages = (budget - 1024 - static_cast<int>(sizeof(FewCtl)) - recv) / STAGE;
     static_assert(4 * STAGE >= MT * 512, "other partials lie over the ring");
     p.stages = stages < kMaxStages ? stages : kMaxStages;
