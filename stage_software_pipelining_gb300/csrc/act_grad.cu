@@ -1,9 +1,9 @@
 // act_grad.cu -- dz = dy act'(z) and the bias gradient, the sum of dz's rows.
 //
-// One pass over dy and z, bound by memory.  A cluster of CTAs owns a strip of
-// columns and shares its rows: every thread adds its rows' unrounded values in
-// fp32, a CTA its threads', and the first CTA of the cluster the others' through
-// distributed shared memory, all in a fixed order and without a workspace.
+// One pass over dy and z, bound by memory.  A CTA, or a cluster of them that
+// shares the rows, owns a strip of columns: every thread adds its rows' unrounded
+// values in fp32, a CTA its threads', and the first CTA of the cluster the others'
+// through distributed shared memory, all in a fixed order and without a workspace.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -17,7 +17,6 @@
 namespace ssp {
 namespace {
 
-constexpr int THREADS = 256;
 
 struct Params {
     int M, N;
@@ -64,9 +63,9 @@ __device__ __forceinline__ Values<VEC> load(const uint16_t* p, int left) {
 
 // Strips of VEC * GROUPS columns; ROWS rows at a time.  VEC = 8 wants rows on
 // 16-byte boundaries.
-template <bool BF16, int VEC, int ACT>
+template <bool BF16, int VEC, int ACT, int GROUPS, int THREADS>
 __device__ __forceinline__ void pass(const Params& p, int r0, int r1, int c, Pair (&sum)[(VEC + 1) / 2]) {
-    constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS;
+    constexpr int ROWS = THREADS / GROUPS;
     constexpr int AHEAD = 4;  // rows of a thread whose loads are under way together
     const int left = p.N - c;
     if (left <= 0) return;
@@ -108,32 +107,43 @@ __device__ __forceinline__ void pass(const Params& p, int r0, int r1, int c, Pai
     }
 }
 
-template <bool BF16, int VEC>
-__global__ void __launch_bounds__(THREADS) act_grad_kernel(const Params p) {
-    constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS, COLS = GROUPS * VEC;
-    __shared__ float sums[ROWS][COLS + 4];
+template <bool BF16, int VEC, int GROUPS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) act_grad_kernel(const Params p) {
+    constexpr int COLS = GROUPS * VEC, WARPS = THREADS / 32;
+    __shared__ float sums[WARPS][COLS];
     __shared__ float total[COLS];
     griddep_launch_dependents();
     griddep_wait();
     const int rank = static_cast<int>(blockIdx.y), parts = static_cast<int>(gridDim.y);  // a cluster is a column of the grid
     const int col0 = static_cast<int>(blockIdx.x) * COLS;
+    const int lane = static_cast<int>(threadIdx.x) & 31;
     const int c = col0 + static_cast<int>(threadIdx.x % GROUPS) * VEC;
-    const int r0 = min(p.M, rank * p.rows), r1 = min(p.M, r0 + p.rows);
+    const int r0 = static_cast<int>(min(static_cast<long long>(p.M), static_cast<long long>(rank) * p.rows));
+    const int r1 = static_cast<int>(min(static_cast<long long>(p.M), static_cast<long long>(r0) + p.rows));
     Pair sum[(VEC + 1) / 2] = {};
     if (p.act == LINEAR_ACT_NONE)
-        pass<BF16, VEC, LINEAR_ACT_NONE>(p, r0, r1, c, sum);
+        pass<BF16, VEC, LINEAR_ACT_NONE, GROUPS, THREADS>(p, r0, r1, c, sum);
     else
-        with_activation(p.act, [&](auto a) { pass<BF16, VEC, decltype(a)::value>(p, r0, r1, c, sum); });
+        with_activation(p.act, [&](auto a) { pass<BF16, VEC, decltype(a)::value, GROUPS, THREADS>(p, r0, r1, c, sum); });
     if (!p.dbias) return;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const float2 s = both(sum[i / 2]);
-        sums[threadIdx.x / GROUPS][(threadIdx.x % GROUPS) * VEC + i] = i & 1 ? s.y : s.x;
+    for (int i = 0; i < (VEC + 1) / 2; ++i) {
+        float2 s = both(sum[i]);
+#pragma unroll
+        for (int d = GROUPS; d < 32; d *= 2) {  // lanes that hold the same columns
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
+        }
+        if (lane < GROUPS) {
+            sums[threadIdx.x / 32][lane * VEC + 2 * i] = s.x;
+            if (VEC > 1) sums[threadIdx.x / 32][(lane * VEC + 2 * i + 1) % COLS] = s.y;
+        }
     }
     __syncthreads();
     if (threadIdx.x < COLS) {
         float s = 0.0f;
-        for (int r = 0; r < ROWS; ++r) s += sums[r][threadIdx.x];
+#pragma unroll 8
+        for (int w = 0; w < WARPS; ++w) s += sums[w][threadIdx.x];
         total[threadIdx.x] = s;
     }
     if (parts > 1) cluster_sync_all();
@@ -148,9 +158,25 @@ __global__ void __launch_bounds__(THREADS) act_grad_kernel(const Params p) {
     if (parts > 1) cluster_sync_all();  // the others' sums have been read
 }
 
-template <bool BF16, int VEC>
+// CTAs that share a strip's rows: as many as have a few each and run at once
+// (fewer CTAs in a second round than in the first leave memory idle).  A sum's are
+// a cluster, of eight at most.
+int parts_of(const ActGradLaunch& L, int cols, int groups, int threads) {
+    const int64_t strips = (L.N + cols - 1) / cols;
+    const int64_t slots = static_cast<int64_t>(tc_current_device_sms()) * (1024 / threads);
+    const int64_t rows = 4 * (threads / groups);
+    int64_t parts = (L.M + rows - 1) / rows;
+    int64_t most = slots / strips;
+    if (L.dbias && most > 8) most = 8;
+    if (most < 1) most = 1;
+    if (parts > most) parts = most;
+    return static_cast<int>(parts < 1 ? 1 : parts);
+}
+
+template <bool BF16, int VEC, int GROUPS, int THREADS>
 int launch(const ActGradLaunch& L, cudaStream_t stream) {
-    constexpr int GROUPS = VEC == 8 ? 8 : 32, ROWS = THREADS / GROUPS, COLS = GROUPS * VEC;
+    constexpr int COLS = VEC * GROUPS;
+    const int parts = parts_of(L, COLS, GROUPS, THREADS);
     Params p = {};
     p.M = static_cast<int>(L.M);
     p.N = static_cast<int>(L.N);
@@ -163,30 +189,26 @@ int launch(const ActGradLaunch& L, cudaStream_t stream) {
     p.lddz = L.lddz;
     p.dbias = L.dbias;
     p.addend = L.addend;
-    // Rows are shared among as many CTAs as have a few each; a sum's are a
-    // cluster of eight at most.
-    const int64_t strips = (L.N + COLS - 1) / COLS;
-    int64_t parts = (L.M + 4 * ROWS - 1) / (4 * ROWS);
-    const int64_t most = L.dbias ? 8 : 65535;
-    if (parts < 1) parts = 1;
-    if (parts > most) parts = most;
     p.rows = static_cast<int>((L.M + parts - 1) / parts);
-    if (p.rows < 1) p.rows = 1;
-    if (!L.dbias) parts = (L.M + p.rows - 1) / p.rows;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = static_cast<unsigned>(parts);
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
-    cfg.blockDim = dim3(THREADS);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = L.dbias && parts > 1 ? 2 : 1;
-    return product_finish(cudaLaunchKernelEx(&cfg, act_grad_kernel<BF16, VEC>, p));
+    const int64_t strips = (L.N + COLS - 1) / COLS;
+    ProductConfig c(strips, parts, THREADS, 0, stream);
+    c.cfg.gridDim = dim3(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
+    c.attr[1].val.clusterDim.x = 1;
+    c.attr[1].val.clusterDim.y = static_cast<unsigned>(parts);
+    if (!L.dbias) c.cfg.numAttrs = 1;  // no cluster
+    return product_finish(cudaLaunchKernelEx(&c.cfg, act_grad_kernel<BF16, VEC, GROUPS, THREADS>, p));
+}
+
+// Strips of 64 columns, 128 bytes a row, and CTAs of 512 threads, two an SM.  Where
+// clusters of eight of them leave places empty (a sum over many rows of few
+// columns), strips of half the width are twice as many.  Where rows are many and the
+// strips fill one CTA an SM better than two, CTAs of 1024 threads.
+template <bool BF16>
+int launch_vectors(const ActGradLaunch& L, cudaStream_t stream) {
+    const int64_t strips = (L.N + 63) / 64, sms = tc_current_device_sms();
+    if (L.dbias && strips * 16 <= 2 * sms && L.M >= 1024) return launch<BF16, 8, 4, 512>(L, stream);
+    if (L.M >= 4096 && 2 * parts_of(L, 64, 8, 1024) > parts_of(L, 64, 8, 512)) return launch<BF16, 8, 8, 1024>(L, stream);
+    return launch<BF16, 8, 8, 512>(L, stream);
 }
 
 }  // namespace
@@ -196,8 +218,8 @@ int act_grad_launch(const ActGradLaunch& L, cudaStream_t stream) {
         return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld % 8 == 0 || L.M <= 1));
     };
     const bool vec = fits(L.dy, L.lddy) && fits(L.pre, L.ldp) && fits(L.dz, L.lddz);
-    if (L.bf16) return vec ? launch<true, 8>(L, stream) : launch<true, 1>(L, stream);
-    return vec ? launch<false, 8>(L, stream) : launch<false, 1>(L, stream);
+    if (L.bf16) return vec ? launch_vectors<true>(L, stream) : launch<true, 1, 32, 512>(L, stream);
+    return vec ? launch_vectors<false>(L, stream) : launch<false, 1, 32, 512>(L, stream);
 }
 
 }  // namespace ssp

@@ -31,16 +31,22 @@ namespace ssp {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int kMostParts = 256;  // CTAs that share a matrix's sum
+constexpr int kMostParts = 1024;  // CTAs that share a matrix's sum
+constexpr int AHEAD = 4;          // groups of eight a thread has under way
 
 struct Params {
     int rows, cols;
     int vecs;  // groups of eight elements a row
+    // Row of group i: i * by >> shift, exact for i < 2^27 (a division otherwise
+    // takes longer than the group).
+    uint32_t by;
+    int shift;
     const void* g;
     long long ldg, stride_g;
     double* parts;  // [batch][gridDim.x]: sums of squares
     int n_parts;
     float eps;
+    int exponent;  // of the first X's norm
     // What the second pass writes: the first X, or (no steps) the output.
     void* out;
     long long ldo, stride_o;
@@ -49,69 +55,103 @@ struct Params {
     float* factor;
 };
 
-// Eight elements of a row from column c on, zeros past its end.
+struct Place {
+    int row, col;
+};
+__device__ __forceinline__ Place place_of(const Params& p, int i) {
+    const int row = static_cast<int>(static_cast<uint64_t>(i) * p.by >> p.shift);
+    return {row, (i - row * p.vecs) * 8};
+}
+
+// Eight elements of a row from column c on, as they lie; zeros past its end.
+struct Raw {
+    uint4 lo, hi;  // hi: fp32 alone
+};
 template <int TYPE>
-__device__ __forceinline__ void load8(const Params& p, int b, int row, int c, float (&v)[8]) {
-    const long long at = static_cast<long long>(b) * p.stride_g + static_cast<long long>(row) * p.ldg + c;
-    const int left = p.cols - c;
+__device__ __forceinline__ Raw load_raw(const Params& p, int b, Place at) {
+    const long long i = static_cast<long long>(b) * p.stride_g + static_cast<long long>(at.row) * p.ldg + at.col;
+    const int left = p.cols - at.col;
+    Raw r = {};
     if constexpr (TYPE == QUANT_F32) {
-        const float* s = static_cast<const float*>(p.g) + at;
+        const uint32_t* s = static_cast<const uint32_t*>(p.g) + i;
         if (left >= 8) {
-            const float4 x = reinterpret_cast<const float4*>(s)[0], y = reinterpret_cast<const float4*>(s)[1];
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+            r.lo = reinterpret_cast<const uint4*>(s)[0];
+            r.hi = reinterpret_cast<const uint4*>(s)[1];
         } else {
+            uint32_t u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < left ? s[i] : 0.0f;
+            for (int e = 0; e < 8; ++e) u[e] = e < left ? s[e] : 0u;
+            r = {make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7])};
         }
     } else {
-        constexpr bool BF16 = TYPE == QUANT_BF16;
-        const uint16_t* s = static_cast<const uint16_t*>(p.g) + at;
+        const uint16_t* s = static_cast<const uint16_t*>(p.g) + i;
         if (left >= 8) {
-            const uint4 u = *reinterpret_cast<const uint4*>(s);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack16<BF16>(w[i]);
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
+            r.lo = *reinterpret_cast<const uint4*>(s);
         } else {
+            uint32_t u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < left ? load16<BF16>(s, i) : 0.0f;
+            for (int e = 0; e < 8; ++e) u[e] = e < left ? s[e] : 0u;
+            r.lo = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+        }
+    }
+    return r;
+}
+template <int TYPE>
+__device__ __forceinline__ void values(const Raw& r, float (&v)[8]) {
+    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+    if constexpr (TYPE == QUANT_F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16<TYPE == QUANT_BF16>(w[e]);
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
         }
     }
 }
 
-// The sum of v over the CTA's threads, in a fixed order, for every thread.
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double warps[THREADS / 32];
+// f(place, values) for this thread's share of matrix b's groups of eight.
+template <int TYPE, class F>
+__device__ __forceinline__ void each_group(const Params& p, int b, F&& f) {
+    const int n = p.rows * p.vecs, stride = static_cast<int>(gridDim.x) * THREADS;
+    for (int i = static_cast<int>(blockIdx.x) * THREADS + static_cast<int>(threadIdx.x); i < n; i += AHEAD * stride) {
+        Place at[AHEAD];
+        Raw raw[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i + k * stride < n) {
+                at[k] = place_of(p, i + k * stride);
+                raw[k] = load_raw<TYPE>(p, b, at[k]);
+            }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i + k * stride < n) {
+                float v[8];
+                values<TYPE>(raw[k], v);
+                f(at[k], v);
+            }
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) s += warps[w];
-    return s;
+    return v;
 }
 
 // Sums of squares.  Sums of squares of elements beyond 2^45 or below 2^-45 may
 // leave fp32's range: a group of eight whose largest is such is scaled by 2^-80
-// or 2^100 and summed apart.  (Beside a larger element of its group, a square
+// or 2^90 and summed apart.  (Beside a larger element of its group, a square
 // that underflows is too small to count.)
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
     griddep_launch_dependents();
     griddep_wait();
     const int b = static_cast<int>(blockIdx.y);
-    const long long n = static_cast<long long>(p.rows) * p.vecs;
     float sum = 0.0f, large = 0.0f, small = 0.0f;
-    for (long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; i < n;
-         i += static_cast<long long>(gridDim.x) * THREADS) {
-        const int row = static_cast<int>(i / p.vecs);
-        float v[8];
-        load8<TYPE>(p, b, row, static_cast<int>(i - static_cast<long long>(row) * p.vecs) * 8, v);
+    each_group<TYPE>(p, b, [&](Place, const float(&v)[8]) {
         float most = 0.0f, s = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -121,62 +161,77 @@ __global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
         if (most <= 0x1p45f && (most >= 0x1p-45f || most == 0.0f)) {
             sum += s;  // a NaN among the eight is in s
         } else {
-            const float by = most > 1.0f ? 0x1p-80f : 0x1p100f;
+            const float by = most > 1.0f ? 0x1p-80f : 0x1p90f;
             s = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s = fmaf(v[e] * by, v[e] * by, s);
             if (most > 1.0f) large += s;
             else small += s;
         }
+    });
+    // 64-bit arithmetic is slow here: one thread a warp, then one a CTA.
+    __shared__ double warps[THREADS / 32];
+    sum = warp_sum(sum);
+    large = warp_sum(large);
+    small = warp_sum(small);
+    if ((threadIdx.x & 31) == 0)
+        warps[threadIdx.x >> 5] = static_cast<double>(sum) + static_cast<double>(large) * 0x1p160 +
+                                  static_cast<double>(small) * 0x1p-180;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int w = 0; w < THREADS / 32; ++w) s += warps[w];
+        p.parts[static_cast<long long>(b) * gridDim.x + blockIdx.x] = s;
     }
-    const double s = block_sum(static_cast<double>(sum) + static_cast<double>(large) * 0x1p160 +
-                               static_cast<double>(small) * 0x1p-200);
-    if (threadIdx.x == 0) p.parts[static_cast<long long>(b) * gridDim.x + blockIdx.x] = s;
 }
 
-// X = G 2^e with a root mean square of about one, and t = 2^-e / (|G| + eps).
-// The largest element is at most 2^15 then.
+// X = G 2^e with a root mean square of about one, or a norm of 2^14 where that is
+// less, and t = 2^-e / (|G| + eps).  The largest element is at most 2^15 then.
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS) ortho_first_kernel(const Params p) {
     griddep_launch_dependents();
     griddep_wait();
     const int b = static_cast<int>(blockIdx.y);
-    double v = 0.0;
-    if (static_cast<int>(threadIdx.x) < p.n_parts) v = p.parts[static_cast<long long>(b) * p.n_parts + threadIdx.x];
-    const double norm = sqrt(block_sum(v));
-    int e = 0;
-    if (norm > 0.0 && norm < 1e300) {
-        double target = sqrt(static_cast<double>(p.rows) * p.cols);
-        if (target > 16384.0) target = 16384.0;
-        e = ilogb(target) - ilogb(norm);
+    __shared__ float factors[3];  // 2^e in two, since it may lie beyond fp32's exponents, and t
+    if (threadIdx.x < 32) {
+        double v = 0.0;
+        for (int i = static_cast<int>(threadIdx.x); i < p.n_parts; i += 32)
+            v += p.parts[static_cast<long long>(b) * p.n_parts + i];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(v);
+            int e = 0;
+            if (norm > 0.0 && norm < 1e300) e = p.exponent - ilogb(norm);
+            // Not finite: NaN everywhere.  No elements but zeros: zeros, or 0 / 0.
+            float t = nanf("");
+            if (norm < 1e300)
+                t = norm == 0.0 && p.eps > 0.0f ? 1.0f
+                                                : static_cast<float>(ldexp(1.0, -e) / (norm + static_cast<double>(p.eps)));
+            factors[0] = ldexpf(1.0f, e / 2);
+            factors[1] = ldexpf(1.0f, e - e / 2);
+            factors[2] = t;
+            if (blockIdx.x == 0) p.factor[b] = t;
+        }
     }
-    // Not finite: NaN everywhere.  No elements but zeros: zeros, or 0 / 0.
-    float t = nanf("");
-    if (norm < 1e300)
-        t = norm == 0.0 && p.eps > 0.0f ? 1.0f : static_cast<float>(ldexp(1.0, -e) / (norm + static_cast<double>(p.eps)));
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.factor[b] = t;
-    // 2^e may lie beyond fp32's exponents: two factors.
-    const float by0 = ldexpf(1.0f, e / 2), by1 = ldexpf(1.0f, e - e / 2);
-    const float after = p.last ? t * p.scale : 1.0f;
-    const long long n = static_cast<long long>(p.rows) * p.vecs;
-    for (long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x; i < n;
-         i += static_cast<long long>(gridDim.x) * THREADS) {
-        const int row = static_cast<int>(i / p.vecs);
-        const int c = static_cast<int>(i - static_cast<long long>(row) * p.vecs) * 8;
-        float x[8];
-        load8<TYPE>(p, b, row, c, x);
+    __syncthreads();
+    const float by0 = factors[0], by1 = factors[1], after = p.last ? factors[2] * p.scale : 1.0f;
+    each_group<TYPE>(p, b, [&](Place at, const float(&x)[8]) {
+        const int c = at.col;
         uint32_t u[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             u[k] = pack16(p.out_bf16 != 0, x[2 * k] * by0 * by1 * after, x[2 * k + 1] * by0 * by1 * after);
         uint16_t* d = static_cast<uint16_t*>(p.out) + static_cast<long long>(b) * p.stride_o +
-                      static_cast<long long>(row) * p.ldo + c;
+                      static_cast<long long>(at.row) * p.ldo + c;
         if (p.cols - c >= 8 || !p.last) {  // the first X's rows are padded to whole groups
             *reinterpret_cast<uint4*>(d) = make_uint4(u[0], u[1], u[2], u[3]);
         } else {
-            for (int k = 0; k < p.cols - c; ++k) d[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (k < p.cols - c) d[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
         }
-    }
+    });
 }
 
 template <int TYPE>
@@ -229,10 +284,18 @@ int ortho_launch(const OrthoLaunch& L, cudaStream_t stream) {
     p.ldg = L.ldg;
     p.stride_g = L.stride_g;
     p.parts = reinterpret_cast<double*>(ws + at.parts);
-    const int64_t groups = (static_cast<int64_t>(p.rows) * p.vecs + THREADS - 1) / THREADS;
-    const int64_t share = (groups + 3) / 4;  // four groups a thread before all CTAs take part
-    p.n_parts = static_cast<int>(share < kMostParts ? share : kMostParts);
+    int bits = 0;
+    while ((1 << bits) < p.vecs) ++bits;
+    p.shift = 27 + bits;
+    p.by = static_cast<uint32_t>(((uint64_t{1} << p.shift) + p.vecs - 1) / p.vecs);
+    // AHEAD groups a thread before another CTA takes part, eight CTAs an SM at most.
+    const int64_t groups = static_cast<int64_t>(p.rows) * p.vecs;
+    const int64_t share = (groups + AHEAD * THREADS - 1) / (AHEAD * THREADS);
+    const int64_t most = (kMostParts + L.batch - 1) / L.batch;
+    p.n_parts = static_cast<int>(share < most ? share : most);
     p.eps = L.eps;
+    const int target = std::ilogb(std::sqrt(static_cast<double>(L.rows) * L.cols));
+    p.exponent = target < 14 ? target : 14;
     p.scale = L.scale;
     p.factor = reinterpret_cast<float*>(ws + at.factor);
     p.last = L.steps == 0;

@@ -544,15 +544,19 @@ bool choose(const ProductLaunch& L, Choice* best) {
     const int64_t tm = up(L.M, 256);
     const int64_t units = product_resident_pairs();
     if (units <= 0) return false;
+    // Bytes, at the rate that memory was measured to give, bound every choice alike
+    // but for what lies beside them.
+    const double bytes = 2.0 * L.batch * (static_cast<double>(L.M + L.N) * L.K + static_cast<double>(L.M) * L.N);
     double least = 1e30;
     // Microseconds of a K block by the tile's width: 256, 224, 192.  (An MN-major B's
     // narrower tiles do not start on whole 128-byte lines.)
-    const double kBlock[3] = {0.2925, L.b_mn ? 0.294 : 0.273, L.b_mn ? 0.27 : 0.244};
+    const double kBlock[3] = {0.286, L.b_mn ? 0.298 : 0.24, L.b_mn ? 0.286 : 0.215};
     for (int w = 0; w < (L.symmetric ? 1 : 3); ++w) {
         const int bn = 256 - 32 * w;
         const int64_t tn = up(L.N, bn);
         const int64_t pairs = (L.symmetric ? tm * (tm + 1) / 2 : tm * tn) * L.batch;
-        const double us = 5.3 + static_cast<double>(up(pairs, units)) * (kBlock[w] * kb + 0.55);
+        double us = 6.4 + static_cast<double>(up(pairs, units)) * (kBlock[w] * kb + 0.48);
+        us = 0.05 * us + (us < 3.0 + bytes / 5.2e6 ? 3.0 + bytes / 5.2e6 : us);
         if (us < least) {
             least = us;
             best->bn = bn;
@@ -570,10 +574,12 @@ bool choose(const ProductLaunch& L, Choice* best) {
             for (int t = 0; t <= (mt <= kTwo && accs * mt <= 256 ? 1 : 0); ++t) {
                 const double rounds = static_cast<double>(up(ctas, resident[c] * (1 + t)));
                 const bool alone = ctas <= resident[c];  // one CTA an SM at most
-                const double block = (t && alone ? 0.29 : 0.163) + 0.0009 * mt;
-                const double us = (t ? 0.74 : 1.93) +
-                                  rounds * (t && !alone ? 2.0 : 1.0) * (up(kb, c) * block + 0.69 + 0.012 * mt) +
-                                  (c > 1 ? 1.17 + 0.0023 * mt + 0.08 * (rounds - 1.0) * c : 0.0);
+                const int64_t rows = mt < L.M ? mt : L.M;
+                double us = (t ? -0.6 : -0.5) +
+                            rounds * (t && !alone ? 1.22 : 1.0) *
+                                (up(kb, c) * ((t && alone ? 0.236 : 0.205) + 0.00056 * mt) + 3.48 + 0.0354 * rows) +
+                            (c > 1 ? 0.00098 * rows + 0.26 * c : 0.0);
+                us = 0.05 * us + (us < 3.0 + bytes / 5.4e6 ? 3.0 + bytes / 5.4e6 : us);
                 if (us < least) {
                     least = us;
                     best->mt = mt;

@@ -15,9 +15,9 @@ Unit roundoffs as in quant_reference.py (bf16 2^-8, fp16 2^-11, fp32 2^-24).
 * Derivatives are sums of terms of at most about one (p, f p (1-p), f phi), each
   good to 2^-19: DERIVATIVE = 1e-5, absolute.  Their second derivatives are not
   needed: z comes rounded, and is taken as given.
-* dbias: a thread adds at most M/64 + 1 rows (M over eight CTAs and eight row
-  lanes, of the kernel for unaligned rows), then 32 threads and 8 CTAs:
-  (M/64 + 42) 2^-24 of the sum of magnitudes, and DERIVATIVE of that of |dy|.
+* dbias: a thread adds at most M/16 + 1 rows (sixteen row lanes, of the kernel for
+  unaligned rows), then two lanes' steps, 32 warps and 8 CTAs follow:
+  (M/16 + 48) 2^-24 of the sum of magnitudes, and DERIVATIVE of that of |dy|.
 """
 import math
 
@@ -103,7 +103,7 @@ def check_act_grad(dz, dbias, dy, pre, name, addend=None, what="act_grad"):
         c = f64(addend) if addend is not None else 0.0
         ref = (g * d).sum(0) + c
         mag = np.abs(g * d).sum(0)
-        bound = ((dy.shape[0] / 64 + 42) * 2.0 ** -24 * mag + off * np.abs(g).sum(0)
+        bound = ((dy.shape[0] / 16 + 48) * 2.0 ** -24 * mag + off * np.abs(g).sum(0)
                  + 2.0 ** -23 * (np.abs(ref) + np.abs(c)) + TINY[torch.float32])
         bad = ~(np.abs(f64(dbias) - ref) <= bound)
         assert not bad.any(), f"{what}: dbias at {np.argwhere(bad)[0]}: {f64(dbias)[bad][0]} for {ref[bad][0]}"
