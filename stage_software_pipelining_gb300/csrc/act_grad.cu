@@ -200,13 +200,13 @@ int launch(const ActGradLaunch& L, cudaStream_t stream) {
 }
 
 // Strips of 64 columns, 128 bytes a row, and CTAs of 512 threads, two an SM.  Where
-// clusters of eight of them leave places empty (a sum over many rows of few
-// columns), strips of half the width are twice as many.  Where rows are many and the
-// strips fill one CTA an SM better than two, CTAs of 1024 threads.
+// clusters of eight of them leave many places empty (a sum over many rows of few
+// columns), strips of 32 columns: 32768 x 1024 in strips of 64 69 us, of 32 39.  Where rows are many and the strips fill one CTA an SM better than two, CTAs
+// of 1024 threads.
 template <bool BF16>
 int launch_vectors(const ActGradLaunch& L, cudaStream_t stream) {
-    const int64_t strips = (L.N + 63) / 64, sms = tc_current_device_sms();
-    if (L.dbias && strips * 16 <= 2 * sms && L.M >= 1024) return launch<BF16, 8, 4, 512>(L, stream);
+    const int64_t sms = tc_current_device_sms();
+    if (L.dbias && L.M >= 1024 && (L.N + 63) / 64 * 8 <= sms) return launch<BF16, 8, 4, 512>(L, stream);
     if (L.M >= 4096 && 2 * parts_of(L, 64, 8, 1024) > parts_of(L, 64, 8, 512)) return launch<BF16, 8, 8, 1024>(L, stream);
     return launch<BF16, 8, 8, 512>(L, stream);
 }

@@ -61,13 +61,12 @@ struct PairParams {
     int act;
     int has_r, has_p;
     int symmetric;
-    int clip;      // tensor stores may write the last 16 bytes of a row
+    int n_copied;  // columns that leave by tensor stores, which clip in units of 16 bytes
     float alpha, beta;
     const float* factor;
     int alpha_pow, beta_pow;
     const void* bias;
-    // For boxes across the right edge, which each thread reads and writes itself.
-    ProductMatrix D, R, P;
+    ProductMatrix D, P;  // for the last columns, which each thread writes itself
     unsigned long long wait_limit_ns;
     int withhold;
 };
@@ -127,22 +126,13 @@ __device__ __forceinline__ void write_box(uint32_t buf, int lane, int h, bool na
                      make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]));
 }
 
-// The same of the first `left` columns of a row in global memory.
-__device__ __forceinline__ void read_row(const uint8_t* p, int left, uint32_t (&u)[16]) {
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+// Those of thirty-two columns from n on that no tensor store writes: columns
+// [n_copied, N) of this thread's row d, seven at most.
+__device__ __forceinline__ void write_last(const PairParams& p, uint8_t* d, int n, const uint32_t (&u)[16]) {
+    uint16_t* to = reinterpret_cast<uint16_t*>(d);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const uint32_t lo = 2 * i < left ? s[2 * i] : 0, hi = 2 * i + 1 < left ? s[2 * i + 1] : 0;
-        u[i] = lo | (hi << 16);
-    }
-}
-__device__ __forceinline__ void write_row(uint8_t* p, int left, const uint32_t (&u)[16]) {
-    uint16_t* d = reinterpret_cast<uint16_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if (2 * i < left) d[2 * i] = static_cast<uint16_t>(u[i]);
-        if (2 * i + 1 < left) d[2 * i + 1] = static_cast<uint16_t>(u[i] >> 16);
-    }
+    for (int e = 0; e < 32; ++e)
+        if (n + e >= p.n_copied && n + e < p.N) to[n + e] = static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1)));
 }
 
 // A cluster of two CTAs computes a 256 x bn tile.  CTA rank r stages rows 128r..
@@ -240,10 +230,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             // Boxes half, half + 2, ... of the tile that lie within the result.
             const int within = row_base < p.M ? min(boxes, (p.N - col0 + COLS - 1) / COLS) : 0;
             auto width = [&](int box) { return min(COLS, p.bn - box * COLS); };
-            // Tensor stores clip rows past M, and columns past N in units of 16
-            // bytes: a box with part of such a unit is read and written by each
-            // thread for its row.
-            auto whole = [&](int box) { return p.clip || col0 + box * COLS + width(box) <= p.N; };
             auto fetch = [&](int box, uint32_t at) {  // lane 0: a box's inputs
                 const uint32_t bar = in_bar0 + 8u * at, buf = buf0 + at * BOX;
                 const int n = col0 + box * COLS;
@@ -258,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) bulk_wait_group_read<0>();  // the last tile's stores have read their boxes
                 for (int d = 0; d < depth; ++d) {
                     const int box = half + 2 * d;
-                    if (box >= within || !whole(box)) break;
+                    if (box >= within) break;
                     const uint32_t at = (count + d) % depth;
                     if (lane == 0) fetch(box, at);
                     in_pending |= 1u << at;
@@ -316,29 +302,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) break;
             // Before a box's slot is written: its inputs are there, or the store
             // that last used it has read it.
-            auto slot_ready = [&](uint32_t at, bool tma) {
-                if (inputs && tma) {
+            auto slot_ready = [&](uint32_t at) {
+                if (inputs) {
                     if (product_wait<true>(in_bar0 + 8u * at, (in_phase >> at) & 1u, abort_flag, p.wait_limit_ns,
                                            &g_product_pair_status, P_EPILOGUE, lt)) {
                         in_phase ^= 1u << at;
                         in_pending &= ~(1u << at);
                     }
                 }
-                if (!inputs && lane == 0) {
+                if (!inputs && lane == 0 && count >= static_cast<uint32_t>(depth)) {
                     if (depth == 2) bulk_wait_group_read<1>();
                     else bulk_wait_group_read<0>();
                 }
                 __syncwarp();
             };
-            auto element = [&](const ProductMatrix& m, int n, int size) -> uint8_t* {
+            auto row_of = [&](const ProductMatrix& m, int size) -> uint8_t* {
                 return const_cast<uint8_t*>(static_cast<const uint8_t*>(m.p)) +
-                       (static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld + n) * size;
+                       (static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld) * size;
             };
             // After a box's store: the slot after this one takes the inputs of this
             // warp's next box, where they are not on their way.
             auto stored = [&](int box) {
                 const int next = box + 2;
-                if (inputs && (depth == 1 || box >= 2) && next < within && whole(next) && !*abort_flag) {
+                if (inputs && (depth == 1 || box >= 2) && next < within && !*abort_flag) {
                     const uint32_t to = (count + 1) % depth;
                     if (lane == 0) {
                         if (depth == 2) bulk_wait_group_read<1>();
@@ -354,34 +340,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 4; ++i) {
                     const int box = half + 2 * i;
                     if (box < within) {
-                        const int n0 = col0 + box * 32, left = p.N - n0;
-                        const bool tma = whole(box);
+                        const int n0 = col0 + box * 32;
                         const uint32_t at = count % depth, buf = buf0 + at * BOX;
-                        slot_ready(at, tma);
-                        if (tma) {
+                        slot_ready(at);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint32_t to = piece_addr(buf, lane, j);
-                                const uint4 u = p.has_r ? ld_shared_v4(to) : make_uint4(0u, 0u, 0u, 0u);
-                                st_shared_v4(to, make_uint4(__float_as_uint(kept[i][4 * j] + __uint_as_float(u.x)),
-                                                            __float_as_uint(kept[i][4 * j + 1] + __uint_as_float(u.y)),
-                                                            __float_as_uint(kept[i][4 * j + 2] + __uint_as_float(u.z)),
-                                                            __float_as_uint(kept[i][4 * j + 3] + __uint_as_float(u.w))));
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t to = piece_addr(buf, lane, j);
+                            if (p.has_r) {
+                                const uint4 u = ld_shared_v4(to);
+                                kept[i][4 * j] += __uint_as_float(u.x);
+                                kept[i][4 * j + 1] += __uint_as_float(u.y);
+                                kept[i][4 * j + 2] += __uint_as_float(u.z);
+                                kept[i][4 * j + 3] += __uint_as_float(u.w);
                             }
-                            fence_proxy_async_shared();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tma_store_3d(&maps.D, buf, n0, row_base, b);
-                                bulk_commit_group();
-                            }
-                            stored(box);
-                        } else if (row < p.M) {
-                            const float* s = reinterpret_cast<const float*>(element(p.R, n0, 4));
-                            float* d = reinterpret_cast<float*>(element(p.D, n0, 4));
+                            st_shared_v4(to, make_uint4(__float_as_uint(kept[i][4 * j]), __float_as_uint(kept[i][4 * j + 1]),
+                                                        __float_as_uint(kept[i][4 * j + 2]),
+                                                        __float_as_uint(kept[i][4 * j + 3])));
+                        }
+                        if (n0 + 32 > p.n_copied && row < p.M) {
+                            float* d = reinterpret_cast<float*>(row_of(p.D, 4));
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (e < left) d[e] = p.has_r ? kept[i][e] + s[e] : kept[i][e];
+                                if (n0 + e >= p.n_copied && n0 + e < p.N) d[n0 + e] = kept[i][e];
                         }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (n0 < p.n_copied) tma_store_3d(&maps.D, buf, n0, row_base, b);
+                            bulk_commit_group();
+                        }
+                        stored(box);
                     }
                 }
             } else {
@@ -389,9 +377,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
                 for (int box = half; box < within; box += 2) {
                     const int n0 = col0 + box * 64;
-                    const bool tma = whole(box), narrow = width(box) == 32;
+                    const bool narrow = width(box) == 32;
                     const uint32_t at = count % depth, buf = buf0 + at * BOX;
-                    slot_ready(at, tma);
+                    slot_ready(at);
                     // Thirty-two columns at a time, in a loop: unrolled, the four
                     // activations' code would be read from memory once a tile.
 #pragma unroll 1
@@ -401,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld_wait();
                         if (box + 2 >= within && (narrow || h == 1)) release(acc);
                         const int n = n0 + 32 * h, left = p.N - n;  // columns within the result, from n
-                        const bool mine = row < p.M && left > 0;    // edge boxes: this thread's row is in the result
+                        const bool last = n + 32 > p.n_copied && row < p.M && left > 0;
                         Pair v[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
@@ -419,7 +407,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     u[4 * j + 3] = x.w;
                                 }
                             } else {
-                                read_row(static_cast<const uint8_t*>(p.bias) + 2ll * n, left, u);
+                                const uint16_t* s = static_cast<const uint16_t*>(p.bias) + n;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    u[e] = (2 * e < left ? s[2 * e] : 0u) |
+                                           (2 * e + 1 < left ? static_cast<uint32_t>(s[2 * e + 1]) << 16 : 0u);
                             }
 #pragma unroll
                             for (int e = 0; e < 16; ++e) v[e] = add2(v[e], unpack16_pair<BF16>(u[e]));
@@ -427,8 +419,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (EPI == EPI_LINEAR && p.has_p) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[e]);
-                            if (tma) write_box(buf + BOX, lane, h, narrow, u);
-                            else if (mine) write_row(element(p.P, n, 2), left, u);
+                            write_box(buf + BOX, lane, h, narrow, u);
+                            if (last) write_last(p, row_of(p.P, 2), n, u);
                         }
                         if constexpr (EPI == EPI_LINEAR)
                             with_activation(p.act, [&](auto a) {
@@ -440,8 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int e = 0; e < 16; ++e) v[e] = mul2(v[e], pair_of(alpha));
                         }
                         if (p.has_r) {
-                            if (tma) read_box(buf, lane, h, narrow, u);
-                            else if (mine) read_row(element(p.R, n, 2), left, u);
+                            read_box(buf, lane, h, narrow, u);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 const Pair f = unpack16_pair<(BF16 && EPI != EPI_STEP)>(u[e]);
@@ -449,8 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             }
                         }
                         if constexpr (EPI == EPI_GRAD) {
-                            if (tma) read_box(buf + (p.has_r ? BOX : 0), lane, h, narrow, u);
-                            else if (mine) read_row(element(p.P, n, 2), left, u);
+                            read_box(buf + (p.has_r ? BOX : 0), lane, h, narrow, u);
                             with_activation(p.act, [&](auto a) {
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
@@ -459,8 +449,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[e]);
-                        if (tma) write_box(buf, lane, h, narrow, u);
-                        else if (mine) write_row(element(p.D, n, 2), left, u);
+                        write_box(buf, lane, h, narrow, u);
+                        if (last) write_last(p, row_of(p.D, 2), n, u);
                         if (EPI == EPI_STEP && mirror) {
                             // Row e of the mirrored box is column n0 + e of this one.
 #pragma unroll
@@ -470,12 +460,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                                               static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1))));
                         }
                     }
-                    if (!tma) continue;
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(narrow ? &maps.D32 : &maps.D, buf, n0, row_base, b);
-                        if (EPI == EPI_LINEAR && p.has_p)
+                        if (n0 < p.n_copied) tma_store_3d(narrow ? &maps.D32 : &maps.D, buf, n0, row_base, b);
+                        if (EPI == EPI_LINEAR && p.has_p && n0 < p.n_copied)
                             tma_store_3d(narrow ? &maps.P32 : &maps.P, buf + BOX, n0, row_base, b);
                         if (EPI == EPI_STEP && mirror) tma_store_3d(&maps.mirror, buf + BOX, row_base, n0, b);
                         bulk_commit_group();
@@ -702,7 +691,8 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.has_p = L.P.p != nullptr;
     p.symmetric = L.symmetric;
     constexpr int size = EPI == EPI_F32 ? 4 : 2;
-    p.clip = L.padded || L.N % (16 / size) == 0;
+    constexpr int unit = 16 / size;
+    p.n_copied = L.padded ? (p.N + unit - 1) / unit * unit : p.N / unit * unit;
     p.alpha = L.alpha;
     p.beta = L.beta;
     p.factor = L.factor;
@@ -710,7 +700,6 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.beta_pow = L.beta_pow;
     p.bias = L.bias;
     p.D = L.D;
-    p.R = L.R;
     p.P = L.P;
     const DebugHooks d = debug_hooks();
     p.wait_limit_ns = static_cast<unsigned long long>(d.wait_limit_ns);
@@ -727,23 +716,26 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     }
     const CUtensorMapDataType dt = EPI == EPI_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type16(BF16);
     const CUtensorMapDataType rt = EPI == EPI_STEP ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : dt;
-    const int64_t cols = L.padded ? (L.N + 7) / 8 * 8 : L.N;
     PairMaps m = {};
-    auto box = [&](CUtensorMap* map, const ProductMatrix& x, CUtensorMapDataType type, int width, int rows) {
+    // Outputs end at the last whole 16 bytes of a row (a map of no columns, which
+    // nothing uses, has one unit); inputs where the row ends.
+    const int64_t out_cols = p.n_copied > 0 ? p.n_copied : unit;
+    auto box = [&](CUtensorMap* map, const ProductMatrix& x, CUtensorMapDataType type, int64_t cols, int width, int rows) {
         return encode_matrices(map, type, size, width * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                                x, L.M, cols, L.batch, width, rows);
     };
+    const int64_t p_cols = EPI == EPI_LINEAR ? out_cols : L.N;  // z kept, or read
     bool ok = encode_operand(&m.A, &m.A_edge, L.A, L.a_mn, L.bf16, L.M, L.K, L.batch, 128) &&
               encode_operand(&m.B, &m.B_edge, L.B, L.b_mn, L.bf16, L.N, L.K, L.batch, bn / 2) &&
-              box(&m.D, L.D, dt, 128 / size, 32);
-    if (L.R.p) ok = ok && box(&m.R, L.R, rt, 128 / size, 32);
-    if (L.P.p) ok = ok && box(&m.P, L.P, dt, 128 / size, 32);
+              box(&m.D, L.D, dt, out_cols, 128 / size, 32);
+    if (L.R.p) ok = ok && box(&m.R, L.R, rt, L.N, 128 / size, 32);
+    if (L.P.p) ok = ok && box(&m.P, L.P, dt, p_cols, 128 / size, 32);
     if (size == 2 && bn % 64 != 0) {
-        ok = ok && box(&m.D32, L.D, dt, 32, 32);
-        if (L.R.p) ok = ok && box(&m.R32, L.R, rt, 32, 32);
-        if (L.P.p) ok = ok && box(&m.P32, L.P, dt, 32, 32);
+        ok = ok && box(&m.D32, L.D, dt, out_cols, 32, 32);
+        if (L.R.p) ok = ok && box(&m.R32, L.R, rt, L.N, 32, 32);
+        if (L.P.p) ok = ok && box(&m.P32, L.P, dt, p_cols, 32, 32);
     }
-    if (L.symmetric) ok = ok && box(&m.mirror, L.D, dt, 32, 64);
+    if (L.symmetric) ok = ok && box(&m.mirror, L.D, dt, out_cols, 32, 64);
     if (!ok) return GEMM_ERR_LAUNCH;
     ProductConfig c(grid, 2, THREADS, kProductSmem, stream);
     return product_finish(cudaLaunchKernelEx(&c.cfg, kernel, m, p));
