@@ -99,5 +99,9 @@ struct OrthoLaunch {
 };
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols);
 int ortho_launch(const OrthoLaunch& L, cudaStream_t stream);
+// Matrices with a short side, all steps in one launch (orthogonalize_small.cu).
+bool ortho_small_takes(const OrthoLaunch& L);
+int ortho_small_launch(const OrthoLaunch& L, cudaStream_t stream);
+int ortho_small_status(GemmDeviceStatus* out);
 
 }  // namespace ssp

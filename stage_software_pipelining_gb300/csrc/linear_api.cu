@@ -62,12 +62,14 @@ int matrices_ok(std::initializer_list<Given> all, int64_t M, int64_t N, int64_t 
 namespace ssp {
 
 int product_read_and_clear_status(GemmDeviceStatus* out) {
-    GemmDeviceStatus few;
-    int st = product_few_status(&few);
-    if (st != GEMM_OK) return st;
-    st = product_pair_status(out);
-    if (st == GEMM_OK && few.code != 0) *out = few;
-    return st;
+    *out = {0, 0, 0, 0};
+    for (auto read : {product_few_status, product_pair_status, ortho_small_status}) {
+        GemmDeviceStatus one;
+        const int st = read(&one);
+        if (st != GEMM_OK) return st;
+        if (one.code != 0) *out = one;
+    }
+    return GEMM_OK;
 }
 
 }  // namespace ssp

@@ -20,12 +20,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <cmath>
-
 #include "internal.h"
 #include "linear.h"
-#include "product.cuh"
-#include "ptx.cuh"
+#include "ortho.cuh"
 
 namespace ssp {
 namespace {
@@ -41,8 +38,7 @@ struct Params {
     // takes longer than the group).
     uint32_t by;
     int shift;
-    const void* g;
-    long long ldg, stride_g;
+    OrthoInput in;
     double* parts;  // [batch][gridDim.x]: sums of squares
     int n_parts;
     float eps;
@@ -63,55 +59,6 @@ __device__ __forceinline__ Place place_of(const Params& p, int i) {
     return {row, (i - row * p.vecs) * 8};
 }
 
-// Eight elements of a row from column c on, as they lie; zeros past its end.
-struct Raw {
-    uint4 lo, hi;  // hi: fp32 alone
-};
-template <int TYPE>
-__device__ __forceinline__ Raw load_raw(const Params& p, int b, Place at) {
-    const long long i = static_cast<long long>(b) * p.stride_g + static_cast<long long>(at.row) * p.ldg + at.col;
-    const int left = p.cols - at.col;
-    Raw r = {};
-    if constexpr (TYPE == QUANT_F32) {
-        const uint32_t* s = static_cast<const uint32_t*>(p.g) + i;
-        if (left >= 8) {
-            r.lo = reinterpret_cast<const uint4*>(s)[0];
-            r.hi = reinterpret_cast<const uint4*>(s)[1];
-        } else {
-            uint32_t u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = e < left ? s[e] : 0u;
-            r = {make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7])};
-        }
-    } else {
-        const uint16_t* s = static_cast<const uint16_t*>(p.g) + i;
-        if (left >= 8) {
-            r.lo = *reinterpret_cast<const uint4*>(s);
-        } else {
-            uint32_t u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = e < left ? s[e] : 0u;
-            r.lo = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
-        }
-    }
-    return r;
-}
-template <int TYPE>
-__device__ __forceinline__ void values(const Raw& r, float (&v)[8]) {
-    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
-    if constexpr (TYPE == QUANT_F32) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack16<TYPE == QUANT_BF16>(w[e]);
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-        }
-    }
-}
-
 // f(place, values) for this thread's share of matrix b's groups of eight.
 template <int TYPE, class F>
 __device__ __forceinline__ void each_group(const Params& p, int b, F&& f) {
@@ -123,7 +70,7 @@ __device__ __forceinline__ void each_group(const Params& p, int b, F&& f) {
         for (int k = 0; k < AHEAD; ++k)
             if (i + k * stride < n) {
                 at[k] = place_of(p, i + k * stride);
-                raw[k] = load_raw<TYPE>(p, b, at[k]);
+                raw[k] = load_raw<TYPE>(p.in, b, at[k].row, at[k].col, p.cols - at[k].col);
             }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
@@ -135,48 +82,16 @@ __device__ __forceinline__ void each_group(const Params& p, int b, F&& f) {
     }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-
-// Sums of squares.  Sums of squares of elements beyond 2^45 or below 2^-45 may
-// leave fp32's range: a group of eight whose largest is such is scaled by 2^-80
-// or 2^90 and summed apart.  (Beside a larger element of its group, a square
-// that underflows is too small to count.)
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
     griddep_launch_dependents();
     griddep_wait();
     const int b = static_cast<int>(blockIdx.y);
-    float sum = 0.0f, large = 0.0f, small = 0.0f;
-    each_group<TYPE>(p, b, [&](Place, const float(&v)[8]) {
-        float most = 0.0f, s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            most = fmaxf(most, fabsf(v[e]));
-            s = fmaf(v[e], v[e], s);
-        }
-        if (most <= 0x1p45f && (most >= 0x1p-45f || most == 0.0f)) {
-            sum += s;  // a NaN among the eight is in s
-        } else {
-            const float by = most > 1.0f ? 0x1p-80f : 0x1p90f;
-            s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(v[e] * by, v[e] * by, s);
-            if (most > 1.0f) large += s;
-            else small += s;
-        }
-    });
-    // 64-bit arithmetic is slow here: one thread a warp, then one a CTA.
+    SquareSum sq;
+    each_group<TYPE>(p, b, [&](Place, const float(&v)[8]) { sq.add(v); });
     __shared__ double warps[THREADS / 32];
-    sum = warp_sum(sum);
-    large = warp_sum(large);
-    small = warp_sum(small);
-    if ((threadIdx.x & 31) == 0)
-        warps[threadIdx.x >> 5] = static_cast<double>(sum) + static_cast<double>(large) * 0x1p160 +
-                                  static_cast<double>(small) * 0x1p-180;
+    const double mine = sq.warp_total();
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = mine;
     __syncthreads();
     if (threadIdx.x == 0) {
         double s = 0.0;
@@ -185,14 +100,13 @@ __global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
     }
 }
 
-// X = G 2^e with a root mean square of about one, or a norm of 2^14 where that is
-// less, and t = 2^-e / (|G| + eps).  The largest element is at most 2^15 then.
+// The first X, G 2^e, or (no steps) the output.
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS) ortho_first_kernel(const Params p) {
     griddep_launch_dependents();
     griddep_wait();
     const int b = static_cast<int>(blockIdx.y);
-    __shared__ float factors[3];  // 2^e in two, since it may lie beyond fp32's exponents, and t
+    __shared__ float factors[3];
     if (threadIdx.x < 32) {
         double v = 0.0;
         for (int i = static_cast<int>(threadIdx.x); i < p.n_parts; i += 32)
@@ -200,18 +114,8 @@ __global__ void __launch_bounds__(THREADS) ortho_first_kernel(const Params p) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
         if (threadIdx.x == 0) {
-            const double norm = sqrt(v);
-            int e = 0;
-            if (norm > 0.0 && norm < 1e300) e = p.exponent - ilogb(norm);
-            // Not finite: NaN everywhere.  No elements but zeros: zeros, or 0 / 0.
-            float t = nanf("");
-            if (norm < 1e300)
-                t = norm == 0.0 && p.eps > 0.0f ? 1.0f
-                                                : static_cast<float>(ldexp(1.0, -e) / (norm + static_cast<double>(p.eps)));
-            factors[0] = ldexpf(1.0f, e / 2);
-            factors[1] = ldexpf(1.0f, e - e / 2);
-            factors[2] = t;
-            if (blockIdx.x == 0) p.factor[b] = t;
+            first_factors(v, p.exponent, p.eps, factors);
+            if (blockIdx.x == 0) p.factor[b] = factors[2];
         }
     }
     __syncthreads();
@@ -272,6 +176,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols) { return layout(batch, rows, cols).bytes; }
 
 int ortho_launch(const OrthoLaunch& L, cudaStream_t stream) {
+    if (ortho_small_takes(L)) return ortho_small_launch(L, stream);
     const Layout at = layout(L.batch, L.rows, L.cols);
     uint8_t* ws = static_cast<uint8_t*>(L.workspace);
     const bool tall = L.rows > L.cols;
@@ -280,9 +185,7 @@ int ortho_launch(const OrthoLaunch& L, cudaStream_t stream) {
     p.rows = static_cast<int>(L.rows);
     p.cols = static_cast<int>(L.cols);
     p.vecs = static_cast<int>((L.cols + 7) / 8);
-    p.g = L.g;
-    p.ldg = L.ldg;
-    p.stride_g = L.stride_g;
+    p.in = {L.g, L.ldg, L.stride_g};
     p.parts = reinterpret_cast<double*>(ws + at.parts);
     int bits = 0;
     while ((1 << bits) < p.vecs) ++bits;
@@ -294,8 +197,8 @@ int ortho_launch(const OrthoLaunch& L, cudaStream_t stream) {
     const int64_t most = (kMostParts + L.batch - 1) / L.batch;
     p.n_parts = static_cast<int>(share < most ? share : most);
     p.eps = L.eps;
-    const int target = std::ilogb(std::sqrt(static_cast<double>(L.rows) * L.cols));
-    p.exponent = target < 14 ? target : 14;
+    const OrthoScales scales = ortho_scales(L.rows, L.cols);
+    p.exponent = scales.exponent;
     p.scale = L.scale;
     p.factor = reinterpret_cast<float*>(ws + at.factor);
     p.last = L.steps == 0;
@@ -313,11 +216,7 @@ int ortho_launch(const OrthoLaunch& L, cudaStream_t stream) {
     int st = L.dtype == QUANT_F32    ? launch_first<QUANT_F32>(p, L.batch, stream)
              : L.dtype == QUANT_BF16 ? launch_first<QUANT_BF16>(p, L.batch, stream)
                                      : launch_first<QUANT_F16>(p, L.batch, stream);
-    // Scales of A (and b A + c A^2) and of X, powers of two.
-    int la = std::ilogb(static_cast<double>(n));
-    if (la > 14) la = 14;
-    const double sa = std::ldexp(1.0, la);
-    const double sx = std::ldexp(1.0, std::ilogb(std::sqrt(static_cast<double>(m))));
+    const double sa = scales.a, sx = scales.x;
     for (int s = 0; st == GEMM_OK && s < L.steps; ++s) {
         const bool first = s == 0, last = s + 1 == L.steps;
         const ProductMatrix X = {ws + at.x[s & 1], ldx, L.rows * ldx};

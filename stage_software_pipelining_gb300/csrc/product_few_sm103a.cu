@@ -544,19 +544,20 @@ bool choose(const ProductLaunch& L, Choice* best) {
     const int64_t tm = up(L.M, 256);
     const int64_t units = product_resident_pairs();
     if (units <= 0) return false;
-    // Bytes, at the rate that memory was measured to give, bound every choice alike
-    // but for what lies beside them.
-    const double bytes = 2.0 * L.batch * (static_cast<double>(L.M + L.N) * L.K + static_cast<double>(L.M) * L.N);
+    // Memory's rate bounds every choice alike but for what lies beside the bytes.
+    const double bytes = L.batch * (2.0 * static_cast<double>(L.M + L.N) * L.K +
+                                    (L.epi == EPI_F32 ? 4.0 : 2.0) * static_cast<double>(L.M) * L.N);
+    auto bounded = [&](double us, double rate) { return 0.05 * us + (us > 3.0 + bytes / rate ? us : 3.0 + bytes / rate); };
     double least = 1e30;
     // Microseconds of a K block by the tile's width: 256, 224, 192.  (An MN-major B's
     // narrower tiles do not start on whole 128-byte lines.)
-    const double kBlock[3] = {0.286, L.b_mn ? 0.298 : 0.24, L.b_mn ? 0.286 : 0.215};
+    const double kBlock[3] = {0.288, L.b_mn ? 0.285 : 0.262, L.b_mn ? 0.262 : 0.236};
     for (int w = 0; w < (L.symmetric ? 1 : 3); ++w) {
         const int bn = 256 - 32 * w;
         const int64_t tn = up(L.N, bn);
         const int64_t pairs = (L.symmetric ? tm * (tm + 1) / 2 : tm * tn) * L.batch;
-        double us = 6.4 + static_cast<double>(up(pairs, units)) * (kBlock[w] * kb + 0.48);
-        us = 0.05 * us + (us < 3.0 + bytes / 5.2e6 ? 3.0 + bytes / 5.2e6 : us);
+        const double end = 0.9 * bn / 256;
+        const double us = bounded(4.0 + end + static_cast<double>(up(pairs, units)) * (kBlock[w] * kb + end), 5.1e6);
         if (us < least) {
             least = us;
             best->bn = bn;
@@ -575,11 +576,12 @@ bool choose(const ProductLaunch& L, Choice* best) {
                 const double rounds = static_cast<double>(up(ctas, resident[c] * (1 + t)));
                 const bool alone = ctas <= resident[c];  // one CTA an SM at most
                 const int64_t rows = mt < L.M ? mt : L.M;
-                double us = (t ? -0.6 : -0.5) +
-                            rounds * (t && !alone ? 1.22 : 1.0) *
-                                (up(kb, c) * ((t && alone ? 0.236 : 0.205) + 0.00056 * mt) + 3.48 + 0.0354 * rows) +
-                            (c > 1 ? 0.00098 * rows + 0.26 * c : 0.0);
-                us = 0.05 * us + (us < 3.0 + bytes / 5.4e6 ? 3.0 + bytes / 5.4e6 : us);
+                const double us = bounded(
+                    (t ? 0.2 : 0.33) +
+                        rounds * (t && !alone ? 1.25 : 1.0) *
+                            (up(kb, c) * ((t && alone ? 0.225 : 0.199) + 0.00056 * mt) + 2.61 + 0.028 * rows) +
+                        (c > 1 ? 0.28 + 0.0047 * rows + 0.092 * c : 0.0),
+                    5.75e6);
                 if (us < least) {
                     least = us;
                     best->mt = mt;

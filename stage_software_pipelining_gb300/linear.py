@@ -43,6 +43,7 @@ OPS = {"linear": 0, "dx": 1, "dw": 2}
 
 _lock = threading.Lock()
 _lib = None
+_ext = None
 
 
 def load_library():
@@ -70,6 +71,13 @@ def load_library():
         return _lib
 
 
+def _binding():
+    """The extension that marshals tensors into libgemm.so.  Raises if it is missing."""
+    global _ext
+    _ext = Q.load_binding()
+    return _ext
+
+
 def _act(name: str) -> int:
     try:
         return ACTIVATIONS[name]
@@ -84,7 +92,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor, *, bias: torch.Ten
 
     x: M x K; W: N x K; y, residual, pre: M x N; bias: N; all fp16 or all
     bf16.  act: one of ACTIVATIONS.  residual may be y itself.  Returns y."""
-    st = Q.load_binding().linear(x, W, y, bias, residual, _act(act), pre, stream, checked)
+    st = (_ext or _binding()).linear(x, W, y, bias, residual, _act(act), pre, stream, checked)
     if st:
         raise GemmError(st, "linear")
     return y
@@ -97,7 +105,7 @@ def act_grad(dy: torch.Tensor, dz: torch.Tensor | None = None, *, pre: torch.Ten
 
     dy, pre, dz: M x N of one 16-bit type; dbias, addend: N fp32.  dz or dbias may
     be None (not computed); dz may be dy or pre itself, addend dbias itself."""
-    st = Q.load_binding().act_grad(dy, dz, pre, _act(act), dbias, addend, stream)
+    st = (_ext or _binding()).act_grad(dy, dz, pre, _act(act), dbias, addend, stream)
     if st:
         raise GemmError(st, "act_grad")
 
@@ -112,7 +120,7 @@ def linear_dx(dz: torch.Tensor, W: torch.Tensor, dx: torch.Tensor, *,
     dz: M x N; W: N x K; dx, residual, pre: M x K; all fp16 or all bf16.  pre
     and an act other than "none" go together.  dx may be residual or pre itself.
     Returns dx."""
-    st = Q.load_binding().linear_dx(dz, W, dx, residual, _act(act), pre, stream, checked)
+    st = (_ext or _binding()).linear_dx(dz, W, dx, residual, _act(act), pre, stream, checked)
     if st:
         raise GemmError(st, "linear_dx")
     return dx
@@ -125,7 +133,7 @@ def linear_dw(dz: torch.Tensor, x: torch.Tensor, dw: torch.Tensor, *,
 
     dz: M x N; x: M x K; both fp16 or both bf16; dw, addend: N x K, fp32 or dz's
     type.  addend may be dw itself (micro-batches).  Returns dw."""
-    st = Q.load_binding().linear_dw(dz, x, dw, addend, stream, checked)
+    st = (_ext or _binding()).linear_dw(dz, x, dw, addend, stream, checked)
     if st:
         raise GemmError(st, "linear_dw")
     return dw
@@ -157,7 +165,7 @@ def orthogonalize(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, *
         a, b, c = coefficients
     except (TypeError, ValueError):
         raise ValueError("coefficients must be three numbers") from None
-    st = Q.load_binding().orthogonalize(g, out, workspace, steps, a, b, c, eps, scale, stream, checked)
+    st = (_ext or _binding()).orthogonalize(g, out, workspace, steps, a, b, c, eps, scale, stream, checked)
     if st:
         raise GemmError(st, "orthogonalize")
     return out

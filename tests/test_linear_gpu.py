@@ -311,7 +311,8 @@ def workspace(g):
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("out", [F16, BF16])
 @pytest.mark.parametrize("B,rows_,cols", [(1, 1, 1), (1, 1, 50), (2, 40, 3), (3, 24, 100), (2, 130, 60), (1, 257, 300),
-                                          (2, 300, 1000), (1, 1000, 301), (1, 520, 2100)])
+                                          (2, 300, 1000), (1, 1000, 301), (1, 520, 2100), (5, 128, 513), (2, 100, 2560),
+                                          (1, 3000, 128), (40, 64, 700), (1, 17, 2049), (1, 128, 2561), (200, 9, 65)])
 def test_orthogonalize(B, rows_, cols, dtype, out):
     g = rand(1, B, rows_, cols, std=1e-3).to(dtype)
     o = batch(torch.zeros(B, rows_, cols, dtype=out))
