@@ -157,9 +157,10 @@ def test_orthogonalize_workspace(lib):
     for B, r, c in ((1, 1, 1), (3, 100, 999), (2, 999, 100), (1, 4096, 8192)):
         g = torch.empty(B, r, c, device="meta")
         small = min(r, c)
-        # two X and two squares in 16 bits, the norm's parts, and each on a boundary of 256
+        # two X and two squares in 16 bits, rows padded by 63 elements at most, the norm's
+        # parts, and each on a boundary of 256
         least = B * (4 * r * c + 4 * small * small)
-        assert least <= L.orthogonalize_workspace(g) <= B * (4 * r * (c + 7) + 4 * small * (small + 7) + 8196) + 2048
+        assert least <= L.orthogonalize_workspace(g) <= B * (4 * r * (c + 63) + 4 * small * (small + 63) + 8196) + 2048
         assert L.orthogonalize_workspace(g[0]) <= L.orthogonalize_workspace(g)
     with pytest.raises(ValueError):
         L.orthogonalize_workspace(torch.empty(4))
