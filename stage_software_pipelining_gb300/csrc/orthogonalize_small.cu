@@ -202,10 +202,10 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
     const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32q.., and which blocks of 64 columns
     const int i = 32 * q + lane;               // this thread's row
     const uint32_t t_row = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    // Sixty-four columns of this thread's row.
-    auto sums = [&](int block, uint32_t (&r)[64]) {
-        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(block * 64), *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(block * 64 + 32), *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+    // Thirty-two columns of this thread's row.  Every use is in a loop that is not
+    // unrolled: the steps' code is to stay in the instruction cache.
+    auto sums = [&](int col, uint32_t (&r)[32]) {
+        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(col), r);
         tmem_ld_wait();
     };
     for (int step = 0; step < p.steps; ++step) {
@@ -222,17 +222,19 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
         __syncwarp();
         products_done();
         const float alpha = first ? p.sa * t * t : p.sa / (p.sx * p.sx);
-        {
-            uint32_t r[64];
-            sums(half, r);
+#pragma unroll 1
+        for (int h = 2 * half; h < 2 * half + 2; ++h) {  // columns 32h..
+            uint32_t r[32];
+            sums(32 * h, r);
             if (split == 1) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     uint32_t u[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         u[k] = pack16<false>(alpha * __uint_as_float(r[8 * j + 2 * k]), alpha * __uint_as_float(r[8 * j + 2 * k + 1]));
-                    st_shared_v4(piece(A + static_cast<uint32_t>(half) * BLOCK, i, j), make_uint4(u[0], u[1], u[2], u[3]));
+                    st_shared_v4(piece(A + static_cast<uint32_t>(half) * BLOCK, i, 4 * (h & 1) + j),
+                                 make_uint4(u[0], u[1], u[2], u[3]));
                 }
             } else {
                 // Each CTA joins a share of the rows: it gets them from all.
@@ -240,13 +242,13 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
                 const uint32_t to = mapa_shared(P + static_cast<uint32_t>(rank * most + i - SIDE * owner / split) * 512u,
                                                 static_cast<uint32_t>(owner));
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    st_cluster_f4(to + static_cast<uint32_t>(((16 * half + j) ^ lane) << 4),
+                for (int j = 0; j < 8; ++j)
+                    st_cluster_f4(to + static_cast<uint32_t>(((8 * h + j) ^ lane) << 4),
                                   make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
                                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
             }
-            tc_fence_before();
         }
+        tc_fence_before();
         if (split > 1) {
             cluster_sync_all();
             const int r0 = SIDE * rank / split, r1 = SIDE * (rank + 1) / split;
@@ -283,13 +285,14 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
         }
         __syncwarp();
         products_done();
-        {
-            uint32_t r[64];
-            sums(half, r);
-            const float gamma = p.c / p.sa;
+        const float gamma = p.c / p.sa;
+#pragma unroll 1
+        for (int h = 2 * half; h < 2 * half + 2; ++h) {
+            uint32_t r[32];
+            sums(32 * h, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint4 old = ld_shared_v4(piece(A + static_cast<uint32_t>(half) * BLOCK, i, j));
+            for (int j = 0; j < 4; ++j) {
+                const uint4 old = ld_shared_v4(piece(A + static_cast<uint32_t>(half) * BLOCK, i, 4 * (h & 1) + j));
                 const uint32_t w[4] = {old.x, old.y, old.z, old.w};
                 uint32_t u[4];
 #pragma unroll
@@ -298,10 +301,11 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
                     u[k] = pack16<false>(fmaf(p.b, f.x, gamma * __uint_as_float(r[8 * j + 2 * k])),
                                          fmaf(p.b, f.y, gamma * __uint_as_float(r[8 * j + 2 * k + 1])));
                 }
-                st_shared_v4(piece(B + static_cast<uint32_t>(half) * BLOCK, i, j), make_uint4(u[0], u[1], u[2], u[3]));
+                st_shared_v4(piece(B + static_cast<uint32_t>(half) * BLOCK, i, 4 * (h & 1) + j),
+                             make_uint4(u[0], u[1], u[2], u[3]));
             }
-            tc_fence_before();
         }
+        tc_fence_before();
         fence_proxy_async_shared();
         __syncthreads();
         tc_fence_after();
@@ -324,42 +328,56 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
         products_done();
         const float sn = last ? p.scale : p.sx;  // what the new X is multiplied by
         const float by_sum = first ? sn / p.sa * t : sn / (p.sa * p.sx), by_old = first ? p.a * sn * t : p.a * sn / p.sx;
+        uint16_t* const o = static_cast<uint16_t*>(p.out) + b * p.stride_o;
 #pragma unroll 1
-        for (int blk = half; blk < p.w / 64; blk += 2) {
-            uint32_t r[64];
-            sums(blk, r);
-            const uint32_t xb = X + static_cast<uint32_t>(blk) * BLOCK;
-            const int j = j0 + 64 * blk;  // the block's first column
+        for (int h = half; h < p.w / 32; h += 2) {  // columns 32h.. of the slice
+            uint32_t r[32];
+            sums(32 * h, r);
+            const uint32_t xb = X + static_cast<uint32_t>(h / 2) * BLOCK;
 #pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) {
-                const uint4 old = ld_shared_v4(piece(xb, i, k8));
+            for (int k8 = 0; k8 < 4; ++k8) {
+                const uint32_t at = piece(xb, i, 4 * (h & 1) + k8);
+                const uint4 old = ld_shared_v4(at);
                 const uint32_t w[4] = {old.x, old.y, old.z, old.w};
                 uint32_t u[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 f = unpack16<false>(w[k]);
-                    const float x = fmaf(by_old, f.x, by_sum * __uint_as_float(r[8 * k8 + 2 * k]));
-                    const float y = fmaf(by_old, f.y, by_sum * __uint_as_float(r[8 * k8 + 2 * k + 1]));
-                    u[k] = pack16(last && p.out_bf16, x, y);
+                    u[k] = pack16(last && p.out_bf16, fmaf(by_old, f.x, by_sum * __uint_as_float(r[8 * k8 + 2 * k])),
+                                  fmaf(by_old, f.y, by_sum * __uint_as_float(r[8 * k8 + 2 * k + 1])));
                 }
-                if (!last) {
-                    st_shared_v4(piece(xb, i, k8), make_uint4(u[0], u[1], u[2], u[3]));
-                } else if (i < p.n) {
-                    const int c = j + 8 * k8, left = p.m - c;
-                    uint16_t* o = static_cast<uint16_t*>(p.out) + b * p.stride_o;
-                    if (p.tall) {  // the lanes' rows are adjacent in the output
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < left) o[(c + k) * p.ldo + i] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
-                    } else if (left >= 8) {
-                        *reinterpret_cast<uint4*>(o + i * p.ldo + c) = make_uint4(u[0], u[1], u[2], u[3]);
+                // (the output, too, leaves by way of X's place)
+                st_shared_v4(at, make_uint4(u[0], u[1], u[2], u[3]));
+            }
+        }
+        if (last) {
+            __syncthreads();
+            if (!p.tall) {
+                // Eight columns of a row a thread.
+                for (int e = tid; e < p.n * (p.w / 8); e += THREADS) {
+                    const int row = e / (p.w / 8), c = e % (p.w / 8) * 8, left = cols - c;
+                    const uint4 v = ld_shared_v4(piece(X + static_cast<uint32_t>(c / 64) * BLOCK, row, c % 64 / 8));
+                    uint16_t* d = o + row * p.ldo + j0 + c;
+                    if (left >= 8) {
+                        *reinterpret_cast<uint4*>(d) = v;
                     } else {
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int k = 0; k < 7; ++k)
-                            if (k < left) o[i * p.ldo + c + k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
+                            if (k < left) d[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
                     }
                 }
+            } else {
+                // A row of the output is a column of X: adjacent lanes, adjacent rows of X.
+                const uint8_t* x = smem;
+                for (int e = tid; e < cols * SIDE; e += THREADS) {
+                    const int row = e % SIDE, c = e / SIDE;
+                    if (row < p.n)
+                        o[(j0 + c) * p.ldo + row] = *reinterpret_cast<const uint16_t*>(
+                            x + (piece(X + static_cast<uint32_t>(c / 64) * BLOCK, row, c % 64 / 8) - X) + c % 8 * 2);
+                }
             }
+            break;
         }
         tc_fence_before();
         fence_proxy_async_shared();
