@@ -29,8 +29,8 @@ __device__ GemmDeviceStatus g_product_pair_status;
 namespace {
 
 constexpr int MAX_STAGES = 6;
-constexpr int EPI_BYTES = 8192;    // boxes of an epilogue warp: two of 4 KB
 constexpr int BOX = 4096;
+constexpr int MOST_SLOTS = 4;      // boxes of an epilogue warp: two, or four
 constexpr uint16_t kPairMask = 0x3;
 
 // Warps: A's copies, MMA, B's copies, none, and eight of the epilogue.  Each
@@ -54,6 +54,7 @@ struct PairParams {
     int k_chunks;  // accumulations of a tile, summed by the epilogue (EPI_F32)
     int group_m;   // tile rows walked together
     int stages;
+    int slots;     // boxes of an epilogue warp
     int a_mn, b_mn;
     int b_chunks;  // MN-major B: chunks of 64 columns of a CTA's stage
     int a_whole, b_whole;  // rows and columns below which a stage's chunks come by one copy
@@ -73,7 +74,7 @@ struct PairParams {
 
 struct PairCtl {
     unsigned long long bar[2 * MAX_STAGES + 5];  // full, empty, tmem_full[2], tmem_empty[2], drain
-    unsigned long long in_bar[8 * 2];            // inputs of an epilogue warp's boxes
+    unsigned long long in_bar[8 * MOST_SLOTS];   // inputs of an epilogue warp's boxes
     uint32_t tmem_base;
     int abort;
 };
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* a_ring = smem;
     uint8_t* b_ring = smem + S * P_TILE_BYTES;
     uint8_t* epi_ring = b_ring + S * b_bytes;
-    PairCtl* ctl = reinterpret_cast<PairCtl*>(epi_ring + 8 * EPI_BYTES);
+    PairCtl* ctl = reinterpret_cast<PairCtl*>(epi_ring + 8 * p.slots * BOX);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank() & 1u;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(tempty_bar(a), 16);  // one arrive per epilogue warp of both CTAs
         }
         mbar_init(drain_bar, 1);
-        for (int i = 0; i < 16; ++i) mbar_init(smem_addr(&ctl->in_bar[i]), 1);
+        for (int i = 0; i < 8 * MOST_SLOTS; ++i) mbar_init(smem_addr(&ctl->in_bar[i]), 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -204,19 +205,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         if constexpr (EPI == EPI_F32) registers_up<208>();
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const uint32_t tempty_leader0 = mapa_shared(tempty_bar(0), 0u);
-        // Two warps a quarter take turns at its boxes.  A box needs a second one
-        // beside it for a second input (z of the activation) or output (z kept, or
-        // the mirror image of a symmetric result's): then there is one at a time,
-        // else two.
+        // Two warps a quarter take turns at its boxes.  A box needs a second slot
+        // beside its own for a second input (z of the activation) or output (z kept,
+        // or the mirror image of a symmetric result's); `depth` boxes have their own.
         const int half = (warp - FIRST) >> 2;
         constexpr int COLS = EPI == EPI_F32 ? 32 : 64;  // of a box
         const int boxes = (p.bn + COLS - 1) / COLS;     // of a tile; the last may have 32 columns
         const bool twin = EPI == EPI_LINEAR ? p.has_p : EPI == EPI_GRAD ? p.has_r : EPI == EPI_STEP ? p.symmetric : false;
-        const int depth = twin ? 1 : 2;
-        const uint32_t buf0 = smem_addr(epi_ring) + static_cast<uint32_t>((warp - FIRST) * EPI_BYTES);
-        const uint32_t in_bar0 = smem_addr(&ctl->in_bar[(warp - FIRST) * 2]);
+        const int depth = twin ? p.slots / 2 : p.slots, size = twin ? 2 * BOX : BOX;
+        const uint32_t buf0 = smem_addr(epi_ring) + static_cast<uint32_t>((warp - FIRST) * p.slots * BOX);
+        const uint32_t in_bar0 = smem_addr(&ctl->in_bar[(warp - FIRST) * MOST_SLOTS]);
         const bool inputs = EPI == EPI_GRAD || p.has_r;
         const bool vec_bias = (reinterpret_cast<uintptr_t>(p.bias) & 15u) == 0;
+        // Nothing but the sums: past all the branches below, which take as long as the
+        // rounding.
+        const bool plain = EPI == EPI_LINEAR && !p.bias && !p.has_p && !p.has_r && p.act == LINEAR_ACT_NONE;
         uint32_t in_phase = 0, in_pending = 0;  // bit d: parity of, and whether a copy is on its way to, slot d
         uint32_t count = 0;  // boxes stored so far: the slots run on from tile to tile
         int lt = 0;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int within = row_base < p.M ? min(boxes, (p.N - col0 + COLS - 1) / COLS) : 0;
             auto width = [&](int box) { return min(COLS, p.bn - box * COLS); };
             auto fetch = [&](int box, uint32_t at) {  // lane 0: a box's inputs
-                const uint32_t bar = in_bar0 + 8u * at, buf = buf0 + at * BOX;
+                const uint32_t bar = in_bar0 + 8u * at, buf = buf0 + at * size;
                 const int n = col0 + box * COLS;
                 const bool narrow = EPI != EPI_F32 && width(box) == 32;
                 const uint32_t bytes = narrow ? BOX / 2 : BOX;
@@ -311,7 +314,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 if (!inputs && lane == 0 && count >= static_cast<uint32_t>(depth)) {
-                    if (depth == 2) bulk_wait_group_read<1>();
+                    if (depth == 4) bulk_wait_group_read<3>();
+                    else if (depth == 2) bulk_wait_group_read<1>();
                     else bulk_wait_group_read<0>();
                 }
                 __syncwarp();
@@ -320,15 +324,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return const_cast<uint8_t*>(static_cast<const uint8_t*>(m.p)) +
                        (static_cast<long long>(b) * m.stride + static_cast<long long>(row) * m.ld) * size;
             };
-            // After a box's store: the slot after this one takes the inputs of this
-            // warp's next box, where they are not on their way.
+            // After a box's store: the slot of this warp's box before it (or this one's
+            // own, the only one) takes the inputs of the next that has none.
             auto stored = [&](int box) {
-                const int next = box + 2;
+                const int next = depth == 1 ? box + 2 : box + 2 * (depth - 1);
                 if (inputs && (depth == 1 || box >= 2) && next < within && !*abort_flag) {
-                    const uint32_t to = (count + 1) % depth;
+                    const uint32_t to = (count + depth - 1) % depth;
                     if (lane == 0) {
-                        if (depth == 2) bulk_wait_group_read<1>();
-                        else bulk_wait_group_read<0>();
+                        if (depth == 1) bulk_wait_group_read<0>();
+                        else bulk_wait_group_read<1>();
                         fetch(next, to);
                     }
                     in_pending |= 1u << to;
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int box = half + 2 * i;
                     if (box < within) {
                         const int n0 = col0 + box * 32;
-                        const uint32_t at = count % depth, buf = buf0 + at * BOX;
+                        const uint32_t at = count % depth, buf = buf0 + at * size;
                         slot_ready(at);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int box = half; box < within; box += 2) {
                     const int n0 = col0 + box * 64;
                     const bool narrow = width(box) == 32;
-                    const uint32_t at = count % depth, buf = buf0 + at * BOX;
+                    const uint32_t at = count % depth, buf = buf0 + at * size;
                     slot_ready(at);
                     // Thirty-two columns at a time, in a loop: unrolled, the four
                     // activations' code would be read from memory once a tile.
@@ -395,6 +399,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int e = 0; e < 16; ++e)
                             v[e] = make_pair2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                         uint32_t u[16];
+                        if (plain && !last) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = pack16<BF16>(v[e]);
+                            write_box(buf, lane, h, narrow, u);
+                            continue;
+                        }
                         if (EPI == EPI_LINEAR && p.bias && left > 0) {
                             if (vec_bias && left >= 32) {
                                 const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + n);
@@ -622,6 +632,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ---------------------------------------------------------------- host side
 constexpr int kInstances = 7;
 
+// K blocks of a tile whose epilogue outlasts its products.
+constexpr int kShortSum = 8;
 // fp32 outputs: K blocks of one accumulation, 1024 rows.
 constexpr int kPairChunk = 16;
 
@@ -680,10 +692,17 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.a_whole = p.M - 127;
     p.b_whole = p.N - (64 * p.b_chunks - 1);
     p.idesc = product_instruction(256, bn, L.bf16, L.a_mn, L.b_mn);
-    // As many stages as there is room for beside the epilogue's boxes.
+    // Four boxes an epilogue warp where a tile's products are over before an epilogue
+    // that moves two tensors a box or fp32, two elsewhere, and as many stages as there
+    // is room for beside them.  (Sums of 8 into 5696 x 4416 fp32 with an addend: 37.8
+    // us, with two boxes 45.3; where only an output leaves, three stages for five cost
+    // more than boxes gain.)
+    const bool moves = EPI == EPI_F32 || (EPI == EPI_GRAD && L.R.p) || (EPI == EPI_LINEAR && L.P.p && L.act != LINEAR_ACT_NONE);
+    p.slots = moves && p.k_blocks <= kShortSum ? 4 : 2;
     const int stage = P_TILE_BYTES + (L.b_mn ? 64 * p.b_chunks : bn / 2) * PK * 2;
-    const int room = kProductSmem - 1024 - 8 * EPI_BYTES - static_cast<int>(sizeof(PairCtl));
-    static_assert((kProductSmem - 1024 - 8 * EPI_BYTES - static_cast<int>(sizeof(PairCtl))) / (2 * P_TILE_BYTES) >= 5,
+    const int room = kProductSmem - 1024 - 8 * p.slots * BOX - static_cast<int>(sizeof(PairCtl));
+    static_assert((kProductSmem - 1024 - 16 * BOX - static_cast<int>(sizeof(PairCtl))) / (2 * P_TILE_BYTES) >= 5 &&
+                      (kProductSmem - 1024 - 32 * BOX - static_cast<int>(sizeof(PairCtl))) / (2 * P_TILE_BYTES) >= 2,
                   "stages of the widest tile");
     p.stages = room / stage < MAX_STAGES ? room / stage : MAX_STAGES;
     p.act = L.act;
