@@ -175,8 +175,8 @@ int linear_plan(int op, int64_t M, int64_t N, int64_t K, int out_dtype, quant_pl
  *     `steps` times:  A = X X^T,  X = a X + (b A + c A^2) X
  *     out = scale * X
  *
- * which brings the singular values of G near one (to 0.7 .. 1.2 in five steps
- * with a, b, c = 3.4445, -4.7750, 2.0315, but for those below 1e-3 |G|) and
+ * which brings the singular values of G near one (to 0.65 .. 1.25 in five steps
+ * with a, b, c = 3.4445, -4.7750, 2.0315, but for those below 2e-3 |G|) and
  * leaves its singular vectors.  A matrix of more rows than columns takes
  * A = X^T X and X (...) instead, which gives the same.
  *   g          batch matrices, `stride_g` elements apart, of any quant_type_t,
@@ -191,9 +191,9 @@ int linear_plan(int op, int64_t M, int64_t N, int64_t K, int out_dtype, quant_pl
  * X, A and b A + c A^2 are held in fp16 between the products, at power-of-two
  * scales that put their elements in fp16's range; the products are summed and
  * combined in fp32.  That is 2^-11 a rounding, an eighth of what bf16 would
- * lose: a gradient of full rank comes out within 1e-3 of its norm, before the
+ * lose: a gradient of full rank comes out within 2e-3 of its norm, before the
  * output's own rounding.  Directions whose singular value is below some
- * 1e-4 |G| are lost in the roundings.  The scales hold for coefficients that
+ * 1e-4 |G| are lost in the roundings, as is a G that is small beside eps.  The scales hold for coefficients that
  * keep X's singular values below 1.9 and those of b A + c A^2 below 3.9; others
  * may overflow to infinity.  A NaN or an infinity in a matrix makes its output
  * NaN; a matrix of zeros gives zeros (with eps = 0: NaN).  Elements of every

@@ -1,5 +1,6 @@
 """Build libgemm.so (the C-ABI library) in-tree for sm_103a, and the Python
-extension ``_quant.so`` that marshals torch tensors into its quantised operators.
+extension ``_quant.so`` that marshals torch tensors into its quantised and training
+operators.
 
 Each ``csrc/*.cu`` file is compiled by its own ``nvcc -c`` and ``binding.cpp``
 by g++ (in parallel), then linked into
