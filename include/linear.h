@@ -56,8 +56,8 @@ extern "C" {
 
 /*
  * Activations and their derivatives.  At infinities both are their limits
- * (those of -infinity are 0), and a NaN gives a NaN, but relu's derivative,
- * which is 1 there.  relu'(0) = 0.
+ * (those of -infinity are 0, to within 1e-17), and a NaN gives a NaN, but relu's
+ * derivative, which is 1 there.  relu'(0) = 0.
  */
 typedef enum {
     LINEAR_ACT_NONE = 0,
@@ -70,7 +70,7 @@ typedef enum {
 /* The kernels of the products, as linear_plan names them. */
 typedef enum {
     LINEAR_KERNEL_FEW = 0, /* tiles of 128 columns by 16 to 256 rows, K cut over a cluster */
-    LINEAR_KERNEL_PAIR = 1 /* tiles of 256 x 256 on CTA pairs */
+    LINEAR_KERNEL_PAIR = 1 /* tiles of 256 rows by 192 to 256 columns on CTA pairs */
 } linear_kernel_t;
 
 /* The products whose launch linear_plan tells. */
@@ -135,8 +135,9 @@ int linear_dx(int64_t M, int64_t N, int64_t K, const void* dz, int64_t lddz, con
  *   addend    N x K of out_dtype, ldc >= K, or NULL; may be dW itself (same
  *             leading dimension)
  * With an fp32 dW, no accumulator sums more than 4096 rows: the tensor cores
- * truncate, which over 32768 rows would lose 4e-5 of a sum.  M = 0 gives the
- * addend (or 0).
+ * truncate, which over 32768 rows would lose 4e-5 of a sum.  (A 16-bit dW is
+ * summed by one accumulator and does lose it: half an fp16 step at 400000 rows.)
+ * M = 0 gives the addend (or 0).
  */
 int linear_dw(int64_t M, int64_t N, int64_t K, const void* dz, int64_t lddz, const void* x,
               int64_t ldx, const void* addend, int64_t ldc, void* dW, int64_t lddw, int dtype,
@@ -191,11 +192,11 @@ int linear_plan(int op, int64_t M, int64_t N, int64_t K, int out_dtype, quant_pl
  * X, A and b A + c A^2 are held in fp16 between the products, at power-of-two
  * scales that put their elements in fp16's range; the products are summed and
  * combined in fp32.  That is 2^-11 a rounding, an eighth of what bf16 would
- * lose: a gradient of full rank comes out within 2e-3 of its norm, before the
+ * lose: a gradient of full rank comes out within 3e-3 of its norm, before the
  * output's own rounding.  Directions whose singular value is below some
- * 1e-4 |G| are lost in the roundings, as is a G that is small beside eps.  The scales hold for coefficients that
- * keep X's singular values below 1.9 and those of b A + c A^2 below 3.9; others
- * may overflow to infinity.  A NaN or an infinity in a matrix makes its output
+ * 1e-4 |G| are lost in the roundings, as is a G that is small beside eps.  The
+ * scales hold for coefficients that keep X's singular values below 1.9 and those of
+ * b A + c A^2 below 3.9; others may overflow to infinity.  A NaN or an infinity in a matrix makes its output
  * NaN; a matrix of zeros gives zeros (with eps = 0: NaN).  Elements of every
  * finite magnitude are taken.  rows and cols above 32768 are
  * GEMM_ERR_UNSUPPORTED, as is a batch above 65535.  The strides between

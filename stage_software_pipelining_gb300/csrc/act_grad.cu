@@ -17,7 +17,6 @@
 namespace ssp {
 namespace {
 
-
 struct Params {
     int M, N;
     int rows;  // of a CTA
@@ -201,8 +200,9 @@ int launch(const ActGradLaunch& L, cudaStream_t stream) {
 
 // Strips of 64 columns, 128 bytes a row, and CTAs of 512 threads, two an SM.  Where
 // clusters of eight of them leave many places empty (a sum over many rows of few
-// columns), strips of 32 columns: 32768 x 1024 in strips of 64 69 us, of 32 39.  Where rows are many and the strips fill one CTA an SM better than two, CTAs
-// of 1024 threads.
+// columns), strips of 32 columns: 32768 x 1024 in strips of 64 takes 69 us, of 32
+// 39.  Where rows are many and the strips fill one CTA an SM better than two, CTAs of
+// 1024 threads.
 template <bool BF16>
 int launch_vectors(const ActGradLaunch& L, cudaStream_t stream) {
     const int64_t sms = tc_current_device_sms();

@@ -1,7 +1,7 @@
 // binding.cpp -- Python's way into libgemm.so's quantised operators
-// (include/quant.h) and training operators (include/linear.h): the checks of tensor arguments and their marshalling into
-// (pointer, leading dimension) pairs, in C++ because at a token a call they
-// are most of a call's time (measured on a Grace host: 14 us of a 20 us
+// (include/quant.h) and training operators (include/linear.h): the checks of
+// tensor arguments and their marshalling into (pointer, leading dimension) pairs,
+// in C++ because at a token a call they are most of a call's time (measured on a Grace host: 14 us of a 20 us
 // gemm_fp8 call when written in Python over ctypes).
 //
 // Every function takes its arguments by position (quant.py and linear.py hold

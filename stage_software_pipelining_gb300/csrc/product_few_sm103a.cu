@@ -348,7 +348,9 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
     auto first = [&](int r) { return (16 * r + split - 1) / split; };
     const uint32_t bias0 = smem_addr(ctl->bias);
     if (PUSH && split > 1) cluster_wait();  // every CTA has started
-    if (warp >= FIRST) {
+    // All eight warps: two share a quarter of the accumulators' lanes and take turns at
+    // its rows, sixteen at a time.
+    {
         const int q = warp & 3;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         const int n = 32 * q + lane;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
                                                       4u * (n & 7)
                                                 : 0u;
 #pragma unroll 1
-        for (int c = 0; c < rows; c += 16) {
+        for (int c = 16 * (warp >> 2); c < rows; c += 32) {
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
             tmem_ld_wait();
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
             } else {
                 // By way of shared memory, a warp its own, from a column a thread
                 // to eight adjacent outputs of two rows a thread.
-                const uint32_t turn = smem_addr(part) + static_cast<uint32_t>(q * 4096 + (c & 16) * 128);
+                const uint32_t turn = smem_addr(part) + static_cast<uint32_t>(warp * 2048);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) st_shared_u32(turn + static_cast<uint32_t>(i * 128 + lane * 4), r[i]);
                 __syncwarp();
@@ -520,13 +522,14 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
 }
 
 // Which kernel, tile and cut of K: the one with the least time by a model in
-// microseconds, whose constants were fitted to every choice measured on 76 shapes of
+// microseconds, whose constants were fitted to every choice measured on 82 shapes of
 // 1 to 30000 rows (the pairs' K blocks to large shapes alone).  On those its choices
-// are 3 % slower than the best one of each on average, 23 % at most (200 x 2048 x
-// 2048: 10.9 us for 8.9).
+// are 1.6 % slower than the best one of each on average, 12 % at most (147 x 2368 x
+// 1856: 9.7 us for 8.7).
 //   * few rows: a round of resident CTAs takes each one's K blocks and an
-//     epilogue that grows with the rows, a quarter more where two share an SM; a cut K
-//     adds the partials' way through distributed shared memory.
+//     epilogue that grows with the rows, and a cut K the partials' way through
+//     distributed shared memory.  A K block takes its products and copies, more where
+//     two CTAs share an SM, or what the SM's port to L2 takes for its bytes (156 GB/s).
 //   * pairs: a round takes its K blocks and the part of an epilogue that does not run
 //     under products, the launch another.
 struct Choice {
@@ -537,8 +540,11 @@ struct Choice {
 };
 
 bool choose(const ProductLaunch& L, Choice* best) {
-    int resident[9];
-    if (!product_resident_ctas(resident)) return false;
+    // CTAs that run at once, one an SM or two.  (A cluster lies within a GPC: two CTAs
+    // an SM take half of its SMs.)
+    int resident[2][9];
+    if (!product_resident_ctas(resident[0])) return false;
+    for (int c = 0; c <= 8; ++c) resident[1][c] = 2 * resident[0][c % 2 == 0 ? c / 2 : c];
     const int64_t kb = (L.K + PK - 1) / PK;
     if (kb == 0) {  // no operands to read: the epilogue alone
         best->mt = 128;
@@ -571,21 +577,23 @@ bool choose(const ProductLaunch& L, Choice* best) {
     for (int mt = mt0; mt <= 256 && (mt == mt0 || mt < 2 * L.M); mt *= 2) {
         const int64_t tiles = up(L.M, mt) * up(L.N, 128) * L.batch;
         for (int c = 1; c <= 8 && c <= kb; ++c) {
-            if (resident[c] <= 0) continue;
+            if (resident[0][c] <= 0) continue;
             const int64_t accs = L.epi == EPI_F32 ? up(up(kb, c), kProductChunk) : 1;
             if (accs * mt > 512) continue;
             const int64_t ctas = tiles * c;
             if (ctas > 0x7fffffff) continue;
+            const double rows = static_cast<double>(mt < L.M ? mt : L.M);
             for (int t = 0; t <= (mt <= kTwo && accs * mt <= 256 ? 1 : 0); ++t) {
-                const double rounds = static_cast<double>(up(ctas, resident[c] * (1 + t)));
-                const bool alone = ctas <= resident[c];  // one CTA an SM at most
-                const int64_t rows = mt < L.M ? mt : L.M;
-                const double us = bounded(
-                    (t ? 0.2 : 0.33) +
-                        rounds * (t && !alone ? 1.25 : 1.0) *
-                            (up(kb, c) * ((t && alone ? 0.225 : 0.199) + 0.00056 * mt) + 2.61 + 0.028 * rows) +
-                        (c > 1 ? 0.28 + 0.0047 * rows + 0.092 * c : 0.0),
-                    5.75e6);
+                const bool shared = t && ctas > resident[0][c];  // two CTAs an SM, not one
+                const double slower = shared ? 1.18 : 1.0;
+                const double block = 0.199 + 0.00042 * mt + (t && !shared ? 0.03 : 0.0);
+                const double port = (shared ? 2.0 : 1.0) * (P_TILE_BYTES + PK * 2.0 * mt) / 156e3;
+                const double rounds = static_cast<double>(up(ctas, resident[t][c]));
+                double us = (t ? 0.53 : 0.67) +
+                            rounds * (up(kb, c) * (slower * block > port ? slower * block : port) +
+                                      slower * (c > 1 ? 3.1 + 0.0427 * rows : 2.36 + 0.0168 * rows));
+                if (c > 1) us += (shared ? 0.157 : 0.1) * c - 0.0088 * rows - 0.46;
+                us = bounded(us, 5.75e6);
                 if (us < least) {
                     least = us;
                     best->mt = mt;

@@ -69,7 +69,7 @@ def test_linear_any_set_of_parts(M, N, K, name, bias, residual, pre):
         assert (z.view.float() == torch.tensor(12345.0).to(dtype).float().item()).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 64, 64), (700, 1100, 200)])
+@pytest.mark.parametrize("M,N,K", [(3, 64, 64), (700, 1100, 200), (1300, 2048, 200)])
 def test_linear_residual_in_place(M, N, K):
     x, W, r = rand(1, M, K).to(BF16), rand(2, N, K, std=0.1).to(BF16), rand(3, M, N).to(BF16)
     h = GuardedC(M, N, BF16, init=r)
@@ -172,7 +172,7 @@ def test_linear_dx_any_set_of_parts(M, N, K, name, residual):
     R.check_dx(dx.view, dz, W, r, z, name)
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 64, 72), (700, 200, 1100)])
+@pytest.mark.parametrize("M,N,K", [(3, 64, 72), (700, 200, 1100), (1300, 200, 2048)])
 @pytest.mark.parametrize("over", ["residual", "pre"])
 def test_linear_dx_in_place(M, N, K, over):
     dz, W = rand(1, M, N).to(F16), rand(2, N, K, std=0.1).to(F16)

@@ -80,19 +80,19 @@ def run(op, M, N, K, dtype, out=None, parts=True):
 CASES = [
     ("linear", 1, 40, 40, "few", 16, 0, None), ("linear", 1, 40, 200, "few", 16, 2, None),
     ("linear", 3000, 40, 40, "few", 32, 0, None), ("linear", 20, 3000, 500, "few", 32, 2, None),
-    ("linear", 5000, 40, 100, "few", 64, 0, None), ("linear", 40, 3000, 1500, "few", 64, 2, None),
+    ("linear", 5000, 40, 200, "few", 64, 0, None), ("linear", 40, 3000, 1500, "few", 64, 2, None),
     ("linear", 100, 3000, 3000, "few", 128, 2, None), ("linear", 130, 5000, 3000, "few", 256, 2, None),
-    ("linear", 600, 2100, 64, "pair", 256, 0, 66),        # tiles of 192 columns
+    ("linear", 1000, 2700, 64, "pair", 256, 0, 120),      # tiles of 192 columns
     ("linear", 300, 8512, 1030, "pair", 256, 0, 152),     # of 224
     ("linear", 2000, 2041, 2000, "pair", 256, 0, 128),    # of 256
     ("dx", 1, 40, 40, "few", 16, 0, None), ("dx", 1, 200, 40, "few", 16, 2, None),
     ("dx", 3000, 40, 40, "few", 32, 0, None), ("dx", 20, 500, 3000, "few", 32, 2, None),
-    ("dx", 5000, 100, 40, "few", 64, 0, None), ("dx", 40, 1500, 3000, "few", 64, 2, None),
+    ("dx", 5000, 200, 40, "few", 64, 0, None), ("dx", 40, 1500, 3000, "few", 64, 2, None),
     ("dx", 100, 3000, 3000, "few", 128, 2, None), ("dx", 130, 3000, 5000, "few", 256, 2, None),
-    ("dx", 600, 64, 2100, "pair", 256, 0, 66), ("dx", 2000, 2000, 2041, "pair", 256, 0, 128),
-    ("dw", 1, 40, 40, "few", 64, 0, None), ("dw", 300, 40, 40, "few", 64, 2, None),
+    ("dx", 1000, 64, 2700, "pair", 256, 0, 120), ("dx", 2000, 2000, 2041, "pair", 256, 0, 128),
+    ("dw", 1, 40, 40, "few", 64, 0, None), ("dw", 500, 40, 40, "few", 64, 2, None),
     ("dw", 3000, 100, 3000, "few", 128, 2, None), ("dw", 3000, 130, 5000, "few", 256, 2, None),
-    ("dw", 64, 600, 2100, "pair", 256, 0, 66), ("dw", 2000, 2000, 2041, "pair", 256, 0, 128),
+    ("dw", 64, 1000, 2700, "pair", 256, 0, 120), ("dw", 2000, 2000, 2041, "pair", 256, 0, 128),
     ("dw", 20000, 130, 5000, "few", 256, 2, None),        # several accumulators a CTA
 ]
 
@@ -109,7 +109,8 @@ def test_every_instance(op, M, N, K, kernel, rows, cut, grid, dtype):
         run(op, M, N, K, dtype, out, parts=False)
 
 
-@pytest.mark.parametrize("M,N,K", [(300, 257, 100), (520, 513, 64), (700, 1025, 77), (257, 4100, 200), (400, 2305, 33)])
+@pytest.mark.parametrize("M,N,K", [(300, 257, 100), (520, 513, 64), (700, 1025, 77), (257, 4100, 200), (400, 2305, 33),
+                                   (1000, 2689, 64), (1300, 2041, 500)])
 def test_every_remainder_of_a_row(M, N, K):
     """Rows that end inside 16 bytes, by 1 to 7 columns: none is missed, none written past it."""
     for extra in range(8):
