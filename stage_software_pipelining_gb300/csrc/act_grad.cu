@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) act_grad_kernel(const
     constexpr int COLS = GROUPS * VEC, WARPS = THREADS / 32;
     __shared__ float sums[WARPS][COLS];
     __shared__ float total[COLS];
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int rank = static_cast<int>(blockIdx.y), parts = static_cast<int>(gridDim.y);  // a cluster is a column of the grid
     const int col0 = static_cast<int>(blockIdx.x) * COLS;
     const int lane = static_cast<int>(threadIdx.x) & 31;

@@ -84,8 +84,8 @@ __device__ __forceinline__ void each_group(const Params& p, int b, F&& f) {
 
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int b = static_cast<int>(blockIdx.y);
     SquareSum sq;
     each_group<TYPE>(p, b, [&](Place, const float(&v)[8]) { sq.add(v); });
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(THREADS) ortho_sum_kernel(const Params p) {
 // The first X, G 2^e, or (no steps) the output.
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS) ortho_first_kernel(const Params p) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int b = static_cast<int>(blockIdx.y);
     __shared__ float factors[3];
     if (threadIdx.x < 32) {

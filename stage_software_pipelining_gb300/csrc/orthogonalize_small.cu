@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
 
     // The slice in G: its rows [j0, j0 + cols) where X is the transpose, else those
     // columns; groups of eight elements of a row.

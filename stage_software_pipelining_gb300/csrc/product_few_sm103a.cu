@@ -185,6 +185,11 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
     // outputs are dealt to the CTAs in runs.  Else they lie over the ring once
     // it is read and are fetched, with a second barrier until they have been.
     constexpr bool PUSH = MT <= kPush;
+    // When the next launch's CTAs may start: once the products are done, so that they
+    // spread over the SMs as these leave, or, where a call is little but its start,
+    // as soon as the launch before has ended (1 x 4096 x 4096: 7.9 us so, 8.5 late; six
+    // 2048 x 512 orthogonalised: 167 us late, 172 so).
+    constexpr bool LATE = MT > 16;
     float* part = reinterpret_cast<float*>(smem);  // [MT][128]
     const uint32_t recv = smem_addr(ctl + 1);
 
@@ -225,8 +230,8 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
     if (PUSH && split > 1) cluster_arrive_relaxed();  // this CTA has started: its shared memory may be written to
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
-    griddep_launch_dependents();
     griddep_wait();
+    if (!LATE) griddep_launch_dependents();
 
     int it = 0;  // the copying threads: stages issued
     if (warp == 0 || warp == 2) {
@@ -322,6 +327,7 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
         }
     }
     __syncthreads();  // the accumulators are complete and the ring is read
+    if (LATE) griddep_launch_dependents();
     tc_fence_after();
     if (*abort_flag) {
         // Copies that no MMA waited for land before the ring is reused.  (A stage
@@ -524,8 +530,8 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
 // Which kernel, tile and cut of K: the one with the least time by a model in
 // microseconds, whose constants were fitted to every choice measured on 82 shapes of
 // 1 to 30000 rows (the pairs' K blocks to large shapes alone).  On those its choices
-// are 1.6 % slower than the best one of each on average, 12 % at most (147 x 2368 x
-// 1856: 9.7 us for 8.7).
+// are 2 % slower than the best one of each on average, 15 % at most (dw 8192 x 512 x
+// 512: 16.0 us for 13.9).
 //   * few rows: a round of resident CTAs takes each one's K blocks and an
 //     epilogue that grows with the rows, and a cut K the partials' way through
 //     distributed shared memory.  A K block takes its products and copies, more where

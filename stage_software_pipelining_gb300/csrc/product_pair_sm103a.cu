@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     cluster_sync_all();  // the peer's barriers exist before any remote arrive
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
 
     // 384 threads of 168 registers: 128 x 88 + 256 x 208 are as many.
     if (warp >= FIRST) {
