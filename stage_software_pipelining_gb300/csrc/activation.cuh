@@ -114,19 +114,19 @@ __device__ __forceinline__ Pair gelu_tanh_argument(Pair z) {
     return mul2(z, fma2(mul2(z, z), pair_of(2.0f * kGeluTanh * kGeluCube), pair_of(2.0f * kGeluTanh)));
 }
 
-// Phi(-|z|) = exp(-z^2 / 2) P(t), t = 1 / (1 + 0.36 |z|), and exp(-z^2 / 2): the
+// -Phi(-|z|) = -exp(-z^2 / 2) P(t), t = 1 / (1 + 0.36 |z|), and exp(-z^2 / 2): the
 // form of Hastings' approximations (Abramowitz and Stegun 7.1.26), with P fitted to
 // the least largest relative error over 0 <= |z| <= 14, 9e-7, so that the tail keeps
 // its digits too.  `size` is |z|, limited to 100.
 __device__ __forceinline__ Pair normal_tail(Pair z, Pair size, Pair& bell) {
     const Pair t = reciprocals(fma2(size, pair_of(0.36f), pair_of(1.0f)));
     bell = exp2_of(mul2(mul2(z, z), pair_of(-0.5f * kLog2e)));
-    Pair p = fma2(t, pair_of(0.0470564048f), pair_of(-0.179765101f));
-    p = fma2(t, p, pair_of(0.180954551f));
-    p = fma2(t, p, pair_of(0.0265489823f));
-    p = fma2(t, p, pair_of(0.139719377f));
-    p = fma2(t, p, pair_of(0.141772435f));
-    p = fma2(t, p, pair_of(0.143713047f));
+    Pair p = fma2(t, pair_of(-0.0470564048f), pair_of(0.179765101f));
+    p = fma2(t, p, pair_of(-0.180954551f));
+    p = fma2(t, p, pair_of(-0.0265489823f));
+    p = fma2(t, p, pair_of(-0.139719377f));
+    p = fma2(t, p, pair_of(-0.141772435f));
+    p = fma2(t, p, pair_of(-0.143713047f));
     return mul2(mul2(p, t), bell);
 }
 __device__ __forceinline__ Pair size_of(Pair z) {
@@ -142,7 +142,7 @@ __device__ __forceinline__ Pair activation(Pair z) {
         Pair bell;
         const Pair size = size_of(z), tail = normal_tail(z, size, bell);
         const float2 v = both(z);
-        return fma2(mul2(size, pair_of(-1.0f)), tail, make_pair2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+        return fma2(size, tail, make_pair2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) {
         const Pair f = at_least(z, -kGeluTanhEnd);
@@ -166,7 +166,7 @@ __device__ __forceinline__ Pair derivative(Pair z) {
         const Pair f = within(z, 30.0f);
         Pair bell;
         const Pair tail = normal_tail(f, size_of(f), bell);
-        const float2 v = both(f), h = both(fma2(tail, pair_of(-1.0f), pair_of(0.5f)));
+        const float2 v = both(f), h = both(add2(tail, pair_of(0.5f)));
         const Pair share = add2(make_pair2(copysignf(h.x, v.x), copysignf(h.y, v.y)), pair_of(0.5f));
         return fma2(mul2(f, pair_of(kBellTop)), bell, share);
     }
