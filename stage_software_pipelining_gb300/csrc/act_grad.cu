@@ -8,6 +8,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "activation.cuh"
 #include "internal.h"
 #include "linear.h"
@@ -16,6 +18,8 @@
 
 namespace ssp {
 namespace {
+
+constexpr int kMostParts = 16;  // CTAs of a cluster
 
 struct Params {
     int M, N;
@@ -150,8 +154,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) act_grad_kernel(const
     if (rank == 0 && threadIdx.x < COLS && col0 + static_cast<int>(threadIdx.x) < p.N) {
         const int j = col0 + static_cast<int>(threadIdx.x);
         float s = total[threadIdx.x];
-        for (int r = 1; r < parts; ++r)
-            s += ld_cluster_f32(mapa_shared(smem_addr(&total[threadIdx.x]), static_cast<uint32_t>(r)));
+#pragma unroll 1
+        for (int r0 = 1; r0 < parts; r0 += 8) {  // eight on their way together
+            float other[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                other[r] = ld_cluster_f32(mapa_shared(smem_addr(&total[threadIdx.x]), static_cast<uint32_t>(min(r0 + r, parts - 1))));
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r0 + r < parts) s += other[r];
+        }
         p.dbias[j] = p.addend ? p.addend[j] + s : s;
     }
     if (parts > 1) cluster_sync_all();  // the others' sums have been read
@@ -159,23 +171,44 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) act_grad_kernel(const
 
 // CTAs that share a strip's rows: as many as have a few each and run at once
 // (fewer CTAs in a second round than in the first leave memory idle).  A sum's are
-// a cluster, of eight at most.
-int parts_of(const ActGradLaunch& L, int cols, int groups, int threads) {
+// a cluster, of `widest` at most.
+int parts_of(const ActGradLaunch& L, int cols, int groups, int threads, int widest = 8) {
     const int64_t strips = (L.N + cols - 1) / cols;
     const int64_t slots = static_cast<int64_t>(tc_current_device_sms()) * (1024 / threads);
     const int64_t rows = 4 * (threads / groups);
     int64_t parts = (L.M + rows - 1) / rows;
     int64_t most = slots / strips;
-    if (L.dbias && most > 8) most = 8;
+    if (L.dbias && most > widest) most = widest;
     if (most < 1) most = 1;
     if (parts > most) parts = most;
     return static_cast<int>(parts < 1 ? 1 : parts);
 }
 
+// Clusters of more than eight CTAs are allowed once a device.
+bool allow_wide(const void* kernel, bool (&done)[64]) {
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> g(mu);
+    if (!done[dev])
+        done[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    return done[dev];
+}
+
 template <bool BF16, int VEC, int GROUPS, int THREADS>
 int launch(const ActGradLaunch& L, cudaStream_t stream) {
     constexpr int COLS = VEC * GROUPS;
-    const int parts = parts_of(L, COLS, GROUPS, THREADS);
+    // Sixteen CTAs a cluster, two an SM, where all strips' clusters run at once: as
+    // many as clusters of eight, one an SM (28491 x 210: 20 us, of eight CTAs 33).
+    int widest = 8;
+    if constexpr (COLS == 32) {
+        static bool done[64] = {};
+        int resident[9];
+        if (L.dbias && product_resident_ctas(resident) && (L.N + COLS - 1) / COLS <= resident[8] / 8 &&
+            allow_wide(reinterpret_cast<const void*>(act_grad_kernel<BF16, VEC, GROUPS, THREADS>), done))
+            widest = kMostParts;
+    }
+    const int parts = parts_of(L, COLS, GROUPS, THREADS, widest);
     Params p = {};
     p.M = static_cast<int>(L.M);
     p.N = static_cast<int>(L.N);

@@ -102,7 +102,8 @@ def test_both_kernels_are_reached():
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("name", ACTS)
 @pytest.mark.parametrize("M,N,extra,offset", [(1, 1, 0, 0), (1, 64, 0, 0), (61, 1000, 0, 0), (128, 70, 2, 0),
-                                              (300, 129, 7, 0), (1000, 96, 8, 1), (4099, 200, 0, 0), (33, 517, 3, 5)])
+                                              (300, 129, 7, 0), (1000, 96, 8, 1), (4099, 200, 0, 0), (33, 517, 3, 5),
+                                              (20000, 40, 0, 0), (9001, 210, 6, 0), (9001, 130, 1, 3)])
 def test_act_grad(M, N, extra, offset, name, dtype):
     dy, z = rand(1, M, N).to(dtype), rand(2, M, N, std=2.0).to(dtype)
 
