@@ -162,7 +162,8 @@ int linear_dw_checked(int64_t M, int64_t N, int64_t K, const void* dz, int64_t l
 
 /*
  * linear_plan -- the launch one of the products (`op`: a linear_op_t) would
- * make for these sizes, without making it; out_dtype is the output's type.  The
+ * make for these sizes, without making it; out_dtype is the output's type.  (A
+ * residual or addend may take the room of some of the ring's stages.)  The
  * plan's kernel is a linear_kernel_t.  Needs a current CUDA device.
  * GEMM_ERR_ARG for sizes below 1, an unknown op or dtype or a NULL plan;
  * GEMM_ERR_UNSUPPORTED as the products.

@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 constexpr int kInstances = 7;
 
 // K blocks of a tile whose epilogue outlasts its products.
-constexpr int kShortSum = 8;
+constexpr int kShortSum = 10;
 // fp32 outputs: K blocks of one accumulation, 1024 rows.
 constexpr int kPairChunk = 16;
 
@@ -716,11 +716,11 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.b_whole = p.N - (64 * p.b_chunks - 1);
     p.idesc = product_instruction(256, bn, L.bf16, L.a_mn, L.b_mn);
     // Four boxes an epilogue warp where a tile's products are over before an epilogue
-    // that moves two tensors a box or fp32, two elsewhere, and as many stages as there
-    // is room for beside them.  (Sums of 8 into 5696 x 4416 fp32 with an addend: 37.8
-    // us, with two boxes 45.3; where only an output leaves, three stages for five cost
-    // more than boxes gain.)
-    const bool moves = EPI == EPI_F32 || (EPI == EPI_GRAD && L.R.p) || (EPI == EPI_LINEAR && L.P.p && L.act != LINEAR_ACT_NONE);
+    // that moves two tensors a box or adds to fp32, two elsewhere, and as many stages as
+    // there is room for beside them.  (Sums of 512 added to 8192^2 fp32: 108 us, with two
+    // boxes 122.  Where only outputs leave, three stages for five cost more than boxes
+    // gain: the same without an addend 80 us, with two boxes 68.)
+    const bool moves = (EPI == EPI_F32 || EPI == EPI_GRAD) && L.R.p;
     p.slots = moves && p.k_blocks <= kShortSum ? 4 : 2;
     const int stage = P_TILE_BYTES + (L.b_mn ? 64 * p.b_chunks : bn / 2) * PK * 2;
     const int room = kProductSmem - 1024 - 8 * p.slots * BOX - static_cast<int>(sizeof(PairCtl));
