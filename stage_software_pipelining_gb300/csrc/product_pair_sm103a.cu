@@ -48,7 +48,7 @@ struct PairMaps {
 };
 
 // t / d for t < 2^30 as t * by >> shift.  (A tile has a few such; the compiler's
-// divisions took 0.4 us of the 1.9 that a plain tile's epilogue takes.)
+// divisions took 0.3 us of the 1.9 that a plain tile's epilogue takes.)
 struct Divisor {
     uint32_t by;
     int shift;
