@@ -193,13 +193,15 @@ int linear_plan(int op, int64_t M, int64_t N, int64_t K, int out_dtype, quant_pl
  * X, A and b A + c A^2 are held in fp16 between the products, at power-of-two
  * scales that put their elements in fp16's range; the products are summed and
  * combined in fp32.  That is 2^-11 a rounding, an eighth of what bf16 would
- * lose: a gradient of full rank comes out within 3e-3 of its norm, before the
- * output's own rounding.  Directions whose singular value is below some
+ * lose: in five steps a gradient of full rank comes out within 2e-3 of its norm
+ * where its shorter side is 100 or more, 4e-3 from 9 on and 1e-2 below (a step makes
+ * an error beside a singular value of 1.2 four times as large; many of them average),
+ * before the output's own rounding.  Directions whose singular value is below some
  * 1e-4 |G| are lost in the roundings, as is a G that is small beside eps.  The
  * scales hold for coefficients that keep X's singular values below 1.9 and those of
- * b A + c A^2 below 3.9; others may overflow to infinity.  A NaN or an infinity in a matrix makes its output
- * NaN; a matrix of zeros gives zeros (with eps = 0: NaN).  Elements of every
- * finite magnitude are taken.  rows and cols above 32768 are
+ * b A + c A^2 below 3.9; others may overflow to infinity.  A NaN or an infinity in a
+ * matrix makes its output NaN; a matrix of zeros gives zeros (with eps = 0: NaN).
+ * Elements of every finite magnitude are taken.  rows and cols above 32768 are
  * GEMM_ERR_UNSUPPORTED, as is a batch above 65535.  The strides between
  * matrices are multiples of 16 bytes (not looked at for a single matrix).
  */
