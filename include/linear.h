@@ -39,7 +39,8 @@
  *
  * Alignment (GEMM_ERR_ALIGN otherwise): matrices start on 16-byte boundaries
  * and their leading dimensions are multiples of 16 bytes, act_grad's excepted;
- * vectors are aligned to their element.
+ * vectors are aligned to their element.  Rows that start on 128-byte lines are the
+ * fast case of the products.
  */
 #ifndef SSP_LINEAR_H
 #define SSP_LINEAR_H
