@@ -57,7 +57,7 @@ extern "C" {
 
 /*
  * Activations and their derivatives.  At infinities both are their limits
- * (those of -infinity are 0, to within 1e-17), and a NaN gives a NaN, but relu's
+ * (those of -infinity are 0, to within 3e-17), and a NaN gives a NaN, but relu's
  * derivative, which is 1 there.  relu'(0) = 0.
  */
 typedef enum {

@@ -1,0 +1,68 @@
+"""The training operators at their limits: the derivatives' tails."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import linear_reference as R
+from stage_software_pipelining_gb300 import build as gemm_build
+from stage_software_pipelining_gb300 import linear as L
+from stage_software_pipelining_gb300 import quant as Q
+
+pytestmark = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib(gpu):
+    gemm_build.build()
+    return L.load_library()
+
+
+# ---------------------------------------------------------------- gelu' below zero
+# gelu'(z) = Phi(z) + z phi(z) of its own size, -9 <= z <= -4.  phi's exponent z^2 / 2 log2(e)
+# is below 58.5 and rounded twice (its factor and itself): 58.5 ln 2 2 2^-24 = 4.9e-6 of phi
+# and of the tail alike.  exp2 itself, z times 1 / sqrt(2 pi) and the sum: 2^-22 + 3 2^-24 =
+# 4.2e-7.  The tail is at most 0.06 of the other term; its fit (9e-7), reciprocal and
+# polynomial (16 2^-24) add 0.06 * 1.9e-6 = 1.2e-7.  |Phi| + |z phi| is at most 1.13 |gelu'|:
+# 1.13 * 5.5e-6 = 6.2e-6 < 2^-17.
+TAIL_REL = 2.0 ** -17
+
+
+def tail(dtype):
+    """Every value of dtype from -9 to -4, and gelu' there in 64 bits."""
+    first, last = (torch.tensor(v, dtype=dtype).view(torch.int16).item() for v in (-4.0, -9.0))
+    z = torch.arange(first, last + 1, dtype=torch.int16).view(dtype)
+    assert z[0] == -4 and z[-1] == -9
+    v = z.double()
+    return z, 0.5 * torch.special.erfc(v * -math.sqrt(0.5)) + v * torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gelu_derivative_keeps_its_tail(dtype):
+    z, ref = tail(dtype)
+    one = torch.ones(1, z.numel(), dtype=dtype, device="cuda")
+    db = torch.empty(z.numel(), device="cuda")
+    L.act_grad(one, pre=z[None].cuda(), act="gelu", dbias=db)
+    off = ((db.cpu().double() - ref) / ref).abs()
+    assert off.max() <= TAIL_REL, (float(off.max()), float(z[off.argmax()]))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M", [1, 600])
+def test_gelu_derivative_keeps_its_tail_in_16_bits(M, dtype):
+    """Times 2^10, by act_grad and by linear_dx on either kernel."""
+    z, ref = tail(dtype)
+    n = z.numel()
+    up, pre = Q.empty_rows(M, n, dtype), Q.empty_rows(M, n, dtype)
+    up.fill_(1024.0)
+    pre.copy_(z.expand(M, n))
+    ref = np.broadcast_to(1024.0 * ref.numpy(), (M, n))
+    dz, dx = Q.empty_rows(M, n, dtype), Q.empty_rows(M, n, dtype)
+    L.act_grad(up, dz, pre=pre, act="gelu")
+    R.check_rounded(dz, ref, TAIL_REL, 0.0, "act_grad")
+    W = Q.empty_rows(64, n, dtype)
+    W.zero_()
+    L.linear_dx(torch.zeros(M, 64, dtype=dtype, device="cuda"), W, dx, residual=up, act="gelu", pre=pre, checked=True)
+    R.check_rounded(dx, ref, TAIL_REL, 0.0, "linear_dx")
