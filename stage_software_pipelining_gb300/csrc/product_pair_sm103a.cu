@@ -67,6 +67,7 @@ struct PairParams {
     int bn;        // tile width
     int tiles_m, tiles_n, tiles, k_blocks, batch;
     int k_chunks;  // accumulations of a tile, summed by the epilogue (EPI_F32)
+    int chunk_blocks, chunk_rest;  // K blocks over accumulations: quotient and remainder
     int group_m;   // tile rows walked together
     Divisor by_tiles, by_group;            // tiles; those of a group
     Divisor by_rows, by_last_rows;         // a group's tile rows; the last group's
@@ -185,9 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 4);
     volatile int* abort_flag = &ctl->abort;
-    // First K block of a tile's accumulation c.
     const int chunks = EPI == EPI_F32 ? p.k_chunks : 1;
-    auto chunk_begin = [&](int c) { return EPI == EPI_F32 ? p.k_blocks * c / p.k_chunks : c * p.k_blocks; };
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.A);
@@ -594,6 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return __all_sync(0xffffffffu, r) != 0;
                 };
                 for (int t = unit; ok && t < tiles; t += units) {
+                    int kb = 0, over_c = 0;  // K blocks c / chunks, rounded down, and what is over
                     for (int c = 0; ok && c < chunks; ++c, ++lt) {
                         const int acc = lt & 1;
                         if (!mma_wait(tempty_bar(acc), static_cast<uint32_t>((lt >> 1) & 1) ^ 1u)) {
@@ -602,8 +602,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         tc_fence_after();
                         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-                        const int kb0 = chunk_begin(c), kb1 = chunk_begin(c + 1);
-                        for (int kb = kb0; kb < kb1; ++kb) {
+                        const int kb0 = kb;
+                        int kb1 = p.k_blocks;
+                        if constexpr (EPI == EPI_F32) {
+                            kb1 = kb0 + p.chunk_blocks;
+                            over_c += p.chunk_rest;
+                            if (over_c >= chunks) {
+                                over_c -= chunks;
+                                ++kb1;
+                            }
+                        }
+                        for (; kb < kb1; ++kb) {
                             if (!mma_wait(full_bar(s), ph)) {
                                 ok = false;
                                 break;
@@ -700,7 +709,8 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.batch = static_cast<int>(L.batch);
     p.k_blocks = static_cast<int>((L.K + PK - 1) / PK);
     p.k_chunks = EPI == EPI_F32 ? (p.k_blocks + kPairChunk - 1) / kPairChunk : 1;
-    if (static_cast<int64_t>(p.k_blocks) * p.k_chunks > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
+    p.chunk_blocks = p.k_blocks / p.k_chunks;
+    p.chunk_rest = p.k_blocks % p.k_chunks;
     // Tile rows walked together: about 32 MB of A, so that the panel stays in
     // L2 while the group walks its columns.
     const int64_t g = (32ll << 20) / (512 * L.K);

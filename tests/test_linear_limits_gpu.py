@@ -1,4 +1,5 @@
-"""The training operators at their limits: the derivatives' tails."""
+"""The training operators at their limits: the derivatives' tails, and the longest
+sums."""
 import math
 
 import numpy as np
@@ -7,6 +8,7 @@ import torch
 
 import linear_reference as R
 from stage_software_pipelining_gb300 import build as gemm_build
+from stage_software_pipelining_gb300 import gemm as G
 from stage_software_pipelining_gb300 import linear as L
 from stage_software_pipelining_gb300 import quant as Q
 
@@ -66,3 +68,32 @@ def test_gelu_derivative_keeps_its_tail_in_16_bits(M, dtype):
     W.zero_()
     L.linear_dx(torch.zeros(M, 64, dtype=dtype, device="cuda"), W, dx, residual=up, act="gelu", pre=pre, checked=True)
     R.check_rounded(dx, ref, TAIL_REL, 0.0, "linear_dx")
+
+
+# ---------------------------------------------------------------- the longest fp32 weight gradients
+def zeros_and_ones(seed, rows, cols, dtype):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(0, 2, (rows, cols), generator=g, device="cuda", dtype=torch.int8).to(dtype)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(262145, 128, 128, F16), (300001, 40, 264, BF16), (1048577, 24, 8, F16),
+                                         (12000001, 24, 40, BF16), (16000000, 8, 16, F16)])
+def test_linear_dw_of_many_rows(M, N, K, dtype):
+    """Sums of zeros and ones below 2^24 are exact in fp32, whatever their order."""
+    dz, x = zeros_and_ones(1, M, N, dtype), zeros_and_ones(2, M, K, dtype)
+    dw = torch.full((N, K), 3.0, device="cuda")
+    L.linear_dw(dz, x, dw, addend=dw, checked=True)
+    ref = torch.full((N, K), 3.0, dtype=torch.float64, device="cuda")
+    for at in range(0, M, 1 << 20):
+        ref += dz[at:at + (1 << 20)].double().t() @ x[at:at + (1 << 20)].double()
+    assert torch.equal(dw.double(), ref)
+
+
+@pytest.mark.parametrize("M", [11863232, 11863233, 100000000, 2 ** 31 - 4097])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_any_number_of_rows_has_a_plan(M, out):
+    """The header's limit is the only one: sizes up to 2^31 - 4097."""
+    assert L.linear_plan("dw", M, 64, 64, out)["grid"] > 0
+    with pytest.raises(G.GemmError) as e:
+        L.linear_plan("dw", 2 ** 31 - 4096, 64, 64, out)
+    assert e.value.status == G.GEMM_ERR_UNSUPPORTED
