@@ -1,6 +1,7 @@
-"""The training operators at their limits: the derivatives' tails, and the longest
-sums."""
+"""The training operators at their limits: the derivatives' tails, the longest sums,
+and waits that run out."""
 import math
+import time
 
 import numpy as np
 import pytest
@@ -97,3 +98,32 @@ def test_any_number_of_rows_has_a_plan(M, out):
     with pytest.raises(G.GemmError) as e:
         L.linear_plan("dw", 2 ** 31 - 4096, 64, 64, out)
     assert e.value.status == G.GEMM_ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------- waits that run out
+def late(rows, cols, step, limit_ms=50, steps=5, batch=()):
+    """orthogonalize with the copy or commit number `step` of its first CTA left out:
+    the status, and how long the call took."""
+    g = torch.randn(*batch, rows, cols, generator=torch.Generator().manual_seed(6)).cuda()
+    out = torch.empty(*batch, rows, cols, dtype=BF16, device="cuda")
+    ws = torch.empty(L.orthogonalize_workspace(g), dtype=torch.uint8, device="cuda")
+    L.orthogonalize(g, out, ws, steps=steps, checked=True)      # the kernels' one-time settings
+    right = out.clone()
+    try:
+        G.debug_set(wait_limit_ns=limit_ms * 1000000, withhold_arrive=step)
+        began = time.perf_counter()
+        with pytest.raises(G.GemmError) as e:
+            L.orthogonalize(g, out, ws, steps=steps, checked=True)
+        took = time.perf_counter() - began
+    finally:
+        G.debug_set()
+    L.orthogonalize(g, out, ws, steps=steps, checked=True)
+    assert torch.equal(out, right)      # the next call is as the one before
+    return e.value.status, took
+
+
+@pytest.mark.parametrize("rows,cols,batch", [(304, 400, ()), (400, 304, (2,))])
+@pytest.mark.parametrize("step", [0, 3])
+def test_products_of_orthogonalize_say_that_they_ran_out(rows, cols, batch, step):
+    """Withheld: a stage of every product."""
+    assert late(rows, cols, step, batch=batch)[0] == G.GEMM_ERR_TIMEOUT
