@@ -214,7 +214,11 @@ int orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void* g, int6
                   int out_dtype, int steps, const float* coefficients, float eps, float scale,
                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* orthogonalize_checked -- orthogonalize as linear_checked is linear. */
+/*
+ * orthogonalize_checked -- orthogonalize as linear_checked is linear.  (Matrices with a
+ * side of 128 at most may take one launch, in which gemm_debug_set's withhold_arrive is
+ * the number of the product, three a step, whose end the first CTA is not told of.)
+ */
 int orthogonalize_checked(int64_t batch, int64_t rows, int64_t cols, const void* g, int64_t ldg,
                           int64_t stride_g, int dtype, void* out, int64_t ldo, int64_t stride_o,
                           int out_dtype, int steps, const float* coefficients, float eps,

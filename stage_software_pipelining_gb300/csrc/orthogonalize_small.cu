@@ -54,10 +54,12 @@ struct Params {
     long long ldo, stride_o;
     int out_bf16;
     unsigned long long wait_limit_ns;
+    int withhold;
 };
 
 struct Ctl {
-    unsigned long long bar;
+    unsigned long long bar, drain;
+    int failed;       // a wait ran out
     double sum;       // of squares, this CTA's slice
     uint32_t tmem_base;
     float factors[3];
@@ -104,6 +106,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
 
     if (tid == 0) {
         mbar_init(bar, 1);
+        mbar_init(smem_addr(&ctl->drain), 1);
+        ctl->failed = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -185,19 +189,33 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
     fence_proxy_async_shared();
     __syncthreads();
 
+    // A wait that runs out ends this CTA's products and waits; it still takes part in
+    // the barriers, and leaves when the products on their way have landed.  (Its threads
+    // learn of it in their waits: a look at the flag beside each takes 0.06 us.)
+    volatile int* failed = &ctl->failed;
+    const int withhold = rank == 0 && b == 0 ? p.withhold : -1;
     uint32_t phase = 0;
+    bool ok = true;
     // Waits until the products issued before the last commit are done.
     auto products_done = [&]() {
-        if (!mbar_try_wait(bar, phase)) {
+        if (ok && !mbar_try_wait(bar, phase)) {
             const unsigned long long t0 = globaltimer_ns();
-            while (!mbar_try_wait(bar, phase))
-                if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+            while (ok && !mbar_try_wait(bar, phase)) {
+                if (*failed) {
+                    ok = false;
+                } else if (globaltimer_ns() - t0 > p.wait_limit_ns) {
                     record_product_timeout(&g_ortho_small_status, P_EPILOGUE, 0);
-                    break;
+                    *failed = 1;
+                    ok = false;
                 }
+            }
         }
         phase ^= 1u;
         tc_fence_after();
+    };
+    // The thread that issues the products: the commit of number n (three a step).
+    auto commit = [&](int n) {
+        if (n != withhold) umma_commit(bar);
     };
     const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32q.., and which blocks of 64 columns
     const int i = 32 * q + lane;               // this thread's row
@@ -211,13 +229,13 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
     for (int step = 0; step < p.steps; ++step) {
         const bool first = step == 0, last = step + 1 == p.steps;
         // ---- A = X X^T
-        if (warp == 0 && elect_one_sync()) {
+        if (warp == 0 && elect_one_sync() && ok) {
             const uint64_t d = operand_desc(X, 0);
             for (int k = 0; k < p.w / 16; ++k) {
                 const uint64_t at = d + static_cast<uint32_t>(k / 4 * (BLOCK / 16) + k % 4 * 2);
                 umma_f16(tmem, at, at, p.idesc_a, k != 0);
             }
-            umma_commit(bar);
+            commit(3 * step);
         }
         __syncwarp();
         products_done();
@@ -274,14 +292,14 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
         __syncthreads();
         tc_fence_after();
         // ---- B = b A + c A^2
-        if (warp == 0 && elect_one_sync()) {
+        if (warp == 0 && elect_one_sync() && ok) {
             const uint64_t d = operand_desc(A, 0);
 #pragma unroll
             for (int k = 0; k < SIDE / 16; ++k) {
                 const uint64_t at = d + static_cast<uint32_t>(k / 4 * (BLOCK / 16) + k % 4 * 2);
                 umma_f16(tmem, at, at, p.idesc_a, k != 0);
             }
-            umma_commit(bar);
+            commit(3 * step + 1);
         }
         __syncwarp();
         products_done();
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
         __syncthreads();
         tc_fence_after();
         // ---- X = a X + B X
-        if (warp == 0 && elect_one_sync()) {
+        if (warp == 0 && elect_one_sync() && ok) {
             const uint64_t db = operand_desc(B, 0);
             // X as an MN-major operand: blocks of 64 columns are BLOCK bytes apart.
             const uint64_t dx = (operand_desc(X, 1) & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(BLOCK / 16) << 16);
@@ -322,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
                     umma_f16(tmem + static_cast<uint32_t>(c), db + static_cast<uint32_t>(k / 4 * (BLOCK / 16) + k % 4 * 2),
                              dx + static_cast<uint32_t>(c / 64 * (BLOCK / 16) + k * (2048 / 16)), idesc, k != 0);
             }
-            umma_commit(bar);
+            commit(3 * step + 2);
         }
         __syncwarp();
         products_done();
@@ -384,6 +402,15 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_small_kernel(const Params p)
         __syncthreads();
         tc_fence_after();
     }
+    if (*failed) {  // (set before the last barrier)
+        if (warp == 0) {
+            const uint32_t drain = smem_addr(&ctl->drain);
+            if (elect_one_sync()) umma_commit(drain);
+            __syncwarp();
+            drain_wait(drain, 0u, p.wait_limit_ns);
+        }
+        __syncthreads();
+    }
     if (split > 1) cluster_sync_all();  // no CTA leaves while another reads its shared memory
     if (warp == 1) tmem_dealloc(tmem, 512u);
 }
@@ -437,7 +464,9 @@ int ortho_small_launch(const OrthoLaunch& L, cudaStream_t stream) {
     p.ldo = L.ldo;
     p.stride_o = L.stride_o;
     p.out_bf16 = L.out_bf16;
-    p.wait_limit_ns = static_cast<unsigned long long>(debug_hooks().wait_limit_ns);
+    const DebugHooks d = debug_hooks();
+    p.wait_limit_ns = static_cast<unsigned long long>(d.wait_limit_ns);
+    p.withhold = d.withhold_arrive;
     // The slice's width with the least time: rounds of clusters that run at once, each
     // the steps' latency, the slice's work and, in a cluster, the exchange.  (us;
     // measured: 128 x 128 in one CTA 24, 128 x 1024 in eight of 128 columns 48, in four

@@ -127,3 +127,13 @@ def late(rows, cols, step, limit_ms=50, steps=5, batch=()):
 def test_products_of_orthogonalize_say_that_they_ran_out(rows, cols, batch, step):
     """Withheld: a stage of every product."""
     assert late(rows, cols, step, batch=batch)[0] == G.GEMM_ERR_TIMEOUT
+
+
+@pytest.mark.parametrize("rows,cols,batch", [(104, 304, ()), (304, 64, (3,)), (120, 2048, ()), (2560, 128, ()),
+                                             (128, 1024, (2,))])
+@pytest.mark.parametrize("step", [0, 1, 2, 7, 149])
+def test_orthogonalize_in_one_launch_says_that_it_ran_out(rows, cols, batch, step):
+    """Withheld: the end of one product of 150, in one CTA and in clusters.  The call ends
+    within some limits, not one for each of the waits that are left."""
+    status, took = late(rows, cols, step, steps=50, batch=batch)
+    assert status == G.GEMM_ERR_TIMEOUT and took < 0.5
