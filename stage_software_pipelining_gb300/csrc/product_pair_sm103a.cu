@@ -1,14 +1,14 @@
 // product_pair_sm103a.cu -- the products of a 16-bit linear layer for many rows:
-// D = epilogue(A B) in tiles of 256 rows by 128 to 256 columns on CTA pairs
+// D = epilogue(A B) in tiles of 256 rows by 192 to 256 columns on CTA pairs
 // (tcgen05, cta_group::2).
 //
 // Persistent; two accumulators in tensor memory, so that a tile's epilogue runs
 // under the next tile's mainloop.  Bound by the tensor pipe.  Either operand may
 // be K-major or MN-major (product.cuh), so none is ever transposed in memory.
 //
-// Tiles are as wide as lets the pairs end together (pair_width): 4096^3 is 256
-// tiles of 256 columns, four rounds of the 76 pairs with the last a third full, or
-// 304 tiles of 224, four full rounds of less work.
+// Tiles are 192, 224 or 256 columns wide, as lets the pairs end together (choose, in
+// product_few_sm103a.cu): 4096^3 is 256 tiles of 256 columns, four rounds of the 76
+// pairs with the last a third full, or 304 tiles of 224, four full rounds of less work.
 //
 // An epilogue warp takes its 32 rows in boxes of 128-byte rows: 64 columns of 16
 // bits, 32 of fp32.  Its inputs (a residual, a gradient, the z of an activation)
@@ -43,7 +43,7 @@ constexpr int THREADS = 32 * (FIRST + 8);
 struct PairMaps {
     CUtensorMap A, A_edge, B, B_edge;
     CUtensorMap D, R, P;           // boxes of 128-byte rows
-    CUtensorMap D32, R32, P32;     // of 32 columns: the last box of a tile of 160 or 224
+    CUtensorMap D32, R32, P32;     // of 32 columns: the last box of a tile of 224
     CUtensorMap mirror;            // the box a symmetric result's box is mirrored into
 };
 
@@ -332,8 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 if (!inputs && lane == 0 && count >= static_cast<uint32_t>(depth)) {
-                    if (depth == 4) bulk_wait_group_read<3>();
-                    else if (depth == 2) bulk_wait_group_read<1>();
+                    if (depth == 2) bulk_wait_group_read<1>();  // (four slots are taken for inputs alone)
                     else bulk_wait_group_read<0>();
                 }
                 __syncwarp();
