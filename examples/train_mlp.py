@@ -120,6 +120,9 @@ def main(argv=None) -> dict:
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--rate", type=float, default=0.01)
     a = ap.parse_args(argv)
+    for name in ("dim", "hidden", "layers", "tokens", "steps"):
+        if getattr(a, name) < 1:
+            ap.error(f"--{name} must be at least 1")
     net = Mlp(a.dim, a.hidden, a.layers, a.tokens)
     x = torch.randn(a.tokens, a.dim, device="cuda").to(DTYPE)
     target = torch.roll(x, 1, dims=1)
@@ -132,7 +135,7 @@ def main(argv=None) -> dict:
         graph.replay()
         losses.append(net.loss.clone())
     torch.cuda.synchronize()
-    ms = (time.perf_counter() - began) / max(1, a.steps) * 1e3
+    ms = (time.perf_counter() - began) / a.steps * 1e3
     result = {"first": float(losses[0]), "last": float(losses[-1]), "ms": ms}
     print(f"{a.layers} layers of {a.dim} x {a.hidden}, {a.tokens} tokens: loss {result['first']:.4f} -> "
           f"{result['last']:.4f} in {a.steps} steps of {ms:.3f} ms")
