@@ -135,12 +135,10 @@ int linear_dx(int64_t M, int64_t N, int64_t K, const void* dz, int64_t lddz, con
  *   dW        N x K of out_dtype: QUANT_F32 or `dtype`; lddw >= K
  *   addend    N x K of out_dtype, ldc >= K, or NULL; may be dW itself (same
  *             leading dimension)
- * With an fp32 dW, no accumulator sums more than 4096 rows: the tensor cores
- * truncate, which over 32768 rows would lose 4e-5 of a sum.  (A 16-bit dW is
- * summed by one accumulator and does lose it: half an fp16 step at 400000 rows.)
- * An fp32 dW of few outputs is slow above 262144 rows, where no sum is cut any more:
- * 128 x 128 takes 117 us over 262144 rows and 1240 over 262208.  Such rows are better
- * given in parts, each call's addend the dW of the one before.
+ * With an fp32 dW, no accumulator of the tensor cores, which truncate as they add, sums
+ * more than 512 rows: a dW of any number of rows is about as good as by fp32 sums.  (A
+ * 16-bit dW is summed by one accumulator, which loses up to 6e-9 of the sum of
+ * magnitudes a row: half an fp16 step at 80000 rows of equal signs.)
  * M = 0 gives the addend (or 0).
  */
 int linear_dw(int64_t M, int64_t N, int64_t K, const void* dz, int64_t lddz, const void* x,

@@ -8,6 +8,10 @@
 // distributed shared memory and are added in rank order, so that a narrow product
 // or a long sum still keeps every SM loading.  Bound by reading the operands.
 //
+// Sums of more than 512 rows a CTA for an fp32 result (product_few_kernel<MT, true>) are
+// made in two accumulators in turn, which the epilogue's warps add up in registers under
+// the products (kProductChunk), so they may be as long as they like.
+//
 // Every wait is bounded as in product_pair_sm103a.cu.
 #include <mutex>
 
@@ -21,7 +25,9 @@ __device__ GemmDeviceStatus g_product_few_status;
 namespace {
 
 constexpr int FIRST = 4;  // first epilogue warp, after the weights' copies, MMA, the rows' copies and none
-constexpr int THREADS = 32 * (FIRST + 4);
+// Warps.  Those that add up the accumulations keep 64 sums a thread at most.
+template <int MT, bool SUMS>
+constexpr int kWarps = FIRST + (SUMS ? (MT == 256 ? 16 : 8) : 4);
 constexpr int kMaxStages = 12;
 constexpr int kTwo = 64;   // widest MT of which two CTAs fit an SM
 constexpr int kPush = 32;  // widest MT with room of its own for the cluster's partials
@@ -35,7 +41,6 @@ struct FewParams {
     int tiles_m, tiles_n, k_blocks;
     int split;       // CTAs of a cluster, each with a part of K
     int stages;
-    int acc_blocks;  // K blocks that one accumulator sums
     uint32_t tmem_cols;
     int f_mn, t_mn;  // the weights' side (columns of the result) and the rows'
     int f_whole, t_whole;  // columns and rows below which a stage's chunks come by one copy
@@ -52,7 +57,7 @@ struct FewParams {
 };
 
 struct FewCtl {
-    unsigned long long bar[2 * kMaxStages + 1];  // full, empty, done
+    unsigned long long bar[2 * kMaxStages + 5];  // full, empty, done; accumulators full and empty
     uint32_t tmem_base;
     int abort;
     alignas(16) float bias[128];  // of the tile's columns
@@ -106,11 +111,12 @@ __device__ __forceinline__ void unpack_eight(bool bf16, uint4 u, Pair (&f)[4]) {
 // shared-memory address of the columns'.  Both its callers call it in a loop that
 // is not unrolled: its code is long, runs once a CTA, and eight copies of it took
 // 8 us to be read and run for 64 rows, one takes 2.
+template <bool SUMS>
 __device__ __forceinline__ void finish_eight(const FewParams& p, int b, int row, int n, Pair (&v)[4], uint32_t bias,
                                              float alpha, float beta) {
     const int left = p.N - n;
     if (left <= 0) return;
-    if (p.epi == EPI_F32) {
+    if (SUMS || p.epi == EPI_F32) {
         float* d = static_cast<float*>(const_cast<void*>(p.D.p)) + place(p.D, b, row, n);
         const float* r = p.R.p ? static_cast<const float*>(p.R.p) + place(p.R, b, row, n) : nullptr;
 #pragma unroll
@@ -168,10 +174,12 @@ __device__ __forceinline__ void finish_eight(const FewParams& p, int b, int row,
     store_eight(bf16, p.D.p, place(p.D, b, row, n), left, v);
 }
 
-// One 128 (columns) x MT (rows) tile, a part of its K blocks.
-template <int MT>
-__global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
+// One 128 (columns) x MT (rows) tile, a part of its K blocks.  SUMS: fp32 results, two
+// accumulators of kProductChunk blocks at most in turn.
+template <int MT, bool SUMS>
+__global__ void __launch_bounds__(32 * kWarps<MT, SUMS>, MT <= kTwo ? 2 : 1)
     product_few_kernel(const __grid_constant__ FewMaps maps, const FewParams p) {
+    constexpr int WARPS = kWarps<MT, SUMS>, THREADS = 32 * WARPS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -206,6 +214,8 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
     const uint32_t done_bar = bar0 + 8u * (2 * S);
+    auto acc_full = [&](int a) { return bar0 + 8u * (2 * S + 1 + a); };
+    auto acc_empty = [&](int a) { return bar0 + 8u * (2 * S + 3 + a); };
     volatile int* abort_flag = &ctl->abort;
 
     if (threadIdx.x == 0) {
@@ -218,6 +228,10 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(done_bar, 1);
+        for (int a = 0; SUMS && a < 2; ++a) {
+            mbar_init(acc_full(a), 1);
+            mbar_init(acc_empty(a), WARPS - FIRST);
+        }
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -232,6 +246,12 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
     const uint32_t tmem_base = ctl->tmem_base;
     griddep_wait();
     if (!LATE) griddep_launch_dependents();
+
+    // SUMS: a warp of the epilogue has a quarter of the columns, a thread each, and ROWS of
+    // the rows.
+    constexpr int ROWS = SUMS ? MT / ((WARPS - FIRST) / 4) : 16;
+    const int row0 = SUMS ? (warp - FIRST) / 4 * ROWS : 0;
+    float kept[ROWS] = {};
 
     int it = 0;  // the copying threads: stages issued
     if (warp == 0 || warp == 2) {
@@ -278,31 +298,43 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
         const uint32_t f_step = operand_step(p.f_mn), t_step = operand_step(p.t_mn);
         int s = 0;
         uint32_t ph = 0;
-        uint32_t d_tmem = tmem_base;
-        int in_acc = 0;  // blocks in the present accumulator
-        for (int kb = k0; kb < k1; ++kb) {
-            const bool r = product_wait<false>(full_bar(s), ph, abort_flag, p.wait_limit_ns, &g_product_few_status,
-                                               P_MMA, kb - k0);
-            if (!__all_sync(0xffffffffu, r)) break;
-            tc_fence_after();
-            if (in_acc == p.acc_blocks) {
-                in_acc = 0;
-                d_tmem += MT;
+        auto mma_wait = [&](uint32_t bar, uint32_t parity, int kb) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            const bool r = product_wait<false>(bar, parity, abort_flag, p.wait_limit_ns, &g_product_few_status, P_MMA,
+                                               kb - k0);
+            return __all_sync(0xffffffffu, r) != 0;
+        };
+        bool ok = true;
+        for (int kb = k0, c = 0; ok && kb < k1; ++c) {  // accumulations
+            const int kb0 = kb, kb1 = SUMS ? min(k1, kb + kProductChunk) : k1;
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(SUMS ? (c & 1) * MT : 0);
+            if constexpr (SUMS) {
+                ok = mma_wait(acc_empty(c & 1), static_cast<uint32_t>((c >> 1) & 1) ^ 1u, kb);
+                if (!ok) break;
+                tc_fence_after();
             }
-            const uint32_t f_off = static_cast<uint32_t>(s * P_TILE_BYTES) / 16u;
-            const uint32_t t_off = static_cast<uint32_t>(s * T_BYTES) / 16u;
-            if (elect_one_sync()) {
+            for (; kb < kb1; ++kb) {
+                ok = mma_wait(full_bar(s), ph, kb);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t f_off = static_cast<uint32_t>(s * P_TILE_BYTES) / 16u;
+                const uint32_t t_off = static_cast<uint32_t>(s * T_BYTES) / 16u;
+                if (elect_one_sync()) {
 #pragma unroll
-                for (int kk = 0; kk < PK / PUMMA_K; ++kk)
-                    umma_f16(d_tmem, f_desc0 + (f_off + f_step * kk), t_desc0 + (t_off + t_step * kk), p.idesc,
-                             in_acc != 0 || kk != 0);
-                umma_commit(empty_bar(s));
+                    for (int kk = 0; kk < PK / PUMMA_K; ++kk)
+                        umma_f16(d_tmem, f_desc0 + (f_off + f_step * kk), t_desc0 + (t_off + t_step * kk), p.idesc,
+                                 kb != kb0 || kk != 0);
+                    umma_commit(empty_bar(s));
+                }
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
-            __syncwarp();
-            ++in_acc;
-            if (++s == S) {
-                s = 0;
-                ph ^= 1u;
+            if constexpr (SUMS) {
+                if (ok && elect_one_sync()) umma_commit(acc_full(c & 1));
+                __syncwarp();
             }
         }
         // Also after an abort: every MMA this warp issued finishes here.
@@ -312,17 +344,38 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
         tc_fence_after();
         tc_fence_before();
     } else if (warp >= FIRST) {
-        const int et = static_cast<int>(threadIdx.x) - 32 * FIRST;  // 0..127
-        ctl->bias[et] = p.bias && n0 + et < p.N ? load16(p.bf16 != 0, p.bias, n0 + et) : 0.0f;
+        const int et = static_cast<int>(threadIdx.x) - 32 * FIRST;  // 0..127, more for SUMS
+        if (!SUMS) ctl->bias[et] = p.bias && n0 + et < p.N ? load16(p.bf16 != 0, p.bias, n0 + et) : 0.0f;
         // What this CTA's epilogue will read comes closer meanwhile, a line a thread.
         if (p.R.p || p.epi == EPI_GRAD) {
             const int rows = min(MT, p.M - m0);
             const int own0 = PUSH ? 0 : rows * rank / split, own1 = PUSH ? rows : rows * (rank + 1) / split;
             const int size = p.epi == EPI_F32 ? 4 : 2, lines = size;  // 128 columns a row
-            for (int i = et; i < (own1 - own0) * lines; i += 128) {
+            for (int i = et; i < (own1 - own0) * lines; i += THREADS - 32 * FIRST) {
                 const int m = m0 + own0 + i / lines, n = min(n0 + i % lines * (128 / size), p.N - 1);
                 if (p.R.p) prefetch_l1(static_cast<const uint8_t*>(p.R.p) + place(p.R, b, m, n) * size);
                 if (p.epi == EPI_GRAD) prefetch_l1(static_cast<const uint8_t*>(p.P.p) + place(p.P, b, m, n) * size);
+            }
+        }
+        if constexpr (SUMS) {
+            const uint32_t mine = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + static_cast<uint32_t>(row0);
+            const int chunks = (k1 - k0 + kProductChunk - 1) / kProductChunk;
+            for (int c = 0; c < chunks; ++c) {
+                const bool w = product_wait<false>(acc_full(c & 1), static_cast<uint32_t>((c >> 1) & 1), abort_flag,
+                                                   p.wait_limit_ns, &g_product_few_status, P_EPILOGUE, c);
+                if (!__all_sync(0xffffffffu, w)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < ROWS; i += 16) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(mine + static_cast<uint32_t>((c & 1) * MT + i), r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) kept[i + e] += __uint_as_float(r[e]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty(c & 1));
             }
         }
     }
@@ -348,14 +401,11 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
             beta *= power_of(p.factor, b, p.beta_pow);
         }
     }
-    const int accs = (k1 - k0 + p.acc_blocks - 1) / p.acc_blocks;
     const int rows = min(MT, p.M - m0);
     const int most = (16 + split - 1) / split;  // groups of eight outputs of an owner
     auto first = [&](int r) { return (16 * r + split - 1) / split; };
     const uint32_t bias0 = smem_addr(ctl->bias);
     if (PUSH && split > 1) cluster_wait();  // every CTA has started
-    // All eight warps: two share a quarter of the accumulators' lanes and take turns at
-    // its rows, sixteen at a time.
     {
         const int q = warp & 3;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
@@ -365,22 +415,8 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
                                                       32u * static_cast<uint32_t>(rank * rows * most + (n >> 3) - first(owner)) +
                                                       4u * (n & 7)
                                                 : 0u;
-#pragma unroll 1
-        for (int c = 16 * (warp >> 2); c < rows; c += 32) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
-            tmem_ld_wait();
-            if (accs == 0) {  // K = 0
-#pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = 0u;
-            }
-            for (int a = 1; a < accs; ++a) {  // fp32 sums of long K, rounded to nearest
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(a * MT + c), o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(o[i]));
-            }
+        // Sixteen rows of the sums, from row c on.
+        auto deliver = [&](int c, const uint32_t (&r)[16]) {
             if (PUSH && split > 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -405,12 +441,37 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
                                  make_pair2(__uint_as_float(hi.x), __uint_as_float(hi.y)),
                                  make_pair2(__uint_as_float(hi.z), __uint_as_float(hi.w))};
                     const int d = 32 * q + 8 * (lane & 3);
-                    finish_eight(p, b, m0 + c + i, n0 + d, v, bias0 + 4u * d, alpha, beta);
+                    finish_eight<SUMS>(p, b, m0 + c + i, n0 + d, v, bias0 + 4u * d, alpha, beta);
                 }
                 __syncwarp();
             }
+        };
+        if constexpr (SUMS) {
+            if (warp >= FIRST) {
+#pragma unroll
+                for (int i = 0; i < ROWS; i += 16) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(kept[i + e]);
+                    if (row0 + i < rows) deliver(row0 + i, r);
+                }
+            }
+        } else {
+            // All eight warps: two share a quarter of the accumulator's lanes and take turns
+            // at its rows.
+#pragma unroll 1
+            for (int c = 16 * (warp >> 2); c < rows; c += 32) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(t_row + static_cast<uint32_t>(c), r);
+                tmem_ld_wait();
+                if (p.k_blocks == 0) {  // K = 0
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = 0u;
+                }
+                deliver(c, r);
+            }
+            tc_fence_before();
         }
-        tc_fence_before();
     }
     if (split > 1) {
         __syncwarp();
@@ -435,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, MT <= kTwo ? 2 : 1)
                 v[2] = add2(v[2], make_pair2(hi.x, hi.y));
                 v[3] = add2(v[3], make_pair2(hi.z, hi.w));
             }
-            finish_eight(p, b, m0 + m, n0 + 8 * d, v, bias0 + 32u * d, alpha, beta);
+            finish_eight<SUMS>(p, b, m0 + m, n0 + 8 * d, v, bias0 + 32u * d, alpha, beta);
         }
     }
     if (!PUSH && split > 1) cluster_sync_all();  // the peers have read this CTA's partials
@@ -460,7 +521,7 @@ bool allow_smem(const void* kernel, int slot) {
     return done[dev][slot];
 }
 
-template <int MT>
+template <int MT, bool SUMS>
 int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t stream) {
     if (MT < 64 && L.a_mn) return GEMM_ERR_UNSUPPORTED;  // an MN-major operand comes in chunks of 64
     FewParams p = {};
@@ -473,14 +534,8 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * L.batch;
     p.split = split;
     if (tiles * split > 0x7fffffff) return GEMM_ERR_UNSUPPORTED;
-    // Accumulators: as many of MT columns as the longest sum of an fp32 output
-    // asks for.
-    const int blocks = (p.k_blocks + split - 1) / split;
-    p.acc_blocks = L.epi == EPI_F32 ? kProductChunk : p.k_blocks > 0 ? p.k_blocks : 1;
-    const int accs = (blocks + p.acc_blocks - 1) / p.acc_blocks;
-    if (accs * MT > 512) return GEMM_ERR_UNSUPPORTED;
     p.tmem_cols = 32;
-    while (static_cast<int>(p.tmem_cols) < (accs > 0 ? accs : 1) * MT) p.tmem_cols *= 2;
+    while (static_cast<int>(p.tmem_cols) < (SUMS ? 2 : 1) * MT) p.tmem_cols *= 2;
     if (p.tmem_cols > 256) two = false;
     // Two CTAs an SM with half of shared memory each, or a ring as deep as one
     // CTA's room.
@@ -521,9 +576,9 @@ int launch(const ProductLaunch& L, int slot, int split, bool two, cudaStream_t s
     if (L.K > 0 && (!encode_operand(&maps.F, &maps.F_edge, L.B, L.b_mn, L.bf16, L.N, L.K, L.batch, 128) ||
                     !encode_operand(&maps.T, &maps.T_edge, L.A, L.a_mn, L.bf16, L.M, L.K, L.batch, MT)))
         return GEMM_ERR_LAUNCH;
-    auto kernel = product_few_kernel<MT>;
+    auto kernel = product_few_kernel<MT, SUMS>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), slot)) return GEMM_ERR_LAUNCH;
-    ProductConfig c(tiles * split, split, THREADS, smem, stream);
+    ProductConfig c(tiles * split, split, 32 * kWarps<MT, SUMS>, smem, stream);
     return product_finish(cudaLaunchKernelEx(&c.cfg, kernel, maps, p));
 }
 
@@ -544,6 +599,12 @@ struct Choice {
     int split = 1;
     bool two = false;  // two CTAs an SM
 };
+
+// Whether a K cut in `split` leaves a CTA more blocks than one accumulator sums.
+bool takes_sums(const ProductLaunch& L, int split) {
+    const int64_t kb = (L.K + PK - 1) / PK;
+    return L.epi == EPI_F32 && (kb + split - 1) / split > kProductChunk;
+}
 
 bool choose(const ProductLaunch& L, Choice* best) {
     // CTAs that run at once, one an SM or two.  (A cluster lies within a GPC: two CTAs
@@ -584,8 +645,7 @@ bool choose(const ProductLaunch& L, Choice* best) {
         const int64_t tiles = up(L.M, mt) * up(L.N, 128) * L.batch;
         for (int c = 1; c <= 8 && c <= kb; ++c) {
             if (resident[0][c] <= 0) continue;
-            const int64_t accs = L.epi == EPI_F32 ? up(up(kb, c), kProductChunk) : 1;
-            if (accs * mt > 512) continue;
+            const int64_t accs = takes_sums(L, c) ? 2 : 1;
             const int64_t ctas = tiles * c;
             if (ctas > 0x7fffffff) continue;
             const double rows = static_cast<double>(mt < L.M ? mt : L.M);
@@ -620,12 +680,12 @@ bool product_resident_ctas(int (&out)[9]) {
     static int n[64][9] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    const void* kernel = reinterpret_cast<const void*>(product_few_kernel<128>);
+    const void* kernel = reinterpret_cast<const void*>(product_few_kernel<128, false>);
     if (!allow_smem(kernel, 3)) return false;
     std::lock_guard<std::mutex> g(mu);
     if (!known[dev]) {
         for (int c = 1; c <= 8; ++c) {
-            ProductConfig cfg(c, c, THREADS, 200 * 1024, nullptr);
+            ProductConfig cfg(c, c, 32 * kWarps<128, false>, 200 * 1024, nullptr);
             cfg.cfg.attrs = &cfg.attr[1];  // the cluster alone
             cfg.cfg.numAttrs = 1;
             int k = 0;
@@ -643,12 +703,19 @@ bool product_resident_ctas(int (&out)[9]) {
 }
 
 int product_few_launch(const ProductLaunch& L, int mt, int split, bool two, cudaStream_t stream) {
+    if (takes_sums(L, split)) {  // (an fp32 result's tiles have 64 rows at least)
+        switch (mt) {
+            case 64: return launch<64, true>(L, 5, split, two, stream);
+            case 128: return launch<128, true>(L, 6, split, two, stream);
+            default: return launch<256, true>(L, 7, split, two, stream);
+        }
+    }
     switch (mt) {
-        case 16: return launch<16>(L, 0, split, two, stream);
-        case 32: return launch<32>(L, 1, split, two, stream);
-        case 64: return launch<64>(L, 2, split, two, stream);
-        case 128: return launch<128>(L, 3, split, two, stream);
-        default: return launch<256>(L, 4, split, two, stream);
+        case 16: return launch<16, false>(L, 0, split, two, stream);
+        case 32: return launch<32, false>(L, 1, split, two, stream);
+        case 64: return launch<64, false>(L, 2, split, two, stream);
+        case 128: return launch<128, false>(L, 3, split, two, stream);
+        default: return launch<256, false>(L, 4, split, two, stream);
     }
 }
 

@@ -661,8 +661,6 @@ constexpr int kInstances = 7;
 
 // K blocks of a tile whose epilogue outlasts its products.
 constexpr int kShortSum = 10;
-// fp32 outputs: K blocks of one accumulation, 1024 rows.
-constexpr int kPairChunk = 16;
 
 // The kernels' dynamic shared-memory limit is set once a device.
 bool allow_smem(const void* kernel, int slot) {
@@ -707,7 +705,7 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.tiles = static_cast<int>(tiles);
     p.batch = static_cast<int>(L.batch);
     p.k_blocks = static_cast<int>((L.K + PK - 1) / PK);
-    p.k_chunks = EPI == EPI_F32 ? (p.k_blocks + kPairChunk - 1) / kPairChunk : 1;
+    p.k_chunks = EPI == EPI_F32 ? (p.k_blocks + kProductChunk - 1) / kProductChunk : 1;
     p.chunk_blocks = p.k_blocks / p.k_chunks;
     p.chunk_rest = p.k_blocks % p.k_chunks;
     // Tile rows walked together: about 32 MB of A, so that the panel stays in

@@ -90,6 +90,34 @@ def test_linear_dw_of_many_rows(M, N, K, dtype):
     assert torch.equal(dw.double(), ref)
 
 
+@pytest.mark.parametrize("M,N,K,kernel,rows", [(17000, 40, 24, "few", 64), (40000, 300, 72, "few", None),
+                                               (9000, 1400, 300, "few", None), (600, 40, 40, "few", 64), (32768, 1024, 1024, "few", 256),
+                                               (262144, 128, 128, "few", 64), (300000, 128, 128, "few", 64),
+                                               (8192, 2304, 2048, "pair", 256)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_linear_dw_sums_512_rows_at_most_in_an_accumulator(M, N, K, kernel, rows, dtype):
+    """Of equal signs.  An accumulator of 512 rows takes 32 steps of 16 products, each of which
+    may drop 2^-22 of the sum so far (linear_reference.py; sixteen products and the sum, cut off
+    two bits below fp32's last: 17 2^-26): in an evenly growing sum (1 + ... + 32) / 32 2^-22 =
+    4e-6 of the whole.  Accumulations join rounded to nearest, 2^-24 of the sum so far each,
+    M/512 of them and of 8 CTAs: (M / 1024 + 8) 2^-24 of the whole at most."""
+    plan = L.linear_plan("dw", M, N, K, F32)
+    assert plan["kernel"] == kernel and plan["tile_rows"] == (rows or plan["tile_rows"])
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def positive(cols):
+        t = Q.empty_rows(M, cols, dtype)
+        t.copy_(1.0 + torch.rand(M, cols, generator=g, device="cuda"))
+        return t
+    dz, x, dw = positive(N), positive(K), Q.empty_rows(N, K, F32)
+    L.linear_dw(dz, x, dw, checked=True)
+    ref = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    for at in range(0, M, 1 << 16):
+        ref += dz[at:at + (1 << 16)].double().t() @ x[at:at + (1 << 16)].double()
+    off = (dw.double() - ref) / ref
+    assert off.abs().max() <= 4e-6 + (M / 1024 + 8) * 2.0 ** -24
+
+
 @pytest.mark.parametrize("M", [11863232, 11863233, 100000000, 2 ** 31 - 4097])
 @pytest.mark.parametrize("out", [F32, BF16])
 def test_any_number_of_rows_has_a_plan(M, out):
@@ -127,6 +155,25 @@ def late(rows, cols, step, limit_ms=50, steps=5, batch=()):
 def test_products_of_orthogonalize_say_that_they_ran_out(rows, cols, batch, step):
     """Withheld: a stage of every product."""
     assert late(rows, cols, step, batch=batch)[0] == G.GEMM_ERR_TIMEOUT
+
+
+@pytest.mark.parametrize("M,N,K,rows", [(262144, 128, 128, 64), (8053, 296, 3016, 128), (32768, 1024, 1024, 256)])
+@pytest.mark.parametrize("step", [0, 7, 8, 20])
+def test_long_fp32_sums_say_that_they_ran_out(M, N, K, rows, step):
+    """A stage withheld in the first, at an end, and in a later accumulation."""
+    assert L.linear_plan("dw", M, N, K, F32)["tile_rows"] == rows
+    dz, x = zeros_and_ones(1, M, N, F16), zeros_and_ones(2, M, K, F16)
+    dw = torch.empty(N, K, device="cuda")
+    try:
+        G.debug_set(wait_limit_ns=50_000_000, withhold_arrive=step)
+        began = time.perf_counter()
+        with pytest.raises(G.GemmError) as e:
+            L.linear_dw(dz, x, dw, checked=True)
+        assert e.value.status == G.GEMM_ERR_TIMEOUT and time.perf_counter() - began < 0.5
+    finally:
+        G.debug_set()
+    L.linear_dw(dz, x, dw, checked=True)
+    assert torch.equal(dw, dz.float().t() @ x.float())      # whole numbers below 2^24
 
 
 @pytest.mark.parametrize("rows,cols,batch", [(104, 304, ()), (304, 64, (3,)), (120, 2048, ()), (2560, 128, ()),
