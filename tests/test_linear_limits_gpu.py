@@ -118,6 +118,60 @@ def test_linear_dw_sums_512_rows_at_most_in_an_accumulator(M, N, K, kernel, rows
     assert off.abs().max() <= 4e-6 + (M / 1024 + 8) * 2.0 ** -24
 
 
+# M, N, K, tile rows, CTAs of a cut: more than 512 rows a CTA, uncut, cut and cut unevenly
+LONG = [(633, 1836, 33, 64, 1), (1639, 2600, 37, 64, 3), (4660, 35, 36, 64, 8), (674, 4946, 152, 128, 1),
+        (1845, 68, 5159, 128, 3), (4614, 67, 1162, 128, 8), (658, 4009, 1040, 256, 1), (2191, 195, 5131, 256, 3),
+        (8067, 134, 1565, 256, 8)]
+
+
+def rand(seed, rows, cols, dtype):
+    t = Q.empty_rows(rows, cols, dtype)
+    t.copy_(torch.randn(rows, cols, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda"))
+    return t
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M,N,K,rows,cut", LONG)
+def test_long_fp32_sums_on_every_instance(M, N, K, rows, cut, dtype):
+    plan = L.linear_plan("dw", M, N, K, F32)
+    assert (plan["kernel"], plan["tile_rows"], plan["split"]) == ("few", rows, cut) and -(-M // 64) > 8 * cut
+    dz, x, c = rand(1, M, N, dtype), rand(2, M, K, dtype), rand(3, N, K, F32)
+    s = dz.double().t() @ x.double()
+    err = R.sum_rel(M, 512) * (dz.double().abs().t() @ x.double().abs())
+    wide = torch.full((N, (K + 3) // 4 * 4 + 8), 7.0, device="cuda")
+    dw = wide[:, :K]
+    L.linear_dw(dz, x, dw, checked=True)
+    assert ((dw.double() - s).abs() <= err + 2.0 ** -23 * s.abs()).all() and (wide[:, K:] == 7.0).all()
+    sums = dw.clone()
+    L.linear_dw(dz, x, dw)
+    assert torch.equal(dw, sums)
+    dw.copy_(c)
+    L.linear_dw(dz, x, dw, addend=dw, checked=True)      # accumulated in place
+    assert torch.equal(dw, c + sums) and (wide[:, K:] == 7.0).all()
+
+
+def test_long_fp32_sums_in_two_graphs_at_once():
+    sets = []
+    for i, (M, N, K) in enumerate([(40000, 72, 304), (32768, 1024, 1024)]):
+        dz, x, dw = rand(10 + i, M, N, F16), rand(20 + i, M, K, F16), Q.empty_rows(N, K, F32)
+        L.linear_dw(dz, x, dw)
+        torch.cuda.synchronize()
+        expect, graph = dw.clone(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                L.linear_dw(dz, x, dw)
+        dw.zero_()
+        sets.append((graph, torch.cuda.Stream(), dw, expect, (dz, x)))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, *_ in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, dw, expect, _ in sets:
+        assert torch.equal(dw, expect)
+
+
 @pytest.mark.parametrize("M", [11863232, 11863233, 100000000, 2 ** 31 - 4097])
 @pytest.mark.parametrize("out", [F32, BF16])
 def test_any_number_of_rows_has_a_plan(M, out):
