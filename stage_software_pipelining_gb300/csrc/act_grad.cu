@@ -199,7 +199,7 @@ template <bool BF16, int VEC, int GROUPS, int THREADS>
 int launch(const ActGradLaunch& L, cudaStream_t stream) {
     constexpr int COLS = VEC * GROUPS;
     // Sixteen CTAs a cluster, two an SM, where all strips' clusters run at once: as
-    // many as clusters of eight, one an SM (28491 x 210: 20 us, of eight CTAs 33).
+    // many as clusters of eight, one an SM (28491 x 210, gelu: 21.4 us, of eight CTAs 34.5).
     int widest = 8;
     if constexpr (COLS == 32) {
         static bool done[64] = {};

@@ -16,7 +16,7 @@
 // rounded where orthogonalize.cu rounds them, at the same scales.
 //
 // Bound by latencies, some 1.2 us a product and 4 us a step for the cluster's
-// exchange: 128 x 128 takes 24 us (as products 57), 128 x 1024 48 (64).
+// exchange: in a graph 128 x 128 takes 22.5 us (as products 54), 128 x 1024 46 (60).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -469,8 +469,8 @@ int ortho_small_launch(const OrthoLaunch& L, cudaStream_t stream) {
     p.withhold = d.withhold_arrive;
     // The slice's width with the least time: rounds of clusters that run at once, each
     // the steps' latency, the slice's work and, in a cluster, the exchange.  (us;
-    // measured: 128 x 128 in one CTA 24, 128 x 1024 in eight of 128 columns 48, in four
-    // of 256 55, 100 x 300 in one of 320 41, in three of 128 45.)
+    // measured: 128 x 128 in one CTA 22.6, 128 x 1024 in eight of 128 columns 46, in four
+    // of 256 53, 100 x 304 in one of 320 34, in three of 128 42.)
     int resident[9];
     if (!product_resident_ctas(resident)) return GEMM_ERR_CUDA;
     double least = 1e30;

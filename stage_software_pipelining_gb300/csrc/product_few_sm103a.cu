@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(32 * kWarps<MT, SUMS>, MT <= kTwo ? 2 : 1)
     constexpr bool PUSH = MT <= kPush;
     // When the next launch's CTAs may start: once the products are done, so that they
     // spread over the SMs as these leave, or, where a call is little but its start,
-    // as soon as the launch before has ended (1 x 4096 x 4096: 7.9 us so, 8.5 late; six
-    // 2048 x 512 orthogonalised: 167 us late, 172 so).
+    // as soon as the launch before has ended (in graphs, 1 x 4096 x 4096: 8.05 us so, 8.2
+    // late; six 2048 x 512 orthogonalised: 165 us late, 169 so).
     constexpr bool LATE = MT > 16;
     float* part = reinterpret_cast<float*>(smem);  // [MT][128]
     const uint32_t recv = smem_addr(ctl + 1);
