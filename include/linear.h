@@ -136,7 +136,8 @@ int linear_dx(int64_t M, int64_t N, int64_t K, const void* dz, int64_t lddz, con
  *   addend    N x K of out_dtype, ldc >= K, or NULL; may be dW itself (same
  *             leading dimension)
  * With an fp32 dW, no accumulator of the tensor cores, which truncate as they add, sums
- * more than 512 rows: a dW of any number of rows is about as good as by fp32 sums.  (A
+ * more than 512 rows (in large ones two of a sum 1024): a dW of any number of rows is
+ * about as good as by fp32 sums.  (A
  * 16-bit dW is summed by one accumulator, which loses up to 6e-9 of the sum of
  * magnitudes a row: half an fp16 step at 80000 rows of equal signs.)
  * M = 0 gives the addend (or 0).

@@ -67,11 +67,11 @@ bool product_resident_ctas(int (&out)[9]);
 int product_few_status(GemmDeviceStatus* out);
 int product_pair_status(GemmDeviceStatus* out);
 
-// fp32 outputs: K blocks of 64 that one accumulator sums at most, 512 rows.  The tensor
-// cores truncate as they add, and accumulations join in registers, rounded to nearest:
-// 32768 rows of fp16 come out 6.5e-7 of the norm off, as by fp32 sums (5.7e-7); with 1024
-// rows an accumulator 1.3e-6, with 4096 4.9e-6.  (32768 x 1024^2 58.0 us for 57.4 with
-// 1024 and 56.3 with 4096.)
+// fp32 outputs: K blocks of 64 that one accumulator sums, 512 rows (a pair tile's first two
+// accumulations may have twice as many).  The tensor cores truncate as they add, and
+// accumulations join in registers, rounded to nearest: 32768 rows of fp16 come out 6.5e-7
+// of the norm off, as by fp32 sums (5.7e-7); with 1024 rows an accumulator 1.3e-6, with
+// 4096 4.9e-6.  (32768 x 1024^2 58.0 us for 57.4 with 1024 and 56.3 with 4096.)
 constexpr int kProductChunk = 8;
 
 struct ActGradLaunch {

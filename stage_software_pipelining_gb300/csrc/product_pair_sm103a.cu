@@ -67,7 +67,7 @@ struct PairParams {
     int bn;        // tile width
     int tiles_m, tiles_n, tiles, k_blocks, batch;
     int k_chunks;  // accumulations of a tile, summed by the epilogue (EPI_F32)
-    int chunk_blocks, chunk_rest;  // K blocks over accumulations: quotient and remainder
+    int long_chunks;  // the first of them, of 2 kProductChunk blocks each; the others have kProductChunk
     int group_m;   // tile rows walked together
     Divisor by_tiles, by_group;            // tiles; those of a group
     Divisor by_rows, by_last_rows;         // a group's tile rows; the last group's
@@ -592,25 +592,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return __all_sync(0xffffffffu, r) != 0;
                 };
                 for (int t = unit; ok && t < tiles; t += units) {
-                    int kb = 0, over_c = 0;  // K blocks c / chunks, rounded down, and what is over
+                    int kb = 0;
                     for (int c = 0; ok && c < chunks; ++c, ++lt) {
-                        const int acc = lt & 1;
+                        const int acc = lt & 1, kb0 = kb;
+                        const int kb1 = EPI == EPI_F32 ? min(p.k_blocks, kb + (c < p.long_chunks ? 2 : 1) * kProductChunk)
+                                                       : p.k_blocks;
                         if (!mma_wait(tempty_bar(acc), static_cast<uint32_t>((lt >> 1) & 1) ^ 1u)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-                        const int kb0 = kb;
-                        int kb1 = p.k_blocks;
-                        if constexpr (EPI == EPI_F32) {
-                            kb1 = kb0 + p.chunk_blocks;
-                            over_c += p.chunk_rest;
-                            if (over_c >= chunks) {
-                                over_c -= chunks;
-                                ++kb1;
-                            }
-                        }
                         for (; kb < kb1; ++kb) {
                             if (!mma_wait(full_bar(s), ph)) {
                                 ok = false;
@@ -705,9 +697,15 @@ int launch(const ProductLaunch& L, int bn, int slot, cudaStream_t stream) {
     p.tiles = static_cast<int>(tiles);
     p.batch = static_cast<int>(L.batch);
     p.k_blocks = static_cast<int>((L.K + PK - 1) / PK);
-    p.k_chunks = EPI == EPI_F32 ? (p.k_blocks + kProductChunk - 1) / kProductChunk : 1;
-    p.chunk_blocks = p.k_blocks / p.k_chunks;
-    p.chunk_rest = p.k_blocks % p.k_chunks;
+    // Accumulations of 512 rows; two of 1024 first where a sum is long enough for them to
+    // cost it little precision (of 8192 rows 8e-7 of the norm for 6.5e-7), so that the
+    // products run on under the last tile's epilogue (8192 x 4096 results of 8192 rows,
+    // added in place: 302 us, with 512 all along 311).
+    p.k_chunks = 1;
+    if (EPI == EPI_F32) {
+        p.long_chunks = p.k_blocks >= 12 * kProductChunk ? 2 : 0;
+        p.k_chunks = p.long_chunks + (p.k_blocks - p.long_chunks * 2 * kProductChunk + kProductChunk - 1) / kProductChunk;
+    }
     // Tile rows walked together: about 32 MB of A, so that the panel stays in
     // L2 while the group walks its columns.
     const int64_t g = (32ll << 20) / (512 * L.K);

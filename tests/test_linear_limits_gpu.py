@@ -93,14 +93,16 @@ def test_linear_dw_of_many_rows(M, N, K, dtype):
 @pytest.mark.parametrize("M,N,K,kernel,rows", [(17000, 40, 24, "few", 64), (40000, 300, 72, "few", None),
                                                (9000, 1400, 300, "few", None), (600, 40, 40, "few", 64), (32768, 1024, 1024, "few", 256),
                                                (262144, 128, 128, "few", 64), (300000, 128, 128, "few", 64),
-                                               (8192, 2304, 2048, "pair", 256)])
+                                               (8192, 2304, 2048, "pair", 256), (5000, 2304, 2048, "pair", 256)])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_linear_dw_sums_512_rows_at_most_in_an_accumulator(M, N, K, kernel, rows, dtype):
+def test_linear_dw_sums_512_rows_in_an_accumulator(M, N, K, kernel, rows, dtype):
     """Of equal signs.  An accumulator of 512 rows takes 32 steps of 16 products, each of which
     may drop 2^-22 of the sum so far (linear_reference.py; sixteen products and the sum, cut off
     two bits below fp32's last: 17 2^-26): in an evenly growing sum (1 + ... + 32) / 32 2^-22 =
     4e-6 of the whole.  Accumulations join rounded to nearest, 2^-24 of the sum so far each,
-    M/512 of them and of 8 CTAs: (M / 1024 + 8) 2^-24 of the whole at most."""
+    M/512 of them and of 8 CTAs: (M / 1024 + 8) 2^-24 of the whole at most.  Two accumulations of
+    1024 rows, of 6144 or more on the pair kernel, drop (1 + ... + 64) / 64 2^-22 = 7.8e-6 of
+    their share of M."""
     plan = L.linear_plan("dw", M, N, K, F32)
     assert plan["kernel"] == kernel and plan["tile_rows"] == (rows or plan["tile_rows"])
     g = torch.Generator(device="cuda").manual_seed(9)
@@ -115,7 +117,8 @@ def test_linear_dw_sums_512_rows_at_most_in_an_accumulator(M, N, K, kernel, rows
     for at in range(0, M, 1 << 16):
         ref += dz[at:at + (1 << 16)].double().t() @ x[at:at + (1 << 16)].double()
     off = (dw.double() - ref) / ref
-    assert off.abs().max() <= 4e-6 + (M / 1024 + 8) * 2.0 ** -24
+    longer = 2048 / M if kernel == "pair" and M >= 6144 else 0.0
+    assert off.abs().max() <= 4e-6 * (1 - longer) + 7.8e-6 * longer + (M / 1024 + 8) * 2.0 ** -24
 
 
 # M, N, K, tile rows, CTAs of a cut: more than 512 rows a CTA, uncut, cut and cut unevenly
